@@ -1,4 +1,4 @@
-"""ctypes binding of liblora.so: the same names as include/lora.h, argument
+"""ctypes binding of liblora.so: the same names as include/*.h, argument
 marshalling only.  Every step of the path runs in the library's CUDA kernels;
 there is no Python or CPU fallback: if the library is missing, loading fails.
 """
@@ -14,12 +14,17 @@ SO = os.path.join(_PKG, "liblora.so")
  LORA_ENOSPACE) = range(8)
 LORA_UNIT_ABSENT, LORA_UNIT_LOADING, LORA_UNIT_READY = range(3)
 DERR = {0x1: "adapter", 0x2: "rank", 0x4: "page-table block", 0x8: "page", 0x10: "segment",
-        0x20: "timeout"}
+        0x20: "timeout", 0x40: "KV cache arrays"}
 LORA_MAX_PROBLEMS_PER_LAUNCH = 256
 LORA_MAX_SEGMENTS = 16384
 LORA_MAX_RANK = 256
 LORA_NOALLOC_MAX_TOKENS = 4096
 LORA_STAGE_MAX_RUNS = 64
+LORA_KV_MAX_HEADS = 256
+LORA_KV_MAX_SEQS = 16384
+LORA_ROPE_HALVES, LORA_ROPE_PAIRS = range(2)
+LORA_W4_MAX_ROWS = 256
+LORA_W4_MAX_PROBLEMS = 16
 
 EXPORTED = ["lora_pool_create", "lora_pool_destroy", "lora_pool_set_tuning", "lora_pool_get_tuning",
             "lora_workspace_size", "lora_workspace_init",
@@ -31,7 +36,10 @@ EXPORTED = ["lora_pool_create", "lora_pool_destroy", "lora_pool_set_tuning", "lo
             # host runtime (include/lora_runtime.h)
             "lora_cache_create", "lora_cache_destroy", "lora_cache_acquire", "lora_cache_loaded",
             "lora_cache_release", "lora_cache_query", "lora_cache_stats", "lora_sched_create",
-            "lora_sched_destroy", "lora_sched_enqueue", "lora_sched_pick", "lora_sched_pending"]
+            "lora_sched_destroy", "lora_sched_enqueue", "lora_sched_pick", "lora_sched_pending",
+            # the 4-bit KV cache (include/lora_kv.h) and 4-bit weights (include/lora_w4.h)
+            "lora_kv_block_bytes", "lora_kv_workspace_size", "lora_kv_workspace_init", "lora_kv_append",
+            "lora_kv_read", "lora_kv_attend", "lora_w4_workspace_size", "lora_w4_matvec"]
 
 
 class lora_pool_desc(ctypes.Structure):
@@ -64,6 +72,31 @@ class lora_ws_view(ctypes.Structure):
     _fields_ = [("error_word", ctypes.c_void_p), ("counts", ctypes.c_void_p),
                 ("perm", ctypes.c_void_p), ("grp_start", ctypes.c_void_p),
                 ("grp_adapter", ctypes.c_void_p)]
+
+
+class lora_kv_cache_desc(ctypes.Structure):
+    _fields_ = [("blocks", ctypes.c_void_p), ("num_blocks", ctypes.c_int64), ("block_stride", ctypes.c_int64),
+                ("block_tokens", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class lora_kv_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("n_seq", ctypes.c_int32), ("T", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
+                ("max_q", ctypes.c_int32)]
+
+
+class lora_rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class lora_w4_problem(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
+                ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class LoraError(RuntimeError):
@@ -123,6 +156,14 @@ def lib():
             "lora_sched_pick": [p, i32, i32, p, p, p, i32, ctypes.POINTER(i32), ctypes.POINTER(i32),
                                 ctypes.POINTER(i32)],
             "lora_sched_pending": [p, ctypes.POINTER(i64)],
+            "lora_kv_block_bytes": [i32, i32, i32, i32, ctypes.POINTER(sz)],
+            "lora_kv_workspace_size": [p, p, i32, ctypes.POINTER(sz)],
+            "lora_kv_workspace_init": [p, sz, p],
+            "lora_kv_append": [p, p, p, i64, p, i64, i32, p, i64, p, i64, p, p, sz, p],
+            "lora_kv_read": [p, p, p, i64, p, i64, p, sz, p],
+            "lora_kv_attend": [p, p, p, i64, i32, ctypes.c_float, p, i64, p, p, sz, p],
+            "lora_w4_workspace_size": [p, i32, i32, ctypes.POINTER(sz)],
+            "lora_w4_matvec": [p, i32, i32, p, sz, p],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -322,6 +363,108 @@ def get_device_error(ws, stream) -> int:
     if st not in (LORA_OK, LORA_EDEVICE):
         raise LoraError(st, "lora_get_device_error")
     return bits.value
+
+
+# ----------------------------------------------------------------------------- 4-bit KV cache
+
+class _Desc:
+    """A description passed by pointer on every call; keeps the tensors it names alive."""
+
+    def __init__(self, struct, *owners):
+        self.struct, self._owners = struct, owners
+        self.ref = ctypes.addressof(struct)
+
+
+class KvCache(_Desc):
+    """One layer's 4-bit paged cache (lora_kv_cache_desc): block b starts block_stride * b
+    bytes after `blocks`."""
+
+    def __init__(self, blocks, num_blocks, block_stride, block_tokens, num_kv_heads, head_dim, group):
+        super().__init__(lora_kv_cache_desc(_ptr(blocks), num_blocks, block_stride, block_tokens, num_kv_heads,
+                                            head_dim, group), blocks)
+
+
+class KvBatch(_Desc):
+    """A batch of requests over a cache (lora_kv_batch): device arrays q_start [n_seq + 1],
+    kv_len [n_seq], block_table [n_seq][max_blocks]; T rows, at most max_q of one request."""
+
+    def __init__(self, q_start, kv_len, block_table, n_seq, T, max_blocks, max_q):
+        super().__init__(lora_kv_batch(_ptr(q_start), _ptr(kv_len), _ptr(block_table), n_seq, T, max_blocks, max_q),
+                         q_start, kv_len, block_table)
+
+
+class Rope(_Desc):
+    """Rotation tables (lora_rope): cos, sin f32 [max_pos][rot_dim / 2], style LORA_ROPE_*;
+    positions int32 [T], or None: each row's cache token."""
+
+    def __init__(self, cos, sin, max_pos, rot_dim, style=LORA_ROPE_HALVES, positions=None):
+        super().__init__(lora_rope(_ptr(cos), _ptr(sin), _ptr(positions), max_pos, rot_dim, style, 0),
+                         cos, sin, positions)
+
+
+def kv_block_bytes(block_tokens, num_kv_heads, head_dim, group) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().lora_kv_block_bytes(block_tokens, num_kv_heads, head_dim, group, ctypes.byref(n)),
+           "lora_kv_block_bytes")
+    return n.value
+
+
+def kv_workspace_size(cache: KvCache, batch: KvBatch, num_q_heads: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().lora_kv_workspace_size(cache.ref, batch.ref, num_q_heads, ctypes.byref(n)),
+           "lora_kv_workspace_size")
+    return n.value
+
+
+def kv_workspace_init(ws, ws_bytes: int, stream: int):
+    _check(lib().lora_kv_workspace_init(_ptr(ws), ws_bytes, stream), "lora_kv_workspace_init")
+
+
+def kv_append(cache, batch, q, ldq, q_out, ldqo, num_q_heads, k, ldk, v, ldv, rope, ws, ws_bytes, stream):
+    """q_out = q turned by its positions; k (turned) and v stored in the cache."""
+    _check(lib().lora_kv_append(cache.ref, batch.ref, _ptr(q), ldq, _ptr(q_out), ldqo, num_q_heads, _ptr(k), ldk,
+                                _ptr(v), ldv, rope.ref, _ptr(ws), ws_bytes, stream), "lora_kv_append")
+
+
+def kv_read(cache, batch, k_out, ldk, v_out, ldv, ws, ws_bytes, stream):
+    """The batch's rows as the cache holds them, bf16."""
+    _check(lib().lora_kv_read(cache.ref, batch.ref, _ptr(k_out), ldk, _ptr(v_out), ldv, _ptr(ws), ws_bytes,
+                              stream), "lora_kv_read")
+
+
+def kv_attend(cache, batch, q, ldq, num_q_heads, softmax_scale, out, ldo, lse, ws, ws_bytes, stream):
+    """Causal attention of the batch's rows over the cache; lse: f32 [T][num_q_heads] or None."""
+    _check(lib().lora_kv_attend(cache.ref, batch.ref, _ptr(q), ldq, num_q_heads, softmax_scale, _ptr(out), ldo,
+                                _ptr(lse), _ptr(ws), ws_bytes, stream), "lora_kv_attend")
+
+
+# ----------------------------------------------------------------------------- 4-bit weights
+
+def w4_problems(problems):
+    """The projections of a call, kept by the caller for as long as the tensors stay where
+    they are: (x, y, ldx, ldy, codes, scales, zeros or None, N, K, group) each."""
+    problems = list(problems)
+    arr = (lora_w4_problem * max(1, len(problems)))()
+    for i, (x, y, ldx, ldy, codes, scales, zeros, n, k, group) in enumerate(problems):
+        arr[i] = lora_w4_problem(_ptr(x), _ptr(y), ldx, ldy, _ptr(codes), _ptr(scales), _ptr(zeros), n, k, group, 0)
+    return _W4Problems(arr, problems)
+
+
+class _W4Problems(_Desc):
+    def __init__(self, arr, problems):
+        super().__init__(arr, problems)
+        self.n = len(problems)
+
+
+def w4_workspace_size(problems, T: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().lora_w4_workspace_size(problems.ref, problems.n, T, ctypes.byref(n)), "lora_w4_workspace_size")
+    return n.value
+
+
+def w4_matvec(problems, T, ws, ws_bytes, stream):
+    """y = x W^T for every projection of w4_problems(...)."""
+    _check(lib().lora_w4_matvec(problems.ref, problems.n, T, _ptr(ws), ws_bytes, stream), "lora_w4_matvec")
 
 
 # ----------------------------------------------------------------------------- host runtime
