@@ -35,7 +35,13 @@ lora_status check_sizes(const lora_kv_cache_desc* c, const lora_kv_batch* b) {
     return LORA_OK;
 }
 
-size_t workspace_bytes() { return sizeof(WsHeader); }
+// Packed rows a KV head has per request at most, and the row tiles (of 8) a CTA of the
+// attention takes at a time.
+int attend_nt(const lora_kv_cache_desc* c, const lora_kv_batch* b, int32_t q_heads) {
+    return (int64_t)b->max_q * (q_heads / c->num_kv_heads) <= 8 ? 1 : 2;
+}
+
+size_t workspace_bytes() { return align256(sizeof(WsHeader) + attend_workspace(2, 128)); }
 
 lora_status check_call(const lora_kv_cache_desc* c, const lora_kv_batch* b, const void* ws, size_t ws_bytes, size_t need) {
     lora_status st = check_sizes(c, b);
@@ -103,10 +109,33 @@ template <int D, int G>
 struct Read {
     static void run(const ReadParams& p, dim3 grid, cudaStream_t s) { kv_read_kernel<D, G><<<grid, kAppendWarps * 32, 0, s>>>(p); }
 };
-template <int D, int G>
-struct Attend {
-    static void run(const AttendParams& p, dim3 grid, cudaStream_t s) { kv_attend_kernel<D, G><<<grid, kAttendThreads, 0, s>>>(p); }
-};
+template <int D, int G, int NT>
+lora_status attend(const AttendParams& p, cudaStream_t s) {
+    DeviceInfo* di = nullptr;
+    lora_status st = device_info(&di);
+    if (st != LORA_OK) return st;
+    constexpr size_t smem = attend_smem(D, G);
+    auto kern = kv_attend_kernel<D, G, NT>;
+    static thread_local int ready_dev = -1, per_sm = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (ready_dev != dev) {
+        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        if (st != LORA_OK) return st;
+        st = cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAttThreads, smem));
+        if (st != LORA_OK) return st;
+        ready_dev = dev;
+    }
+    const int grid = std::min(di->sm_count * std::max(per_sm, 1), kAttMaxCtas);
+    kern<<<grid, kAttThreads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int NT>
+lora_status attend_by_shape(const lora_kv_cache_desc* c, const AttendParams& p, cudaStream_t s) {
+    if (c->head_dim == 128) return c->group == 32 ? attend<128, 32, NT>(p, s) : attend<128, 128, NT>(p, s);
+    return c->group == 32 ? attend<64, 32, NT>(p, s) : attend<64, 64, NT>(p, s);
+}
 
 }  // namespace
 
@@ -127,6 +156,7 @@ lora_status lora_kv_workspace_size(const lora_kv_cache_desc* cache, const lora_k
     lora_status st = check_sizes(cache, batch);
     if (st != LORA_OK) return st;
     if (num_q_heads < 0 || num_q_heads % cache->num_kv_heads != 0) return LORA_EINVAL;
+    if (num_q_heads > 65536) return LORA_ETOOBIG;
     *bytes = workspace_bytes();
     return LORA_OK;
 }
@@ -211,11 +241,12 @@ lora_status lora_kv_read(const lora_kv_cache_desc* cache, const lora_kv_batch* b
 lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch* batch, const void* q, int64_t ldq,
                            int32_t num_q_heads, float softmax_scale, void* out, int64_t ldo, float* lse, void* ws,
                            size_t ws_bytes, void* stream) {
-    lora_status st = check_call(cache, batch, ws, ws_bytes, workspace_bytes());
+    lora_status st = check_sizes(cache, batch);
     if (st != LORA_OK) return st;
     if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 || !(softmax_scale > 0.f && softmax_scale <= 3.4e38f))
         return LORA_EINVAL;
-    if (num_q_heads > 65535) return LORA_ETOOBIG;
+    if (num_q_heads > 65536) return LORA_ETOOBIG;
+    if ((st = check_call(cache, batch, ws, ws_bytes, workspace_bytes())) != LORA_OK) return st;
     if (batch->T == 0 || batch->n_seq == 0) return LORA_OK;
     const int64_t cols = (int64_t)num_q_heads * cache->head_dim;
     if ((st = check_rows(q, ldq, cols)) != LORA_OK) return st;
@@ -228,8 +259,12 @@ lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch*
     p.ldq = ldq;
     p.ldo = ldo;
     p.q_heads = num_q_heads;
+    p.rep = num_q_heads / cache->num_kv_heads;
     p.scale = softmax_scale;
-    return by_shape<Attend>(cache, p, dim3((unsigned)batch->T, (unsigned)num_q_heads), (cudaStream_t)stream);
+    p.tickets = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + sizeof(WsHeader));
+    p.part = reinterpret_cast<float*>(p.tickets + kAttMaxCtas);
+    if (attend_nt(cache, batch, num_q_heads) == 1) return attend_by_shape<1>(cache, p, (cudaStream_t)stream);
+    return attend_by_shape<2>(cache, p, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,56 @@
+// Warp-level matrix pieces of the 4-bit kernels: ldmatrix, mma.sync on bf16, and the step
+// from packed 4-bit codes to bf16 operands.
+#pragma once
+#include <stdint.h>
+
+namespace lora {
+
+// Four 8 x 8 matrices of 16-bit elements; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements held one register a lane.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// c += a b, a 16 x 16 (row), b 16 x 8 (column), bf16 with fp32 sums.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Nibbles I and I + 4 of a word of eight codes, as the bf16 pair (code - bias): 0x4300 is
+// 128.0 in bf16, whose last seven bits count in ones, so 0x4300 | c = 128 + c, and
+// `minus` = (128 + bias) twice is taken off exactly.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t minus) {
+    uint32_t t, r;
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(t) : "r"(I ? w >> (4 * I) : w));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(minus));
+    return r;
+}
+constexpr uint32_t kMinus8 = 0x43084308u;   // 136.0 twice: codes as -8 .. 7
+
+// 2^x to about 2 ulp; 2^-inf = 0.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+}  // namespace lora

@@ -10,7 +10,7 @@
  * Format.  For each token, KV head and K or V, every `group` neighbouring values share a
  * scale and an offset (f16); a 4-bit code c in 0..15 stands for
  *
- *     value = scale * (c - 8) + offset.
+ *     value = scale * (c - 8) + offset,    scale >= 0.
  *
  * A block holds block_tokens tokens of every KV head of one layer as tiles of 16 tokens of
  * one head, [num_kv_heads][block_tokens / 16] tiles, each
@@ -124,8 +124,8 @@ lora_status lora_kv_read(const lora_kv_cache_desc* cache, const lora_kv_batch* b
  *     a_t = softmax_scale * (q . k_t),   out = sum_t exp(a_t - lse) v_t,   lse = log sum_t exp(a_t).
  *   q, out  bf16 [T][ldq], [T][ldo]; lse: f32 [T][num_q_heads], or NULL
  * A row with no token (kv_len smaller than the request's rows) gets zeros and lse = -inf.
- * Scores, softmax statistics and sums are fp32; a probability is rounded to bf16 once,
- * before its product with the V codes.  The result does not depend on how the device
+ * Scores, softmax statistics and sums are fp32; a probability (times the V scale) is
+ * rounded to bf16 once, before its product with the V codes.  The result does not depend on how the device
  * schedules the work.  num_q_heads is a multiple of num_kv_heads. */
 lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch* batch, const void* q, int64_t ldq,
                            int32_t num_q_heads, float softmax_scale, void* out, int64_t ldo, float* lse, void* ws,
