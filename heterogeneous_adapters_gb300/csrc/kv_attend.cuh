@@ -15,12 +15,14 @@
 // products, 8 rows fill an MMA; mma.sync serves because the kernel is bound by the bytes of
 // the cache (136 a token and head) and next by the unpacking, not by the MMAs.
 //
-// Work.  An item is (request, KV head, tile of 8 NT packed rows), of ceil(tokens / 32) steps.
-// The steps of all items in a row are dealt to the CTAs in equal contiguous ranges; a CTA's
-// four warps take the steps of its part of an item in turn, each with its own bulk-copy ring
-// and running maximum and sum, and merge at the part's end.  An item that spans several CTAs
-// is put together from partial results in the workspace by the CTA that arrives last, in
-// the order of the parts, so the result does not depend on the order of arrival.
+// Work.  An item is (request, KV head, tile of 8 NT packed rows), of ceil(tokens / 32) steps
+// and kAttItemCost more for its fixed part.  The units of all items in a row are dealt to
+// the CTAs in equal contiguous ranges.  A short item that lies in one range is a warp's own
+// (the CTA's warps take such items in turn, without meeting); of any other item the CTA's
+// four warps take the steps in turn, each with its own bulk-copy ring and running maximum
+// and sum, and merge at the end of the CTA's part.  An item that spans several CTAs is put
+// together from partial results in the workspace by the CTA that arrives last, in the order
+// of the parts, so the result does not depend on the order of arrival.
 #pragma once
 #include "kv_layout.cuh"
 #include "mma_legacy.cuh"
@@ -33,8 +35,11 @@ constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kAttStep = 32;          // tokens of a step (two tiles)
 constexpr int kAttStages = 3;
 constexpr int kAttMaxCtas = 1024;
+constexpr int kAttJoin = 8;           // parts of an item whose loads are in flight together
 constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40: stands for a scale of 0, below f16's smallest
-constexpr int kAttMinSteps = kAttWarps;   // a CTA's range is at least a step per warp
+constexpr int kAttItemCost = 3;       // units of an item beside its steps
+constexpr int kAttMinUnits = 8;       // a CTA's range is at least this
+constexpr int kAttSolo = 8;           // an item of at most this many steps is one warp's
 
 struct AttendParams {
     KvView v;
@@ -45,14 +50,14 @@ struct AttendParams {
     int32_t q_heads, rep;
     float scale;
     uint32_t* tickets;      // [kAttMaxCtas], zero between calls
-    float* part;            // [kAttMaxCtas][2][8 NT][D + 2]
+    float* part;            // [kAttMaxCtas][2][8 NT][D + 4]
 };
 
 __host__ __device__ constexpr size_t attend_smem(int dim, int group) {
     return (size_t)kAttWarps * kAttStages * 2 * kv_tile_bytes(dim, group);
 }
 // Workspace after the header: tickets and partial results.
-__host__ __device__ constexpr size_t attend_part_floats(int nt, int dim) { return (size_t)2 * 8 * nt * (dim + 2); }
+__host__ __device__ constexpr size_t attend_part_floats(int nt, int dim) { return (size_t)2 * 8 * nt * (dim + 4); }
 __host__ __device__ constexpr size_t attend_workspace(int nt, int dim) {
     return kAttMaxCtas * 4 + kAttMaxCtas * attend_part_floats(nt, dim) * 4;
 }
@@ -85,17 +90,26 @@ __device__ __forceinline__ int att_steps(const KvView& v, const AttSeq& q, int r
     return tokens <= 0 ? 1 : (int)((tokens + kAttStep - 1) / kAttStep);
 }
 
-// Steps of one KV head of a request.
-__device__ __forceinline__ int64_t att_head_steps(const KvView& v, const AttSeq& q, int rep, int width) {
+// Units of one KV head of a request.
+__device__ __forceinline__ int64_t att_head_units(const KvView& v, const AttSeq& q, int rep, int width) {
     int64_t n = 0;
-    for (int r0 = 0; r0 < q.rows * rep; r0 += width) n += att_steps(v, q, rep, r0, width);
+    for (int r0 = 0; r0 < q.rows * rep; r0 += width) n += att_steps(v, q, rep, r0, width) + kAttItemCost;
     return n;
+}
+
+__device__ __forceinline__ void att_store(const AttendParams& p, int row, int hq, int D, int d, float4 x, float sum) {
+    const float f = sum != 0.f ? __fdividef(1.f, sum) : 0.f;     // no token: zeros
+    uint2 w = make_uint2(pack2(x.x * f, x.y * f), pack2(x.z * f, x.w * f));
+    *reinterpret_cast<uint2*>(p.out + row * p.ldo + (int64_t)hq * D + d) = w;
+}
+__device__ __forceinline__ void att_store_lse(const AttendParams& p, int row, int hq, float top, float sum) {
+    if (p.lse) p.lse[(int64_t)row * p.q_heads + hq] = top == -INFINITY ? -INFINITY : top * p.scale + logf(sum);
 }
 
 template <int D, int G, int NT>
 __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kRows = 8 * NT, kChunks = D / 32, kGroups = D / G, kPerG = G / 32;
-    constexpr int kTile = kv_tile_bytes(D, G), kStage = 2 * kTile, kPitch = D + 2;
+    constexpr int kTile = kv_tile_bytes(D, G), kStage = 2 * kTile, kPitch = D + 4;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ __align__(8) uint64_t bars[kAttWarps][kAttStages];
     __shared__ int64_t scan[kAttWarps + 1];
@@ -107,12 +121,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
     if (tid < kAttWarps * kAttStages) mbar_init(smem_addr(&bars[0][0]) + tid * 8, 1);
     fence_mbar_init();
 
-    // ---- the schedule: the steps before each request, by a scan over the requests
+    // ---- the schedule: the units before each request, by a scan over the requests
     const int chunk = (v.n_seq + kAttThreads - 1) / kAttThreads;
     const int s_lo = min(tid * chunk, v.n_seq), s_hi = min(s_lo + chunk, v.n_seq);
     int64_t mine = 0;
     for (int s = s_lo; s < s_hi; ++s)
-        mine += v.heads * att_head_steps(v, att_seq(v, s, blockIdx.x == 0), p.rep, kRows);
+        mine += v.heads * att_head_units(v, att_seq(v, s, blockIdx.x == 0), p.rep, kRows);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -120,7 +134,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
         if (lane >= o) incl += n;
     }
     if (lane == 31) scan[warp + 1] = incl;
-    if (tid == 0) scan[0] = 0;
     __syncthreads();
     int64_t before = incl - mine, total = 0;
 #pragma unroll
@@ -128,51 +141,94 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
         if (w < warp) before += scan[w + 1];
         total += scan[w + 1];
     }
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kAttMinSteps);
+    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kAttMinUnits);
     const int64_t first = per * blockIdx.x, end = min(first + per, total);
     if (first >= end) return;
-    if (before <= first && first < before + mine) {   // this thread's requests hold the first step
+    if (before <= first && first < before + mine) {   // this thread's requests hold the first unit
         int s = s_lo;
+        AttSeq q;
+        int64_t n;
         for (;; ++s) {
-            const int64_t n = v.heads * att_head_steps(v, att_seq(v, s, false), p.rep, kRows);
-            if (first < before + n) break;
-            before += n;
+            q = att_seq(v, s, false);
+            n = att_head_units(v, q, p.rep, kRows);
+            if (first < before + v.heads * n) break;
+            before += v.heads * n;
         }
-        found[0] = s;
-        found[1] = before;
+        int head = 0;
+        while (first >= before + n) {
+            before += n;
+            ++head;
+        }
+        found[0] = (int64_t)s << 32 | head;
+        found[1] = before;                              // units before the head
     }
     __syncthreads();
-    int seq = (int)found[0];
-    int64_t at = found[1];                              // steps before request `seq`
+    int seq = (int)(found[0] >> 32), head = (int)found[0], r0 = 0;
+    int64_t item = found[1];                            // first unit of the item
+    AttSeq q = att_seq(v, seq, false);
     const float sl = p.scale * 1.44269504f;
     const uint32_t wring = smem_addr(ring) + warp * kAttStages * kStage;
     const uint32_t wbar = smem_addr(&bars[warp][0]);
+    const int cap = (int)((int64_t)v.max_blocks * v.block_tokens);
     uint32_t it = 0;                                    // steps this warp has consumed
+    uint32_t solos = 0;
     bool ok = true;
 
-    for (int64_t pos = first; pos < end && ok;) {
-        // ---- the item at `pos`: request, KV head, row tile
-        AttSeq q = att_seq(v, seq, false);
-        int64_t per_head = att_head_steps(v, q, p.rep, kRows);
-        while (pos >= at + v.heads * per_head) {
-            at += v.heads * per_head;
-            q = att_seq(v, ++seq, false);
-            per_head = att_head_steps(v, q, p.rep, kRows);
+    while (item < end) {
+        // ---- the item (seq, head, r0) and this CTA's steps of it
+        const int steps = att_steps(v, q, p.rep, r0, kRows);
+        const int64_t body = item + kAttItemCost;
+        const int cur_seq = seq, cur_head = head, cur_r0 = r0;
+        const AttSeq cq = q;
+        const int st0 = (int)max(first - body, (int64_t)0), st1 = (int)min(max(end - body, (int64_t)0), (int64_t)steps);
+        const int width = min(kRows, cq.rows * p.rep - cur_r0);
+        // the item after it
+        item = body + steps;
+        r0 += kRows;
+        if (r0 >= q.rows * p.rep) {
+            r0 = 0;
+            if (++head == v.heads) {
+                head = 0;
+                do q = att_seq(v, min(++seq, v.n_seq - 1), false);
+                while (seq < v.n_seq && q.rows == 0);
+            }
         }
-        const int head = (int)((pos - at) / per_head);
-        int64_t item = at + head * per_head;            // first step of the item
-        int r0 = 0, steps = att_steps(v, q, p.rep, 0, kRows);
-        while (pos >= item + steps) {
-            item += steps;
-            r0 += kRows;
-            steps = att_steps(v, q, p.rep, r0, kRows);
-        }
-        const int width = min(kRows, q.rows * p.rep - r0);
-        const int st0 = (int)(pos - item), st1 = (int)min((int64_t)steps, end - item);
-        const int lead = q.len - q.rows;                // row i's token is lead + i
-        const int cap = v.max_blocks * v.block_tokens;
-        const int tokens = min(lead + (r0 + width - 1) / p.rep + 1, cap);
-        const int low = lead + r0 / p.rep;              // the first row's token: steps before see no mask
+        if (st1 <= st0) continue;
+        const bool whole = st0 == 0 && st1 == steps;
+        const bool solo = whole && steps <= kAttSolo;
+        if (solo && (int)(solos++ % kAttWarps) != warp) continue;
+        const int way = solo ? 1 : kAttWarps, me = solo ? 0 : warp;
+        const int lead = cq.len - cq.rows;              // row i's token is lead + i
+        const int tokens = min(lead + (cur_r0 + width - 1) / p.rep + 1, cap);
+        const int low = lead + cur_r0 / p.rep;          // the first row's token: steps before see no mask
+
+        // ---- this warp's steps st0 + me + way i.  Lane j looks up the two tiles of the
+        // warp's step i0 + j, for 32 steps at a time.
+        const int mine_n = ok && st1 - st0 > me ? (st1 - st0 - me + way - 1) / way : 0;
+        const unsigned char* tile_a = nullptr;
+        const unsigned char* tile_b = nullptr;
+        uint32_t now_a = 0, now_b = 0;                  // which of the 32 steps' tiles are there
+        auto lookup = [&](int i) {
+            const int tok = (st0 + me + way * (i + lane)) * kAttStep;
+            tile_a = i + lane < mine_n && tok < tokens ? kv_tile_of(v, cur_seq, tok, cur_head, kTile) : nullptr;
+            tile_b = i + lane < mine_n && tok + kKvTile < tokens ? kv_tile_of(v, cur_seq, tok + kKvTile, cur_head, kTile) : nullptr;
+            now_a = __ballot_sync(0xffffffffu, tile_a != nullptr);
+            now_b = __ballot_sync(0xffffffffu, tile_b != nullptr);
+        };
+        uint32_t have_a = 0, have_b = 0;                // tiles of the steps in the ring, bit step % 32
+        auto put = [&](int i, uint32_t stage) {         // copies of step i into `stage`
+            const int j = i & 31;
+            if (j == 0) lookup(i);
+            const uint32_t bit = 1u << j;
+            have_a = (have_a & ~bit) | (now_a & bit);
+            have_b = (have_b & ~bit) | (now_b & bit);
+            if (lane == j) {
+                mbar_arrive_expect_tx(wbar + stage * 8, (tile_a ? kTile : 0) + (tile_b ? kTile : 0));
+                if (tile_a) bulk_g2s(wring + stage * kStage, tile_a, kTile, wbar + stage * 8);
+                if (tile_b) bulk_g2s(wring + stage * kStage + kTile, tile_b, kTile, wbar + stage * 8);
+            }
+        };
+        for (int i = 0; i < min(kAttStages, mine_n); ++i) put(i, (it + i) % kAttStages);
 
         // ---- q as the right-hand operand, and its sums per group
         uint32_t qb[NT][kChunks][4];
@@ -180,10 +236,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
         int32_t last[NT][2];                            // last token of this lane's columns
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = r0 + n * 8 + g;
+            const int r = cur_r0 + n * 8 + g;
             const bool live = n * 8 + g < width;
-            const __nv_bfloat16* src = p.q + (int64_t)(q.row0 + (live ? r / p.rep : 0)) * p.ldq +
-                                       (int64_t)(head * p.rep + (live ? r % p.rep : 0)) * D;
+            const __nv_bfloat16* src = p.q + (int64_t)(cq.row0 + (live ? r / p.rep : 0)) * p.ldq +
+                                       (int64_t)(cur_head * p.rep + (live ? r % p.rep : 0)) * D;
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
                 float sum = 0.f;
@@ -207,7 +263,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int col = n * 8 + 2 * t + j;
-                last[n][j] = col < width ? min(lead + (r0 + col) / p.rep, cap - 1) : -1;
+                last[n][j] = col < width ? min(lead + (cur_r0 + col) / p.rep, cap - 1) : -1;
             }
         }
 
@@ -226,53 +282,17 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             }
         }
 
-        // ---- this warp's steps st0 + warp + 4 i.  Lane j looks up the two tiles of the
-        // warp's step i0 + j, for 32 steps at a time.
-        const int mine_n = st1 - st0 > warp ? (st1 - st0 - warp + kAttWarps - 1) / kAttWarps : 0;
-        const unsigned char* tile_a = nullptr;
-        const unsigned char* tile_b = nullptr;
-        auto lookup = [&](int i) {
-            const int tok = (st0 + warp + kAttWarps * (i + lane)) * kAttStep;
-            tile_a = i + lane < mine_n && tok < tokens ? kv_tile_of(v, seq, tok, head, kTile) : nullptr;
-            tile_b = i + lane < mine_n && tok + kKvTile < tokens ? kv_tile_of(v, seq, tok + kKvTile, head, kTile) : nullptr;
-        };
-        int i_look = 0;
-        uint32_t have_a = 0, have_b = 0;                // tiles present, one bit per looked-up step
-        auto issue = [&](int i, uint32_t stage) {       // copies of step i into `stage`
-            const int j = i - i_look;
-            const unsigned char* a = reinterpret_cast<const unsigned char*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(tile_a), j));
-            const unsigned char* b = reinterpret_cast<const unsigned char*>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(tile_b), j));
-            if (lane == 0) {
-                mbar_arrive_expect_tx(wbar + stage * 8, (a ? kTile : 0) + (b ? kTile : 0));
-                if (a) bulk_g2s(wring + stage * kStage, a, kTile, wbar + stage * 8);
-                if (b) bulk_g2s(wring + stage * kStage + kTile, b, kTile, wbar + stage * 8);
-            }
-        };
-        // presence bits follow the issue: bit (step % 32) is set when the step is issued
-        auto put = [&](int i, uint32_t stage) {
-            if (i - i_look >= 32) {
-                i_look += 32;
-                lookup(i_look);
-            }
-            const int j = i - i_look;
-            const uint32_t ba = __ballot_sync(0xffffffffu, tile_a != nullptr), bb = __ballot_sync(0xffffffffu, tile_b != nullptr);
-            const uint32_t bit = 1u << (i & 31);
-            have_a = (ba >> j & 1) ? have_a | bit : have_a & ~bit;
-            have_b = (bb >> j & 1) ? have_b | bit : have_b & ~bit;
-            issue(i, stage);
-        };
-        lookup(0);
-        for (int i = 0; i < min(kAttStages, mine_n); ++i) put(i, (it + i) % kAttStages);
-
         for (int i = 0; i < mine_n; ++i, ++it) {
             const uint32_t stage = it % kAttStages;
             if (!mbar_wait(wbar + stage * 8, (it / kAttStages) & 1, kWaitLimitNs)) {
+                // let the copies in flight land; the rest of the range does no work
                 ok = false;
+                for (int k = 1; k < kAttStages; ++k)
+                    mbar_wait(wbar + ((it + k) % kAttStages) * 8, ((it + k) / kAttStages) & 1, 100000000ull);
+                if (lane == 0) set_error(v.err, LORA_DERR_TIMEOUT);
                 break;
             }
-            const int tok0 = (st0 + warp + kAttWarps * i) * kAttStep;
+            const int tok0 = (st0 + me + way * i) * kAttStep;
             const bool has_a = have_a >> (i & 31) & 1, has_b = have_b >> (i & 31) & 1;
             const bool masked = tok0 + kAttStep - 1 > low || !has_a || !has_b;
             const uint32_t base = wring + stage * kStage;
@@ -429,7 +449,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             if (i + kAttStages < mine_n) put(i + kAttStages, stage);
         }
 
-        // ---- the four warps' results, through the ring (idle now)
+        // ---- the lanes' sums, and the offsets' part of the output
         float* mine_o = reinterpret_cast<float*>(ring + warp * kAttStages * kStage);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -440,10 +460,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                 ls += __shfl_xor_sync(0xffffffffu, ls, 8);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 16);
                 const int col = n * 8 + 2 * t + j;
-                if (g == 0) {
-                    stat[warp][col][0] = m[n][j];
-                    stat[warp][col][1] = ls;
-                }
                 float of[kGroups];
 #pragma unroll
                 for (int gr = 0; gr < kGroups; ++gr) {
@@ -452,50 +468,61 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                     of[gr] += __shfl_xor_sync(0xffffffffu, of[gr], 8);
                     of[gr] += __shfl_xor_sync(0xffffffffu, of[gr], 16);
                 }
+                const int row = cq.row0 + (cur_r0 + col) / p.rep, hq = cur_head * p.rep + (cur_r0 + col) % p.rep;
+                if (g == 0) {
+                    if (!solo) {
+                        stat[warp][col][0] = m[n][j];
+                        stat[warp][col][1] = ls;
+                    } else if (col < width) {
+                        att_store_lse(p, row, hq, m[n][j], ls);
+                    }
+                }
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     const float a = of[c / kPerG];
-                    *reinterpret_cast<float4*>(mine_o + col * D + c * 32 + 4 * g) =
-                        make_float4(o[n][2 * c][j] + a, o[n][2 * c][2 + j] + a, o[n][2 * c + 1][j] + a,
-                                    o[n][2 * c + 1][2 + j] + a);
+                    const float4 x = make_float4(o[n][2 * c][j] + a, o[n][2 * c][2 + j] + a, o[n][2 * c + 1][j] + a,
+                                                 o[n][2 * c + 1][2 + j] + a);
+                    if (!solo) *reinterpret_cast<float4*>(mine_o + col * D + c * 32 + 4 * g) = x;
+                    else if (col < width) att_store(p, row, hq, D, c * 32 + 4 * g, x, ls);
                 }
             }
-        if (!ok) {                                      // let the copies in flight land
-            for (int i = 1; i < kAttStages; ++i)
-                mbar_wait(wbar + ((it + i) % kAttStages) * 8, ((it + i) / kAttStages) & 1, 100000000ull);
-            if (lane == 0) set_error(v.err, LORA_DERR_TIMEOUT);
+        if (solo) {
+            __syncwarp();
+            continue;
         }
+
+        // ---- the four warps' results, through the ring (idle now), four values a thread
         ok = !__syncthreads_or(!ok);
-        const bool whole = st0 == 0 && st1 == steps;
-        const int64_t c0 = item / per, c1 = (item + steps - 1) / per;
-        const int slot = pos == first ? 0 : 1;
-        float* part = p.part + ((int64_t)blockIdx.x * 2 + slot) * kRows * kPitch;
-        for (int e = tid; e < width * D; e += kAttThreads) {
-            const int r = e / D, d = e % D;
+        float* part = p.part + ((int64_t)blockIdx.x * 2 + (body < first ? 0 : 1)) * kRows * kPitch;
+        for (int e = tid; e < width * (D / 4); e += kAttThreads) {
+            const int r = e / (D / 4), d = e % (D / 4) * 4;
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, stat[w][r][0]);
-            float acc = 0.f, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kAttWarps; ++w) {
                 const float f = top == -INFINITY ? 0.f : exp2_approx((stat[w][r][0] - top) * sl);
-                acc += f * reinterpret_cast<const float*>(ring + w * kAttStages * kStage)[e];
+                const float4 x = *reinterpret_cast<const float4*>(ring + w * kAttStages * kStage + (r * D + d) * 4);
+                acc.x += f * x.x;
+                acc.y += f * x.y;
+                acc.z += f * x.z;
+                acc.w += f * x.w;
                 sum += f * stat[w][r][1];
             }
             if (whole) {
-                const int pr = r0 + r, row = q.row0 + pr / p.rep, hq = head * p.rep + pr % p.rep;
-                p.out[row * p.ldo + (int64_t)hq * D + d] = __float2bfloat16_rn(sum > 0.f || sum != sum ? acc / sum : 0.f);
-                if (d == 0 && p.lse) p.lse[(int64_t)row * p.q_heads + hq] = top == -INFINITY ? -INFINITY : top * p.scale + logf(sum);
+                const int pr = cur_r0 + r, row = cq.row0 + pr / p.rep, hq = cur_head * p.rep + pr % p.rep;
+                att_store(p, row, hq, D, d, acc, sum);
+                if (d == 0) att_store_lse(p, row, hq, top, sum);
             } else {
-                part[r * kPitch + d] = acc;
-                if (d == 0) {
-                    part[r * kPitch + D] = top;
-                    part[r * kPitch + D + 1] = sum;
-                }
+                *reinterpret_cast<float4*>(part + r * kPitch + d) = acc;
+                if (d == 0) *reinterpret_cast<float2*>(part + r * kPitch + D) = make_float2(top, sum);
             }
         }
         fence_proxy_async_smem();                       // the ring is written by copies next
         if (!whole) {
+            const int64_t c0 = body / per, c1 = (body + steps - 1) / per;
             __threadfence();
             __syncthreads();
             if (tid == 0) last_in = atomicAdd(&p.tickets[c0], 1u) == (uint32_t)(c1 - c0);
@@ -503,28 +530,52 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             if (last_in) {
                 __threadfence();
                 if (tid == 0) p.tickets[c0] = 0;
-                for (int e = tid; e < width * D; e += kAttThreads) {
-                    const int r = e / D, d = e % D;
-                    float top = -INFINITY, acc = 0.f, sum = 0.f;
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        // a CTA's first part lies in its slot 0
-                        const float* src = p.part + (c * 2 + (item > c * per ? 1 : 0)) * kRows * kPitch + r * kPitch;
-                        const float mt = __ldcg(src + D), ls = __ldcg(src + D + 1), x = __ldcg(src + d);
-                        const float mn = fmaxf(top, mt);
-                        const float fa = mn == -INFINITY ? 1.f : exp2_approx((top - mn) * sl);
-                        const float fb = mn == -INFINITY ? 0.f : exp2_approx((mt - mn) * sl);
-                        acc = acc * fa + x * fb;
-                        sum = sum * fa + ls * fb;
+                const int n = (int)(c1 - c0) + 1;
+                auto src = [&](int i) {                 // the item's part of CTA c0 + i
+                    return p.part + ((c0 + i) * 2 + (body < (c0 + i) * per ? 0 : 1)) * (int64_t)(kRows * kPitch);
+                };
+                for (int e = tid; e < width * (D / 4); e += kAttThreads) {
+                    const int r = e / (D / 4), d = e % (D / 4) * 4;
+                    float top = -INFINITY, sum = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int i0 = 0; i0 < n; i0 += kAttJoin) {  // kAttJoin parts' loads in flight
+                        float2 ms[kAttJoin];
+                        float4 x[kAttJoin];
+#pragma unroll
+                        for (int i = 0; i < kAttJoin; ++i) {
+                            ms[i] = make_float2(-INFINITY, 0.f);
+                            x[i] = acc;
+                            if (i0 + i < n) {
+                                const float* from = src(i0 + i) + r * kPitch;
+                                ms[i] = __ldcg(reinterpret_cast<const float2*>(from + D));
+                                x[i] = __ldcg(reinterpret_cast<const float4*>(from + d));
+                            }
+                        }
+                        float mn = top;
+#pragma unroll
+                        for (int i = 0; i < kAttJoin; ++i) mn = fmaxf(mn, ms[i].x);
+                        const float f0 = mn == -INFINITY ? 0.f : exp2_approx((top - mn) * sl);
+                        acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+                        sum *= f0;
                         top = mn;
+#pragma unroll
+                        for (int i = 0; i < kAttJoin; ++i) {
+                            if (i0 + i >= n) continue;
+                            const float f = mn == -INFINITY ? 0.f : exp2_approx((ms[i].x - mn) * sl);
+                            acc.x += f * x[i].x;
+                            acc.y += f * x[i].y;
+                            acc.z += f * x[i].z;
+                            acc.w += f * x[i].w;
+                            sum += f * ms[i].y;
+                        }
                     }
-                    const int pr = r0 + r, row = q.row0 + pr / p.rep, hq = head * p.rep + pr % p.rep;
-                    p.out[row * p.ldo + (int64_t)hq * D + d] = __float2bfloat16_rn(sum > 0.f || sum != sum ? acc / sum : 0.f);
-                    if (d == 0 && p.lse) p.lse[(int64_t)row * p.q_heads + hq] = top == -INFINITY ? -INFINITY : top * p.scale + logf(sum);
+                    const int pr = cur_r0 + r, row = cq.row0 + pr / p.rep, hq = cur_head * p.rep + pr % p.rep;
+                    att_store(p, row, hq, D, d, acc, sum);
+                    if (d == 0) att_store_lse(p, row, hq, top, sum);
                 }
             }
         }
         __syncthreads();
-        pos = item + st1;
     }
 }
 
