@@ -34,7 +34,7 @@ constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kAttStep = 32;          // tokens of a step (two tiles)
 constexpr int kAttStages = 3;
-constexpr int kAttMaxCtas = 1024;
+constexpr int kAttMaxCtas = kStepTickets;
 constexpr int kAttJoin = 8;           // parts of an item whose loads are in flight together
 constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40: stands for a scale of 0, below f16's smallest
 constexpr int kAttItemCost = 3;       // units of an item beside its steps
@@ -49,17 +49,17 @@ struct AttendParams {
     int64_t ldq, ldo;
     int32_t q_heads, rep;
     float scale;
-    uint32_t* tickets;      // [kAttMaxCtas], zero between calls
+    uint32_t* tickets;      // [kStepTickets], zero between calls
     float* part;            // [kAttMaxCtas][2][8 NT][D + 4]
 };
 
 __host__ __device__ constexpr size_t attend_smem(int dim, int group) {
     return (size_t)kAttWarps * kAttStages * 2 * kv_tile_bytes(dim, group);
 }
-// Workspace after the header: tickets and partial results.
+// Bytes of workspace: header, tickets and partial results.
 __host__ __device__ constexpr size_t attend_part_floats(int nt, int dim) { return (size_t)2 * 8 * nt * (dim + 4); }
 __host__ __device__ constexpr size_t attend_workspace(int nt, int dim) {
-    return kAttMaxCtas * 4 + kAttMaxCtas * attend_part_floats(nt, dim) * 4;
+    return kStepPartAt + kAttMaxCtas * attend_part_floats(nt, dim) * 4;
 }
 
 // One request as the schedule sees it.

@@ -41,7 +41,7 @@ int attend_nt(const lora_kv_cache_desc* c, const lora_kv_batch* b, int32_t q_hea
     return (int64_t)b->max_q * (q_heads / c->num_kv_heads) <= 8 ? 1 : 2;
 }
 
-size_t workspace_bytes() { return align256(sizeof(WsHeader) + attend_workspace(2, 128)); }
+size_t workspace_bytes() { return align256(attend_workspace(2, 128)); }
 
 lora_status check_call(const lora_kv_cache_desc* c, const lora_kv_batch* b, const void* ws, size_t ws_bytes, size_t need) {
     lora_status st = check_sizes(c, b);
@@ -262,7 +262,7 @@ lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch*
     p.rep = num_q_heads / cache->num_kv_heads;
     p.scale = softmax_scale;
     p.tickets = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + sizeof(WsHeader));
-    p.part = reinterpret_cast<float*>(p.tickets + kAttMaxCtas);
+    p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kStepPartAt);
     if (attend_nt(cache, batch, num_q_heads) == 1) return attend_by_shape<1>(cache, p, (cudaStream_t)stream);
     return attend_by_shape<2>(cache, p, (cudaStream_t)stream);
 }

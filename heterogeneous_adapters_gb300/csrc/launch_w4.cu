@@ -1,6 +1,8 @@
 // C ABI of the products with 4-bit weights (include/lora_w4.h): argument checks and launch.
 #include <string.h>
 
+#include <algorithm>
+
 #include "host.h"
 #include "w4_matvec.cuh"
 
@@ -21,6 +23,31 @@ lora_status check_sizes(const lora_w4_problem* probs, int32_t nprob, int32_t T) 
     return LORA_OK;
 }
 
+size_t workspace_bytes() { return align256(w4_workspace(2)); }
+
+template <int G, int NT>
+lora_status launch(W4Params& p, cudaStream_t s) {
+    DeviceInfo* di = nullptr;
+    lora_status st = device_info(&di);
+    if (st != LORA_OK) return st;
+    constexpr size_t smem = w4_smem(G, NT);
+    auto kern = w4_matvec_kernel<G, NT>;
+    static thread_local int ready_dev = -1, per_sm = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (ready_dev != dev) {
+        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        if (st != LORA_OK) return st;
+        st = cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kW4Threads, smem));
+        if (st != LORA_OK) return st;
+        ready_dev = dev;
+    }
+    const int grid = std::min(di->sm_count * std::max(per_sm, 1), kW4MaxCtas);
+    p.per = (p.total + grid - 1) / grid;
+    kern<<<grid, kW4Threads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
 }  // namespace
 
 extern "C" {
@@ -29,7 +56,7 @@ lora_status lora_w4_workspace_size(const lora_w4_problem* probs, int32_t nprob, 
     if (bytes == nullptr) return LORA_EINVAL;
     lora_status st = check_sizes(probs, nprob, T);
     if (st != LORA_OK) return st;
-    *bytes = sizeof(WsHeader);
+    *bytes = workspace_bytes();
     return LORA_OK;
 }
 
@@ -37,10 +64,6 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
                            void* stream) {
     lora_status st = check_sizes(probs, nprob, T);
     if (st != LORA_OK) return st;
-    if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < sizeof(WsHeader)) return LORA_EWORKSPACE;
-    if (nprob == 0 || T == 0) return LORA_OK;
-    W4Params p;
-    memset(&p, 0, sizeof p);
     for (int32_t i = 0; i < nprob; ++i) {
         const lora_w4_problem& pr = probs[i];
         if (pr.x == nullptr || pr.y == nullptr || pr.codes == nullptr || pr.scales == nullptr) return LORA_EINVAL;
@@ -48,14 +71,48 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
             ((uintptr_t)pr.zeros & 3u) != 0 || pr.ldx % 8 != 0 || pr.ldy % 8 != 0)
             return LORA_EALIGN;
         if (pr.ldx < pr.K || pr.ldy < pr.N) return LORA_EINVAL;
-        p.prob[i] = pr;
-        p.first[i + 1] = p.first[i] + (pr.N + kW4Warps - 1) / kW4Warps;
     }
-    p.nprob = nprob;
-    p.T = T;
-    p.err = &reinterpret_cast<WsHeader*>(ws)->err;
-    w4_matvec_kernel<<<dim3(p.first[nprob], (T + kW4Rows - 1) / kW4Rows), kW4Warps * 32, 0, (cudaStream_t)stream>>>(p);
-    return cuda_status(cudaGetLastError());
+    if (nprob == 0 || T == 0) return LORA_OK;
+    if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes()) return LORA_EWORKSPACE;
+    // one launch per group size of the call
+    for (const int32_t group : {32, 64, 128}) {
+        for (int32_t t0 = 0; t0 < T; t0 += 16) {
+            W4Params p;
+            memset(&p, 0, sizeof p);
+            int64_t total = 0;
+            for (int32_t i = 0; i < nprob; ++i) {
+                const lora_w4_problem& pr = probs[i];
+                if (pr.group != group) continue;
+                W4Prob& o = p.prob[p.nprob++];
+                o.x = reinterpret_cast<const __nv_bfloat16*>(pr.x) + t0 * pr.ldx;
+                o.y = reinterpret_cast<__nv_bfloat16*>(pr.y) + t0 * pr.ldy;
+                o.codes = reinterpret_cast<const unsigned char*>(pr.codes);
+                o.scales = reinterpret_cast<const unsigned char*>(pr.scales);
+                o.zeros = reinterpret_cast<const unsigned char*>(pr.zeros);
+                o.ldx = pr.ldx;
+                o.ldy = pr.ldy;
+                o.N = pr.N;
+                o.K = pr.K;
+                o.group = pr.group;
+                o.kblocks = (pr.K + kW4K - 1) / kW4K;
+                o.first = (int32_t)total;
+                total += (int64_t)((pr.N + kW4Rows - 1) / kW4Rows) * o.kblocks;
+                if (total > INT32_MAX) return LORA_ETOOBIG;
+            }
+            if (p.nprob == 0) break;
+            p.total = (int32_t)total;
+            p.T = std::min(T - t0, 16);
+            p.tickets = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + sizeof(WsHeader));
+            p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kStepPartAt);
+            cudaStream_t s = (cudaStream_t)stream;
+            if (p.T <= 8)
+                st = group == 32 ? launch<32, 1>(p, s) : group == 64 ? launch<64, 1>(p, s) : launch<128, 1>(p, s);
+            else
+                st = group == 32 ? launch<32, 2>(p, s) : group == 64 ? launch<64, 2>(p, s) : launch<128, 2>(p, s);
+            if (st != LORA_OK) return st;
+        }
+    }
+    return LORA_OK;
 }
 
 }  // extern "C"

@@ -38,12 +38,12 @@ typedef struct {
 } lora_w4_problem;
 
 /* Bytes of device workspace for the call (the device error word and partial sums); the
- * pointers of the problems are not read.  Prepare it once with lora_kv_workspace_init or
- * lora_workspace_init; it may be the workspace of the lora_kv.h calls if large enough. */
+ * pointers of the problems are not read.  Prepare it once with lora_kv_workspace_init
+ * (lora_kv.h); one workspace, large enough for both, may serve those calls and this one. */
 lora_status lora_w4_workspace_size(const lora_w4_problem* probs, int32_t nprob, int32_t T, size_t* bytes);
 
 /* All projections of the call, at most LORA_W4_MAX_PROBLEMS, over the same T <=
- * LORA_W4_MAX_ROWS rows (their x may differ), in one launch. */
+ * LORA_W4_MAX_ROWS rows (their x may differ), in one launch per group size. */
 lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
                            void* stream);
 
