@@ -58,6 +58,9 @@ RingShape ring_shape(int h, int r_max, int smem_optin, int cwarps, int force_rp,
 lora_status run_delta_ring(const lora_pool* pool, const lora_problem* probs, int32_t nprob, void* ws,
                            float* t_out, cudaStream_t stream);
 
+// cuTensorMapEncodeTiled, looked up once (launch_tile.cu).
+lora_status encode_fn(PFN_cuTensorMapEncodeTiled_v12000* out);
+
 // launch_tile.cu: the tensor-core kernel over the tile list, and the fused launch of both
 // work classes (h <= 5120).
 int mma_min_rows(const lora_pool* pool);

@@ -5,6 +5,7 @@
 
 #include "host.h"
 #include "w4_matvec.cuh"
+#include "w4_wide.cuh"
 
 using namespace lora;
 using namespace lora::host;
@@ -23,7 +24,7 @@ lora_status check_sizes(const lora_w4_problem* probs, int32_t nprob, int32_t T) 
     return LORA_OK;
 }
 
-size_t workspace_bytes() { return align256(w4_workspace(2)); }
+size_t workspace_bytes() { return align256(std::max(w4_workspace(2), wide_workspace(128))); }
 
 template <int G, int NT>
 lora_status launch(W4Params& p, cudaStream_t s) {
@@ -46,6 +47,58 @@ lora_status launch(W4Params& p, cudaStream_t s) {
     p.per = (p.total + grid - 1) / grid;
     kern<<<grid, kW4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
+}
+
+// 2-D map of `rows` rows of `inner` elements, box {box0, box1}, 128-byte swizzle, zeros outside.
+lora_status map2d(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                  uint64_t inner, uint64_t rows, uint64_t pitch, uint32_t box0, uint32_t box1) {
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {box0, box1}, one[2] = {1, 1};
+    const CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return LORA_OK;
+    g_last_cuda_error = 10000 + (int)r;
+    return LORA_ECUDA;
+}
+
+template <int G, int N>
+lora_status launch_wide(WideParams& w, cudaStream_t s) {
+    DeviceInfo* di = nullptr;
+    lora_status st = device_info(&di);
+    if (st != LORA_OK) return st;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    if ((st = encode_fn(&enc)) != LORA_OK) return st;
+    for (int i = 0; i < w.p.nprob; ++i) {
+        const W4Prob& pr = w.p.prob[i];
+        st = map2d(enc, &w.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.codes, pr.K / 2, pr.N, pr.K / 2, kWideK / 2, kWideRows);
+        if (st != LORA_OK) return st;
+        st = map2d(enc, &w.x[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.x, pr.K, w.p.T, pr.ldx * 2, 64, N);
+        if (st != LORA_OK) return st;
+    }
+    constexpr size_t smem = wide_smem(N);
+    auto kern = w4_wide_kernel<G, N>;
+    static thread_local int ready_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (ready_dev != dev) {
+        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        if (st != LORA_OK) return st;
+        ready_dev = dev;
+    }
+    const int grid = std::min(di->sm_count, kWideMaxCtas);
+    w.p.per = (w.p.total + grid - 1) / grid;
+    kern<<<grid, kWideThreads, smem, s>>>(w);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int G>
+lora_status launch_group(WideParams& w, cudaStream_t s) {
+    const int T = w.p.T;
+    if (T <= 8) return launch<G, 1>(w.p, s);
+    if (T <= kW4NarrowRows) return launch<G, 2>(w.p, s);
+    if (T <= 32) return launch_wide<G, 32>(w, s);
+    return T <= 64 ? launch_wide<G, 64>(w, s) : launch_wide<G, 128>(w, s);
 }
 
 }  // namespace
@@ -74,11 +127,15 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
     }
     if (nprob == 0 || T == 0) return LORA_OK;
     if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes()) return LORA_EWORKSPACE;
-    // one launch per group size of the call
+    // one launch per group size of the call and 128 rows
+    static_assert(kW4K == kWideK, "both kernels' blocks are 256 of K");
+    static thread_local WideParams w;
     for (const int32_t group : {32, 64, 128}) {
-        for (int32_t t0 = 0; t0 < T; t0 += 16) {
-            W4Params p;
-            memset(&p, 0, sizeof p);
+        for (int32_t t0 = 0; t0 < T; t0 += 128) {
+            memset(&w, 0, sizeof w);
+            W4Params& p = w.p;
+            p.T = std::min(T - t0, 128);
+            const int32_t block_rows = p.T <= kW4NarrowRows ? kW4Rows : kWideRows;
             int64_t total = 0;
             for (int32_t i = 0; i < nprob; ++i) {
                 const lora_w4_problem& pr = probs[i];
@@ -96,19 +153,16 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
                 o.group = pr.group;
                 o.kblocks = (pr.K + kW4K - 1) / kW4K;
                 o.first = (int32_t)total;
-                total += (int64_t)((pr.N + kW4Rows - 1) / kW4Rows) * o.kblocks;
+                total += (int64_t)((pr.N + block_rows - 1) / block_rows) * o.kblocks;
                 if (total > INT32_MAX) return LORA_ETOOBIG;
             }
             if (p.nprob == 0) break;
             p.total = (int32_t)total;
-            p.T = std::min(T - t0, 16);
             p.tickets = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + sizeof(WsHeader));
             p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kStepPartAt);
+            w.err = &reinterpret_cast<WsHeader*>(ws)->err;
             cudaStream_t s = (cudaStream_t)stream;
-            if (p.T <= 8)
-                st = group == 32 ? launch<32, 1>(p, s) : group == 64 ? launch<64, 1>(p, s) : launch<128, 1>(p, s);
-            else
-                st = group == 32 ? launch<32, 2>(p, s) : group == 64 ? launch<64, 2>(p, s) : launch<128, 2>(p, s);
+            st = group == 32 ? launch_group<32>(w, s) : group == 64 ? launch_group<64>(w, s) : launch_group<128>(w, s);
             if (st != LORA_OK) return st;
         }
     }

@@ -24,6 +24,7 @@ namespace lora {
 
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = kW4Warps * 32;
+constexpr int kW4NarrowRows = 16;  // rows of x up to which this kernel serves
 constexpr int kW4Rows = 32;        // rows of W of a block
 constexpr int kW4K = 256;          // K of a block (128 bytes of codes a row)
 constexpr int kW4Stages = 3;
