@@ -49,14 +49,14 @@ lora_status launch(W4Params& p, cudaStream_t s) {
     return cuda_status(cudaGetLastError());
 }
 
-// 2-D map of `rows` rows of `inner` elements, box {box0, box1}, 128-byte swizzle, zeros outside.
+// 2-D map of `rows` rows of `inner` elements, box {box0, box1}, zeros outside.
 lora_status map2d(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, CUtensorMapDataType type, const void* base,
-                  uint64_t inner, uint64_t rows, uint64_t pitch, uint32_t box0, uint32_t box1) {
+                  uint64_t inner, uint64_t rows, uint64_t pitch, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[2] = {inner, rows};
     const cuuint64_t strides[1] = {pitch};
     const cuuint32_t box[2] = {box0, box1}, one[2] = {1, 1};
     const CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                           swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r == CUDA_SUCCESS) return LORA_OK;
     g_last_cuda_error = 10000 + (int)r;
     return LORA_ECUDA;
@@ -71,12 +71,17 @@ lora_status launch_wide(WideParams& w, cudaStream_t s) {
     if ((st = encode_fn(&enc)) != LORA_OK) return st;
     for (int i = 0; i < w.p.nprob; ++i) {
         const W4Prob& pr = w.p.prob[i];
-        st = map2d(enc, &w.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.codes, pr.K / 2, pr.N, pr.K / 2, kWideK / 2, kWideRows);
+        st = map2d(enc, &w.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.codes, pr.K / 2, pr.N, pr.K / 2, kWideK / 2, kWideRows,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
         if (st != LORA_OK) return st;
-        st = map2d(enc, &w.x[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.x, pr.K, w.p.T, pr.ldx * 2, 64, N);
+        st = map2d(enc, &w.x[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.x, pr.K, w.p.T, pr.ldx * 2, 64, N,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != LORA_OK) return st;
+        st = map2d(enc, &w.y[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.y, pr.N, w.p.T, pr.ldy * 2, kWideRows, N,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
         if (st != LORA_OK) return st;
     }
-    constexpr size_t smem = wide_smem(N);
+    constexpr size_t smem = wide_smem(N, G);
     auto kern = w4_wide_kernel<G, N>;
     static thread_local int ready_dev = -1;
     int dev = 0;
@@ -88,7 +93,7 @@ lora_status launch_wide(WideParams& w, cudaStream_t s) {
     }
     const int grid = std::min(di->sm_count, kWideMaxCtas);
     w.p.per = (w.p.total + grid - 1) / grid;
-    kern<<<grid, kWideThreads, smem, s>>>(w);
+    kern<<<grid, wide_threads(N), smem, s>>>(w);
     return cuda_status(cudaGetLastError());
 }
 

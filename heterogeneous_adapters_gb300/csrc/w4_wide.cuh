@@ -10,8 +10,9 @@
 // the order of K) and draining (one FMA per group, row and column) fill most of the issue
 // slots of that time at 64 rows.
 //
-// One CTA per SM: warp 0 streams codes (blocks of 128 rows x 256 of K) and x by TMA, warp 1
-// issues the MMAs, warps 2-9 unpack, warps 10-17 drain.  CTAs take equal contiguous ranges of
+// One CTA per SM: warp 0 streams codes (blocks of 128 rows x 256 of K) by TMA and warp 11 x,
+// warp 1 issues the MMAs, warps 2-9 unpack, warp 10 brings scales and zero points, the others
+// drain.  CTAs take equal contiguous ranges of
 // the blocks of all projections; a row tile shared by several CTAs is joined over partial
 // sums in the workspace by the CTA that arrives last, in the order of K.
 #pragma once
@@ -21,18 +22,28 @@
 
 namespace lora {
 
-constexpr int kWideThreads = 18 * 32;
 constexpr int kWideRows = 128;                 // rows of W of a block
 constexpr int kWideK = 256;                    // K of a block
-constexpr int kWideChunk = 128;                // K of an A buffer and of an x stage
-constexpr int kWideCodeStages = 4;
-constexpr int kWideA = 4;                      // A buffers in tensor memory
 constexpr int kWideMaxCtas = 192;
 constexpr int kWideCodeBytes = kWideRows * kWideK / 2;
 
-__host__ __device__ constexpr int wide_x_stages(int n) { return n >= 128 ? 4 : 6; }
-__host__ __device__ constexpr size_t wide_smem(int n) {
-    return 1024 + (size_t)kWideCodeStages * kWideCodeBytes + (size_t)wide_x_stages(n) * n * kWideChunk * 2;
+// Shapes by the columns N (rows of x) and the group.  A span is what the roles hand over at
+// once: a block's 256 of K, or 128 where the x stages of 256 would not fit.  Half of tensor
+// memory holds the spans' A operands, half the D sums of `set` groups, twice.
+__host__ __device__ constexpr int wide_span(int n) { return n > 64 ? 128 : 256; }
+__host__ __device__ constexpr int wide_spans(int n) { return 512 / wide_span(n); }    // A buffers and x stages
+__host__ __device__ constexpr int wide_set(int n, int group) {
+    return 128 / n < wide_span(n) / group ? 128 / n : wide_span(n) / group;
+}
+__host__ __device__ constexpr int wide_code_stages(int n) { return n > 64 ? 3 : 4; }
+// Warps that drain: a thread holds at most 64 columns' sums.
+__host__ __device__ constexpr int wide_drain(int n) { return n > 64 ? 8 : 4; }
+__host__ __device__ constexpr int wide_threads(int n) { return (12 + wide_drain(n)) * 32; }
+// A stage's scales [groups][128] f16 and zeros [groups][64 bytes].
+__host__ __device__ constexpr int wide_param_bytes(int group) { return (kWideK / group) * (kWideRows * 2 + kWideRows / 2); }
+__host__ __device__ constexpr size_t wide_smem(int n, int group) {
+    return 1024 + (size_t)wide_code_stages(n) * (kWideCodeBytes + wide_param_bytes(group)) + (size_t)n * 512 * 2 +
+           (size_t)n * kWideRows * 2;
 }
 __host__ __device__ constexpr size_t wide_workspace(int n) {
     return kStepPartAt + (size_t)kWideMaxCtas * 2 * kWideRows * n * 4;
@@ -41,6 +52,7 @@ __host__ __device__ constexpr size_t wide_workspace(int n) {
 struct WideParams {
     CUtensorMap codes[LORA_W4_MAX_PROBLEMS];   // bytes {K / 2, N}, box {128, 128}, 128-byte swizzle
     CUtensorMap x[LORA_W4_MAX_PROBLEMS];       // bf16 {K, T}, box {64, N columns}, 128-byte swizzle
+    CUtensorMap y[LORA_W4_MAX_PROBLEMS];       // bf16 {N, T}, box {128, N columns}
     W4Params p;                                // blocks of 128 x 256
     uint32_t* err;
 };
@@ -64,9 +76,6 @@ __device__ __forceinline__ void wide_next(const W4Params& p, WideAt& a) {
     a.tile = 0;
     ++a.prob;
 }
-// 128-wide pieces of K in a block.
-__device__ __forceinline__ int wide_chunks(const W4Prob& pr, int kb) { return pr.K - kb * kWideK > kWideChunk ? 2 : 1; }
-
 // The eight codes of a word minus the zero point, in order, as four bf16 pairs.
 __device__ __forceinline__ void codes_in_order(uint32_t w, uint32_t minus, uint32_t* out) {
     const uint32_t h = w >> 4;
@@ -91,39 +100,38 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 }
 
 template <int G, int N>
-__global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_constant__ WideParams prm) {
-    constexpr int kXStages = wide_x_stages(N), kXBytes = N * kWideChunk * 2, kGroups = kWideChunk / G;
-    constexpr int kMine = N / 2;               // columns of a drain thread
-    constexpr uint32_t kACol = 256;            // D buffers at columns 0 and N, A buffers from 256
+__global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __grid_constant__ WideParams prm) {
+    constexpr int kSpan = wide_span(N), kSpans = wide_spans(N), kCodeStages = wide_code_stages(N);
+    constexpr int kXBytes = N * kSpan * 2, kParams = wide_param_bytes(G), kBlockGroups = kWideK / G;
+    constexpr int kSet = wide_set(N, G), kSets = kSpan / G / kSet;    // groups of a D set, sets of a span
+    constexpr int kDrain = wide_drain(N), kMine = N / (kDrain / 4);   // columns of a drain thread
+    // D sets at columns 0 and 128, A buffers from 256.  A set's MMAs end in one commit, to
+    // d_full[set % kDone]; the commit of a span's last set also says that its A buffer and x
+    // stage are free.
+    constexpr uint32_t kDCols = 128, kACol = 256;
+    constexpr int kDone = kSpans * kSets;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t code_full[kWideCodeStages], code_empty[kWideCodeStages], x_full[kXStages], x_empty[kXStages],
-        a_full[kWideA], a_empty[kWideA], d_full[2], d_empty[2], join, final_bar;
+    __shared__ __align__(8) uint64_t code_full[kCodeStages], code_empty[kCodeStages], a_full[kSpans], d_full[kDone], d_empty[2],
+        join, final_bar;
     __shared__ uint32_t tmem_slot, last_in;
     const W4Params& p = prm.p;
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t codes0 = smem_addr(base), x0 = codes0 + kWideCodeStages * kWideCodeBytes;
+    const uint32_t codes0 = smem_addr(base), x0 = codes0 + kCodeStages * kWideCodeBytes, y0 = x0 + kSpans * kXBytes;
+    const uint32_t params0 = y0 + N * kWideRows * 2;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int first = blockIdx.x * p.per, end = min(first + p.per, p.total);
     if (first >= end) return;
     auto bar = [](uint64_t& b) { return smem_addr(&b); };
     if (tid == 0) {
-        for (int i = 0; i < kWideCodeStages; ++i) {
-            mbar_init(bar(code_full[i]), 1);
-            mbar_init(bar(code_empty[i]), 8);
+        for (int i = 0; i < kCodeStages; ++i) {
+            mbar_init(bar(code_full[i]), 1 + 32);      // the TMA's bytes, and each lane's copies
+            mbar_init(bar(code_empty[i]), 8 + kDrain);
         }
-        for (int i = 0; i < kXStages; ++i) {
-            mbar_init(bar(x_full[i]), 1);
-            mbar_init(bar(x_empty[i]), 1);
-        }
-        for (int i = 0; i < kWideA; ++i) {
-            mbar_init(bar(a_full[i]), 8);
-            mbar_init(bar(a_empty[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(d_full[i]), 1);
-            mbar_init(bar(d_empty[i]), 8);
-        }
-        mbar_init(bar(join), 8);
+        // x's bytes, and the unpacking warps of the span
+        for (int i = 0; i < kSpans; ++i) mbar_init(bar(a_full[i]), 1 + (kSpan == kWideK ? 8 : 4));
+        for (int i = 0; i < kDone; ++i) mbar_init(bar(d_full[i]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(bar(d_empty[i]), kDrain);
+        mbar_init(bar(join), kDrain);
         mbar_init(bar(final_bar), 1);
         fence_mbar_init();
     }
@@ -137,120 +145,136 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
     bool ok = true;
 
+    const uint32_t spans = kWideK / kSpan * (uint32_t)(end - first);   // of this CTA's range
     if (warp == 0) {
-        // ------------------------------------------------------------------ codes and x
+        // ------------------------------------------------------------------ codes, one thread
         if (lane == 0) {
             WideAt a = wide_at(p, first);
-            uint32_t ic = 0, ix = 0;
+            uint32_t ic = 0;
             for (int u = first; u < end && ok; ++u, wide_next(p, a), ++ic) {
-                const uint32_t s = ic % kWideCodeStages;
-                if (!mbar_wait(bar(code_empty[s]), ((ic / kWideCodeStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                const uint32_t s = ic % kCodeStages;
+                if (!mbar_wait_quiet(bar(code_empty[s]), ((ic / kCodeStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
                 mbar_arrive_expect_tx(bar(code_full[s]), kWideCodeBytes);
-                tma_load_2d(codes0 + s * kWideCodeBytes, &prm.codes[a.prob], a.kb * (kWideK / 2), a.tile * kWideRows, bar(code_full[s]));
-                const int n = wide_chunks(p.prob[a.prob], a.kb);
-                for (int c = 0; c < n; ++c, ++ix) {
-                    const uint32_t t = ix % kXStages;
-                    if (!mbar_wait(bar(x_empty[t]), ((ix / kXStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-                    mbar_arrive_expect_tx(bar(x_full[t]), kXBytes);
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_2d(x0 + t * kXBytes + h * (kXBytes / 2), &prm.x[a.prob], a.kb * kWideK + c * kWideChunk + h * 64, 0,
-                                    bar(x_full[t]));
-                }
+                tma_load_2d(codes0 + s * kWideCodeBytes, &prm.codes[a.prob], a.kb * (kWideK / 2), a.tile * kWideRows,
+                            bar(code_full[s]));
             }
             if (!ok) set_error(prm.err, LORA_DERR_TIMEOUT);
             // every copy has landed before the CTA can end
-            for (uint32_t k = ic > kWideCodeStages ? ic - kWideCodeStages : 0; k < ic; ++k)
-                mbar_wait(bar(code_full[k % kWideCodeStages]), (k / kWideCodeStages) & 1, 100000000ull);
-            for (uint32_t k = ix > kXStages ? ix - kXStages : 0; k < ix; ++k)
-                mbar_wait(bar(x_full[k % kXStages]), (k / kXStages) & 1, 100000000ull);
+            for (uint32_t k = ic > kCodeStages ? ic - kCodeStages : 0; k < ic; ++k)
+                mbar_wait_quiet(bar(code_full[k % kCodeStages]), (k / kCodeStages) & 1, 100000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 11) {
+        // ------------------------------------------------------------------ x, one thread
+        if (lane == 0) {
+            WideAt a = wide_at(p, first);
+            uint32_t ix = 0;
+            for (int u = first; u < end && ok; ++u, wide_next(p, a)) {
+                for (int c = 0; c < kWideK / kSpan; ++c, ++ix) {
+                    const uint32_t b = ix % kSpans;
+                    if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((ix / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                    mbar_arrive_expect_tx(bar(a_full[b]), kXBytes);
+#pragma unroll
+                    for (int h = 0; h < kSpan / 64; ++h)
+                        tma_load_2d(x0 + b * kXBytes + h * N * 128, &prm.x[a.prob], a.kb * kWideK + c * kSpan + h * 64, 0, bar(a_full[b]));
+                }
+            }
+            if (!ok) set_error(prm.err, LORA_DERR_TIMEOUT);
+            for (uint32_t k = ix > kSpans ? ix - kSpans : 0; k < ix; ++k)
+                mbar_wait_quiet(bar(a_full[k % kSpans]), (k / kSpans) & 1, 100000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issue
-        constexpr uint32_t idesc = idesc_bf16(128, N, 0, 0);
-        WideAt a = wide_at(p, first);
-        uint32_t ix = 0, id = 0;               // chunks (A buffers, x stages) and groups (D buffers)
-        for (int u = first; u < end && ok; ++u, wide_next(p, a)) {
-            const int n = wide_chunks(p.prob[a.prob], a.kb);
-            for (int c = 0; c < n && ok; ++c, ++ix) {
-                const uint32_t t = ix % kXStages, b = ix % kWideA;
-                if (!mbar_wait(bar(x_full[t]), (ix / kXStages) & 1, kWaitLimitNs) ||
-                    !mbar_wait(bar(a_full[b]), (ix / kWideA) & 1, kWaitLimitNs)) { ok = false; break; }
-                for (int g = 0; g < kGroups; ++g, ++id) {
-                    if (!mbar_wait(bar(d_empty[id & 1]), ((id >> 1) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-                    tc_fence_after();
-                    if (lane == 0) {
+        // ------------------------------------------------------------------ MMA issue, one thread
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16(128, N, 0, 0);
+            uint32_t id = 0;                   // D sets
+            for (uint32_t i = 0; i < spans && ok; ++i) {
+                const uint32_t b = i % kSpans;
+                if (!mbar_wait_quiet(bar(a_full[b]), (i / kSpans) & 1, kWaitLimitNs)) { ok = false; break; }
+                const uint64_t db = smem_desc(x0 + b * kXBytes, 16, 1024, 2);
 #pragma unroll
-                        for (int k = 0; k < G / 16; ++k) {
-                            const int ks = g * (G / 16) + k;
-                            const uint64_t db = smem_desc(x0 + t * kXBytes + (ks / 4) * (kXBytes / 2) + (ks % 4) * 32, 16, 1024, 2);
-                            tc_mma_f16_ts(tmem + (id & 1) * N, tmem + kACol + b * 64 + ks * 8, db, idesc, k != 0);
-                        }
-                        tc_commit(bar(d_full[id & 1]));
-                        if (g == kGroups - 1) {
-                            tc_commit(bar(a_empty[b]));
-                            tc_commit(bar(x_empty[t]));
-                        }
+                for (int s = 0; s < kSets; ++s, ++id) {
+                    if (!mbar_wait_quiet(bar(d_empty[id & 1]), ((id >> 1) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kSet * G / 16; ++k) {
+                        const int ks = s * (kSet * G / 16) + k;
+                        tc_mma_f16_ts(tmem + (id & 1) * kDCols + k / (G / 16) * N, tmem + kACol + b * (kSpan / 2) + ks * 8,
+                                      db + ((ks / 4) * (N * 128) + (ks % 4) * 32) / 16, idesc, k % (G / 16) != 0);
                     }
-                    __syncwarp();
+                    tc_commit(bar(d_full[b * kSets + s]));
                 }
             }
-        }
-        if (!ok && lane == 0) set_error(prm.err, LORA_DERR_TIMEOUT);
-        if (lane == 0) {                       // the MMAs are done before tensor memory is given back
-            tc_commit(bar(final_bar));
-            mbar_wait(bar(final_bar), 0, 100000000ull);
+            if (!ok) set_error(prm.err, LORA_DERR_TIMEOUT);
+            tc_commit(bar(final_bar));         // the MMAs are done before tensor memory is given back
+            mbar_wait_quiet(bar(final_bar), 0, 100000000ull);
         }
         __syncwarp();
+    } else if (warp == 10) {
+        // ------------------------------------------------------------------ scales and zero points
+        WideAt a = wide_at(p, first);
+        uint32_t ic = 0;
+        for (int u = first; u < end && ok; ++u, wide_next(p, a), ++ic) {
+            const W4Prob& pr = p.prob[a.prob];
+            const uint32_t s = ic % kCodeStages;
+            if (!mbar_wait_quiet(bar(code_empty[s]), ((ic / kCodeStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+            const int row0 = a.tile * kWideRows, groups = pr.K / G;
+            for (int i = lane; i < kBlockGroups * 16; i += 32) {       // 8 rows of a group's scales, and of its zeros
+                const int g = i / 16, j = i % 16, grp = a.kb * kBlockGroups + g;
+                const bool in = grp < groups && row0 + j * 8 < pr.N;
+                const uint32_t dst = params0 + s * kParams;
+                cp_async16(dst + g * kWideRows * 2 + j * 16, pr.scales + (in ? ((int64_t)grp * pr.N + row0 + j * 8) * 2 : 0), in ? 16 : 0);
+                if (pr.zeros)
+                    cp_async4(dst + kBlockGroups * kWideRows * 2 + g * (kWideRows / 2) + j * 4,
+                              pr.zeros + (in ? (int64_t)grp * (pr.N / 2) + row0 / 2 + j * 4 : 0), in ? 4 : 0);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(code_full[s])) : "memory");
+        }
+        if (!ok && lane == 0) set_error(prm.err, LORA_DERR_TIMEOUT);
+        cp_async_wait<0>();
     } else if (warp < 10) {
-        // ------------------------------------------------------------------ unpacking: a row, 64 of every 128 of K
-        const int quad = warp & 3, half = (warp - 2) >> 2, r = quad * 32 + lane;
+        // ------------------------------------------------------------------ unpacking: a row, every other 128 of K
+        const int quad = warp & 3, turn = (warp - 2) >> 2, r = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         WideAt a = wide_at(p, first);
-        uint32_t ic = 0, ia = 0;
-        constexpr int kZ = G < 64 ? 2 : 1;     // zero points of 64 of K
-        // the zero points of chunk c of block a, as 128 + zero twice
-        auto zeros = [&](const WideAt& a, int c, uint32_t (&z)[kZ]) {
+        uint32_t ic = 0;
+        for (int u = first; u < end && ok; ++u, ++ic, wide_next(p, a)) {
             const W4Prob& pr = p.prob[a.prob];
-            const int row = a.tile * kWideRows + r;
+            const bool zeros = pr.zeros != nullptr;
+            const uint32_t s = ic % kCodeStages;
+            if (!mbar_wait_quiet(bar(code_full[s]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
+            {
+                const int c = turn;
+                const uint32_t i = kSpan == kWideK ? ic : 2 * ic + c, b = i % kSpans;   // span
+                const uint32_t acol = tmem + lane_base + kACol + b * (kSpan / 2) + (kSpan == kWideK ? c * 64 : 0);
 #pragma unroll
-            for (int i = 0; i < kZ; ++i) {
-                const int g = (a.kb * kWideK + c * kWideChunk + half * 64 + i * 32) / G;
-                uint32_t v = 8;
-                if (pr.zeros && row < pr.N && g * G < pr.K)
-                    v = __ldg(pr.zeros + (int64_t)g * (pr.N / 2) + row / 2) >> (row & 1) * 4 & 15;
-                z[i] = 0x43004300u + v * 0x00010001u;
-            }
-        };
-        uint32_t znext[kZ];
-        zeros(a, 0, znext);
-        for (int u = first; u < end && ok; ++u, ++ic) {
-            const int n = wide_chunks(p.prob[a.prob], a.kb);
-            WideAt an = a;
-            wide_next(p, an);
-            const uint32_t s = ic % kWideCodeStages;
-            if (!mbar_wait(bar(code_full[s]), (ic / kWideCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
-            for (int c = 0; c < n; ++c, ++ia) {
-                uint32_t z[kZ];
+                for (int h = 0; h < 2; ++h) {                      // 64 of K: 32 columns of tensor memory
+                    uint32_t out[32];
 #pragma unroll
-                for (int i = 0; i < kZ; ++i) z[i] = znext[i];
-                if (c + 1 < n) zeros(a, c + 1, znext);
-                else if (u + 1 < end) zeros(an, 0, znext);
-                uint32_t out[32];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int col = c * 4 + half * 2 + j;      // 16-byte column of the row
-                    const uint4 w = lds128(codes0 + s * kWideCodeBytes + r * 128 + ((col ^ (r & 7)) << 4));
-                    const uint32_t m = z[kZ > 1 ? j : 0];
-                    codes_in_order(w.x, m, out + j * 16);
-                    codes_in_order(w.y, m, out + j * 16 + 4);
-                    codes_in_order(w.z, m, out + j * 16 + 8);
-                    codes_in_order(w.w, m, out + j * 16 + 12);
+                    for (int j = 0; j < 2; ++j) {
+                        const int col = c * 4 + h * 2 + j;         // 16-byte column of the row
+                        const uint4 w = lds128(codes0 + s * kWideCodeBytes + r * 128 + ((col ^ (r & 7)) << 4));
+                        uint32_t m = kMinus8;
+                        if (zeros) {
+                            uint32_t z;
+                            const int g = (c * 128 + h * 64 + j * 32) / G;
+                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z)
+                                         : "r"(params0 + s * kParams + kBlockGroups * kWideRows * 2 + g * (kWideRows / 2) + r / 2));
+                            m = 0x43004300u + (z >> (r & 1) * 4 & 15u) * 0x00010001u;
+                        }
+                        codes_in_order(w.x, m, out + j * 16);
+                        codes_in_order(w.y, m, out + j * 16 + 4);
+                        codes_in_order(w.z, m, out + j * 16 + 8);
+                        codes_in_order(w.w, m, out + j * 16 + 12);
+                    }
+                    if (h == 0) {
+                        if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((i / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                        tc_fence_after();
+                    }
+                    tmem_st32(acol + h * 32, out);
                 }
-                const uint32_t b = ia % kWideA;
-                if (!mbar_wait(bar(a_empty[b]), ((ia / kWideA) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-                tc_fence_after();
-                tmem_st32(tmem + lane_base + kACol + b * 64 + half * 32, out);
+                if (!ok) break;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -258,33 +282,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(code_empty[s]));
-            a = an;
         }
         if (!ok && lane == 0) set_error(prm.err, LORA_DERR_TIMEOUT);
     } else {
         // ------------------------------------------------------------------ draining: a row, half of the columns
-        const int quad = warp & 3, half = (warp - 10) >> 2, r = quad * 32 + lane;
+        const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         WideAt a = wide_at(p, first);
-        uint32_t id = 0, ij = 0;
-        // the eight draining warps meet (bounded, as every wait); false on a timeout
+        uint32_t id = 0, ij = 0, ic = 0;
+        // the draining warps meet (bounded, as every wait); false on a timeout
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(join));
-            return mbar_wait(bar(join), ij++ & 1, kWaitLimitNs);
+            return mbar_wait_quiet(bar(join), ij++ & 1, kWaitLimitNs);
         };
-        auto scales = [&](const WideAt& a, int c, float (&s)[kGroups]) {
-            const W4Prob& pr = p.prob[a.prob];
-            const int row = a.tile * kWideRows + r;
-#pragma unroll
-            for (int i = 0; i < kGroups; ++i) {
-                const int g = (a.kb * kWideK + c * kWideChunk) / G + i;
-                s[i] = row < pr.N && g * G < pr.K
-                           ? __half2float(__ldg(reinterpret_cast<const __half*>(pr.scales) + (int64_t)g * pr.N + row)) : 0.f;
-            }
-        };
-        float snext[kGroups];
-        scales(a, 0, snext);
         for (int at = first; at < end && ok;) {
             const W4Prob& pr = p.prob[a.prob];
             const int row0 = a.tile * kWideRows;
@@ -293,49 +304,61 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
 #pragma unroll
             for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
             for (int u = at; u < stop && ok; ++u) {
-                const int n = wide_chunks(pr, a.kb);
-                WideAt an = a;
-                wide_next(p, an);
-                for (int c = 0; c < n && ok; ++c) {
-                    float s[kGroups];
+                const uint32_t st = ic % kCodeStages;
+                if (!mbar_wait_quiet(bar(code_full[st]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
 #pragma unroll
-                    for (int i = 0; i < kGroups; ++i) s[i] = snext[i];
-                    if (c + 1 < n) scales(a, c + 1, snext);
-                    else if (u + 1 < end) scales(an, 0, snext);
+                for (int c = 0; c < kBlockGroups / kSet; ++c, ++id) {
+                    float s[kSet];
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g, ++id) {
-                        if (!mbar_wait(bar(d_full[id & 1]), (id >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
-                        tc_fence_after();
+                    for (int i = 0; i < kSet; ++i) {
+                        unsigned short h;
+                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h)
+                                     : "r"(params0 + st * kParams + ((c * kSet + i) * kWideRows + r) * 2));
+                        s[i] = __half2float(__ushort_as_half(h));
+                    }
+                    if (!mbar_wait_quiet(bar(d_full[id % kDone]), (id / kDone) & 1, kWaitLimitNs)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int g = 0; g < kSet; ++g)
 #pragma unroll
                         for (int j = 0; j < kMine; j += 16) {
                             float v[16];
-                            tmem_ld16(tmem + lane_base + (id & 1) * N + half * kMine + j, v);
+                            tmem_ld16(tmem + lane_base + (id & 1) * kDCols + g * N + half * kMine + j, v);
                             tmem_ld_wait();
 #pragma unroll
                             for (int i = 0; i < 16; ++i) acc[j + i] = fmaf(s[g], v[i], acc[j + i]);
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(d_empty[id & 1]));
-                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(d_empty[id & 1]));
                 }
-                a = an;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(code_empty[st]));
+                wide_next(p, a);
+                ++ic;
             }
             if (!ok) break;
             // ---- the row tile's sums: y, or a part of them
             const bool whole = at == tile_first && stop == tile_end;
-            const bool in = row0 + r < pr.N;
-            // y[half of the columns][row], the pointer moved on column by column
+            // y's tile, [column][row of W], through shared memory and one bulk store (what lies
+            // outside y is not written).  False on a timeout.
             auto store = [&]() {
-                __nv_bfloat16* y = pr.y + half * kMine * pr.ldy + row0 + r;
+                if (tid == 12 * 32) bulk_wait_read0();             // the last store has left the buffer
+                if (!meet()) return false;
 #pragma unroll
-                for (int j = 0; j < kMine; ++j, y += pr.ldy) {
-                    if (j % 8 == 0) asm volatile("" : "+l"(y)::"memory");      // no 64 addresses at once
-                    if (in && half * kMine + j < p.T) *y = __float2bfloat16_rn(acc[j]);
+                for (int j = 0; j < kMine; ++j)
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(y0 + ((half * kMine + j) * kWideRows + r) * 2),
+                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(acc[j]))) : "memory");
+                fence_proxy_async_smem();
+                if (!meet()) return false;
+                if (tid == 12 * 32) {
+                    tma_store_2d(&prm.y[&pr - p.prob], row0, 0, y0);
+                    bulk_commit();
                 }
+                return true;
             };
             if (whole) {
-                store();
+                if (!(ok = store())) break;
             } else {
                 float* part = p.part + (((int64_t)blockIdx.x * 2 + (tile_first < first ? 0 : 1)) * N + half * kMine) * kWideRows + r;
 #pragma unroll
@@ -345,11 +368,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
                 const int c0 = tile_first / p.per, c1 = (tile_end - 1) / p.per;
                 __threadfence();
                 if (!(ok = meet())) break;
-                if (tid == 10 * 32) last_in = atomicAdd(&p.tickets[c0], 1u) == (uint32_t)(c1 - c0);
+                if (tid == 12 * 32) last_in = atomicAdd(&p.tickets[c0], 1u) == (uint32_t)(c1 - c0);
                 if (!(ok = meet())) break;
                 if (*reinterpret_cast<volatile uint32_t*>(&last_in)) {
                     __threadfence();
-                    if (tid == 10 * 32) p.tickets[c0] = 0;
+                    if (tid == 12 * 32) p.tickets[c0] = 0;
 #pragma unroll
                     for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
                     for (int c = c0; c <= c1; ++c) {
@@ -360,12 +383,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) w4_wide_kernel(const __grid_c
                             acc[j] += __ldcg(from + j * kWideRows);
                         }
                     }
-                    store();
+                    if (!(ok = store())) break;
                 }
                 if (!(ok = meet())) break;
             }
             at = stop;
         }
+        if (tid == 12 * 32) bulk_wait0();
         if (!ok && lane == 0) set_error(prm.err, LORA_DERR_TIMEOUT);
     }
     tc_fence_before();
