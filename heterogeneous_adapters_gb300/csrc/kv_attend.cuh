@@ -24,6 +24,8 @@
 // together from partial results in the workspace by the CTA that arrives last, in the order
 // of the parts, so the result does not depend on the order of arrival.
 #pragma once
+#include <type_traits>
+
 #include "kv_layout.cuh"
 #include "mma_legacy.cuh"
 #include "ptx.cuh"
@@ -294,8 +296,9 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             }
             const int tok0 = (st0 + me + way * i) * kAttStep;
             const bool has_a = have_a >> (i & 31) & 1, has_b = have_b >> (i & 31) & 1;
-            const bool masked = tok0 + kAttStep - 1 > low || !has_a || !has_b;
             const uint32_t base = wring + stage * kStage;
+            auto step = [&](auto some_masked) {
+            constexpr bool masked = decltype(some_masked)::value;
             // ---- S^T = K q^T
             float s[2][NT][4];
 #pragma unroll
@@ -355,20 +358,22 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             uint32_t pb[2][NT][kGroups][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float mn[2];
+                // the maximum moves only when some lane sees a larger score: a vote decides
+                // whether it is looked for across the lanes
+                float top[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]), fmaxf(s[1][n][j], s[1][n][2 + j]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    mn[j] = fmaxf(m[n][j], x);
-                }
-                if (__any_sync(0xffffffffu, mn[0] != m[n][0] || mn[1] != m[n][1])) {
+                for (int j = 0; j < 2; ++j)
+                    top[j] = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]), fmaxf(s[1][n][j], s[1][n][2 + j]));
+                if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float f = mn[j] == -INFINITY ? 1.f : exp2_approx((m[n][j] - mn[j]) * sl);
-                        m[n][j] = mn[j];
+                        float mn = top[j];
+                        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 4));
+                        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
+                        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
+                        mn = fmaxf(mn, m[n][j]);
+                        const float f = mn == -INFINITY ? 1.f : exp2_approx((m[n][j] - mn) * sl);
+                        m[n][j] = mn;
                         l[n][j] *= f;
 #pragma unroll
                         for (int gr = 0; gr < kGroups; ++gr) off[n][gr][j] *= f;
@@ -379,12 +384,12 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                         }
                     }
                 }
+                const float ms[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0] * sl, m[n][1] == -INFINITY ? 0.f : m[n][1] * sl};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float ms = m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1] * sl;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        s[h][n][j] = exp2_approx(fmaf(s[h][n][j], sl, -ms));
+                        s[h][n][j] = exp2_approx(fmaf(s[h][n][j], sl, -ms[j & 1]));
                         l[n][j & 1] += s[h][n][j];
                     }
                 }
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         vp[e].x = fmaxf(vp[e].x, kTinyScale);
-                        vp[e].y = __fdividef(vp[e].y, vp[e].x);     // offset in units of the scale
+                        vp[e].y *= rcp_approx(vp[e].x);             // offset in units of the scale
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -445,6 +450,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                         }
                     }
                 }
+            };
+            // most steps lie before the item's first row's token: nothing to mask
+            if (tok0 + kAttStep - 1 > low || !has_a || !has_b) step(std::true_type{});
+            else step(std::false_type{});
             __syncwarp();                               // every lane has read the stage
             if (i + kAttStages < mine_n) put(i + kAttStages, stage);
         }
