@@ -3,17 +3,22 @@
 //
 // For one request and KV head the query rows that share the head (the request's rows times
 // the query heads of the KV head) are the columns of a transposed product: with K and V as
-// codes c in -8 .. 7 (exact in bf16), a score is
+// codes c in -8 .. 7 (exact in f16), a score is
 //     q . k_t = sum over groups of  scale_t (q . c_t) + offset_t sum(q),
 // so the MMA runs on the codes as they are, S^T = C_K q^T (tokens x rows, 16 tokens a tile),
-// and the scale enters once per token in fp32.  The output is likewise
-//     O^T = C_V^T (scale_t p_t)  +  sum_t offset_t p_t,
-// scale_t p_t being the one value that is rounded to bf16 (2^-9 of a probability on average
-// adds less than the output's own rounding does).  ldmatrix hands each lane its words of
-// codes in the operand's order (transposed for V, which pairs the tokens), so a code costs
-// 11 / 8 instructions on its way to the tensor core.  The tokens being the long side of both
-// products, 8 rows fill an MMA; mma.sync serves because the kernel is bound by the bytes of
-// the cache (136 a token and head) and next by the unpacking, not by the MMAs.
+// and the scale enters once per token in fp32.  q goes in as f16 times a power of two that
+// puts a row's largest value at 2^13: its eight bits are kept for every value above 2^-27
+// of the largest.  The output is likewise
+//     O^T = C_V^T x  +  sum_t x_t (offset_t / scale_t),    x_t = f16(scale_t p_t),
+// where x_t is the one value that is rounded (2^-11 of itself) and both terms use it
+// rounded: the sum is over whole values v_t with weights off by that much, however large
+// scale and offset are against v_t.  p_t = 2^(score log2 e - M) has the reference M at the
+// largest scale_t p_t seen (x fits f16 whatever the scales), moved when an x exceeds 2^10.
+// ldmatrix hands each lane its words of codes in the operand's order (transposed for V,
+// which pairs the tokens), so a code costs 9 / 8 instructions on its way to the tensor core.
+// The tokens being the long side of both products, 8 rows fill an MMA; mma.sync serves
+// because the kernel is bound by the bytes of the cache (136 a token and head) and next by
+// the unpacking, not by the MMAs.
 //
 // Work.  An item is (request, KV head, tile of 8 NT packed rows), of ceil(tokens / 32) steps
 // and kAttItemCost more for its fixed part.  The units of all items in a row are dealt to
@@ -38,7 +43,12 @@ constexpr int kAttStep = 32;          // tokens of a step (two tiles)
 constexpr int kAttStages = 3;
 constexpr int kAttMaxCtas = kStepTickets;
 constexpr int kAttJoin = 8;           // parts of an item whose loads are in flight together
-constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40: stands for a scale of 0, below f16's smallest
+// A scale below 2^-14 of its offset stands as that, so that offset / scale stays in range: a
+// constant group's codes are 8, and otherwise the value is off by less than 2^-11 of itself.
+constexpr float kScaleOfOffset = 6.1035156e-5f;
+constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40
+constexpr float kMoveAbove = 1024.f;
+constexpr float kNoRef = -3e38f;               // M before the first token
 constexpr int kAttItemCost = 3;       // units of an item beside its steps
 constexpr int kAttMinUnits = 8;       // a CTA's range is at least this
 constexpr int kAttSolo = 8;           // an item of at most this many steps is one warp's
@@ -104,8 +114,18 @@ __device__ __forceinline__ void att_store(const AttendParams& p, int row, int hq
     uint2 w = make_uint2(pack2(x.x * f, x.y * f), pack2(x.z * f, x.w * f));
     *reinterpret_cast<uint2*>(p.out + row * p.ldo + (int64_t)hq * D + d) = w;
 }
-__device__ __forceinline__ void att_store_lse(const AttendParams& p, int row, int hq, float top, float sum) {
-    if (p.lse) p.lse[(int64_t)row * p.q_heads + hq] = top == -INFINITY ? -INFINITY : top * p.scale + logf(sum);
+// (scale, offset) of tokens g and g + 8 of a tile and group, at shared address `at` of the first.
+__device__ __forceinline__ void att_params(float2 (&k)[2], uint32_t at) {
+    uint32_t a, b;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a) : "r"(at));
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(b) : "r"(at + 32));
+    k[0] = __half22float2(*reinterpret_cast<__half2*>(&a));
+    k[1] = __half22float2(*reinterpret_cast<__half2*>(&b));
+}
+
+// ref: the reference M of the sum, in powers of two.
+__device__ __forceinline__ void att_store_lse(const AttendParams& p, int row, int hq, float ref, float sum) {
+    if (p.lse) p.lse[(int64_t)row * p.q_heads + hq] = sum == 0.f ? -INFINITY : ref * 0.693147181f + logf(sum);
 }
 
 template <int D, int G, int NT>
@@ -168,7 +188,6 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
     int seq = (int)(found[0] >> 32), head = (int)found[0], r0 = 0;
     int64_t item = found[1];                            // first unit of the item
     AttSeq q = att_seq(v, seq, false);
-    const float sl = p.scale * 1.44269504f;
     const uint32_t wring = smem_addr(ring) + warp * kAttStages * kStage;
     const uint32_t wbar = smem_addr(&bars[warp][0]);
     const int cap = (int)((int64_t)v.max_blocks * v.block_tokens);
@@ -232,9 +251,10 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
         };
         for (int i = 0; i < min(kAttStages, mine_n); ++i) put(i, (it + i) % kAttStages);
 
-        // ---- q as the right-hand operand, and its sums per group
+        // ---- q as the right-hand operand, and its sums per group, both times 2^13 over the
+        // power of two of the row's largest value; `sl` takes that out again
         uint32_t qb[NT][kChunks][4];
-        float qsum[NT][kGroups][2];
+        float qsum[NT][kGroups][2], sl[NT][2];
         int32_t last[NT][2];                            // last token of this lane's columns
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -242,20 +262,39 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             const bool live = n * 8 + g < width;
             const __nv_bfloat16* src = p.q + (int64_t)(cq.row0 + (live ? r / p.rep : 0)) * p.ldq +
                                        (int64_t)(cur_head * p.rep + (live ? r % p.rep : 0)) * D;
+            uint4 w[kChunks];
+            uint32_t big = 0;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                w[c] = live ? ld16(src + c * 32 + t * 8) : make_uint4(0, 0, 0, 0);
+                const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) big = max(big, max(x[j] << 16 & 0x7F800000u, x[j] & 0x7F800000u));
+            }
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // 2^(13 - e) and its inverse, the exponent e kept where both are normal
+            const int e = max(16, min((int)(big >> 23), 254)) - 127;
+            const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+            const float back = p.scale * 1.44269504f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+            sl[n][0] = __shfl_sync(0xffffffffu, back, t * 8);
+            sl[n][1] = __shfl_sync(0xffffffffu, back, t * 8 + 4);
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
                 float sum = 0.f;
 #pragma unroll
                 for (int c = gr * kPerG; c < (gr + 1) * kPerG; ++c) {
-                    const uint4 w = live ? ld16(src + c * 32 + t * 8) : make_uint4(0, 0, 0, 0);
-                    qb[n][c][0] = __byte_perm(w.x, w.z, 0x5410);
-                    qb[n][c][1] = __byte_perm(w.x, w.z, 0x7632);
-                    qb[n][c][2] = __byte_perm(w.y, w.w, 0x5410);
-                    qb[n][c][3] = __byte_perm(w.y, w.w, 0x7632);
                     float f[8];
-                    unpack8(w, f);
+                    unpack8(w[c], f);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum += f[j];
+                    for (int j = 0; j < 8; ++j) {
+                        f[j] *= up;
+                        sum += f[j];
+                    }
+                    qb[n][c][0] = pack_f16(f[0], f[4]);
+                    qb[n][c][1] = pack_f16(f[1], f[5]);
+                    qb[n][c][2] = pack_f16(f[2], f[6]);
+                    qb[n][c][3] = pack_f16(f[3], f[7]);
                 }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -277,7 +316,7 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             for (int i = 0; i < 2 * kChunks; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                m[n][j] = -INFINITY;
+                m[n][j] = kNoRef;
                 l[n][j] = 0.f;
 #pragma unroll
                 for (int gr = 0; gr < kGroups; ++gr) off[n][gr][j] = 0.f;
@@ -299,47 +338,42 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
             const uint32_t base = wring + stage * kStage;
             auto step = [&](auto some_masked) {
             constexpr bool masked = decltype(some_masked)::value;
-            // ---- S^T = K q^T
+            // ---- S^T = K q^T, both tiles side by side
             float s[2][NT][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t tb = base + h * kTile;
+            for (int gr = 0; gr < kGroups; ++gr) {
+                float acc[2][NT][4];
 #pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr) {
-                    float acc[NT][4];
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                    for (int n = 0; n < NT; ++n) acc[h][n][0] = acc[h][n][1] = acc[h][n][2] = acc[h][n][3] = 0.f;
 #pragma unroll
-                    for (int c = gr * kPerG; c < (gr + 1) * kPerG; ++c) {
-                        uint32_t w[2];
-                        asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];"
-                                     : "=r"(w[0]), "=r"(w[1])
-                                     : "r"(tb + c * 256 + (lane & 15) * 16)
-                                     : "memory");
-                        const uint32_t a0[4] = {code_pair<0>(w[0], kMinus8), code_pair<0>(w[1], kMinus8),
-                                                code_pair<1>(w[0], kMinus8), code_pair<1>(w[1], kMinus8)};
-                        const uint32_t a1[4] = {code_pair<2>(w[0], kMinus8), code_pair<2>(w[1], kMinus8),
-                                                code_pair<3>(w[0], kMinus8), code_pair<3>(w[1], kMinus8)};
+                for (int c = gr * kPerG; c < (gr + 1) * kPerG; ++c) {
+                    // the two tiles' words: lanes 0-15 address tile 0's rows, 16-31 tile 1's
+                    uint32_t w[4];
+                    ldmatrix4(w, base + (lane >> 4) * kTile + c * 256 + (lane & 15) * 16);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t a[4], b[4];
+                        codes_f16(w[2 * h], a);
+                        codes_f16(w[2 * h + 1], b);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            mma16816(acc[n], a0, qb[n][c][0], qb[n][c][1]);
-                            mma16816(acc[n], a1, qb[n][c][2], qb[n][c][3]);
+                            mma16816_f16(acc[h][n], a[0], b[0], a[1], b[1], qb[n][c][0], qb[n][c][1]);
+                            mma16816_f16(acc[h][n], a[2], b[2], a[3], b[3], qb[n][c][2], qb[n][c][3]);
                         }
                     }
-                    const uint32_t pa = tb + kv_params_at(D, G, 0) + gr * 64 + g * 4;
-                    uint32_t r0w, r1w;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r0w) : "r"(pa));
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r1w) : "r"(pa + 32));
-                    const float2 k0 = __half22float2(*reinterpret_cast<__half2*>(&r0w));
-                    const float2 k1 = __half22float2(*reinterpret_cast<__half2*>(&r1w));
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2 k[2];
+                    att_params(k, base + h * kTile + kv_params_at(D, G, 0) + gr * 64 + g * 4);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float a = fmaf(k0.x, acc[n][j], k0.y * qsum[n][gr][j]);
-                            const float b = fmaf(k1.x, acc[n][2 + j], k1.y * qsum[n][gr][j]);
+                        for (int j = 0; j < 4; ++j) {
+                            const float a = fmaf(k[j >> 1].x, acc[h][n][j], k[j >> 1].y * qsum[n][gr][j & 1]);
                             s[h][n][j] = gr ? s[h][n][j] + a : a;
-                            s[h][n][2 + j] = gr ? s[h][n][2 + j] + b : b;
                         }
                 }
             }
@@ -354,25 +388,59 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                             if (tok > last[n][j & 1] || !(h ? has_b : has_a)) s[h][n][j] = -INFINITY;
                         }
             }
-            // ---- running maximum, probabilities, sums
+            // ---- V's scales, and offsets in units of them
+            float2 vp[2][kGroups][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    att_params(vp[h][gr], base + h * kTile + kv_params_at(D, G, 1) + gr * 64 + g * 4);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float2& q = vp[h][gr][e];
+                        q.x = fmaxf(fmaxf(q.x, fabsf(q.y) * kScaleOfOffset), kTinyScale);
+                        q.y *= rcp_approx(q.x);
+                    }
+                }
+            // ---- probabilities, and with each group's scale the right-hand operand of V
             uint32_t pb[2][NT][kGroups][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                // the maximum moves only when some lane sees a larger score: a vote decides
-                // whether it is looked for across the lanes
-                float top[2];
+                float pr[2][4];
+                auto weigh = [&]() {
+                    float top = 0.f;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    top[j] = fmaxf(fmaxf(s[0][n][j], s[0][n][2 + j]), fmaxf(s[1][n][j], s[1][n][2 + j]));
-                if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            pr[h][j] = exp2_approx(fmaf(s[h][n][j], sl[n][j & 1], -m[n][j & 1]));
+#pragma unroll
+                            for (int gr = 0; gr < kGroups; ++gr) {
+                                float x = pr[h][j] * vp[h][gr][j >> 1].x;
+                                if (masked && pr[h][j] == 0.f) x = 0.f;      // a masked token's parameters may be anything
+                                top = fmaxf(top, x);
+                            }
+                        }
+                    return top;
+                };
+                if (__any_sync(0xffffffffu, weigh() > kMoveAbove)) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        float mn = top[j];
+                        float mn = m[n][j];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float sc = vp[h][0][e].x;
+#pragma unroll
+                                for (int gr = 1; gr < kGroups; ++gr) sc = fmaxf(sc, vp[h][gr][e].x);
+                                const float a = s[h][n][2 * e + j];
+                                if (!masked || a != -INFINITY) mn = fmaxf(mn, fmaf(a, sl[n][j], log2_approx(sc)));
+                            }
                         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 4));
                         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
                         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 16));
-                        mn = fmaxf(mn, m[n][j]);
-                        const float f = mn == -INFINITY ? 1.f : exp2_approx((m[n][j] - mn) * sl);
+                        const float f = exp2_approx(m[n][j] - mn);
                         m[n][j] = mn;
                         l[n][j] *= f;
 #pragma unroll
@@ -383,51 +451,30 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                             o[n][k][2 + j] *= f;
                         }
                     }
+                    weigh();
                 }
-                const float ms[2] = {m[n][0] == -INFINITY ? 0.f : m[n][0] * sl, m[n][1] == -INFINITY ? 0.f : m[n][1] * sl};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        s[h][n][j] = exp2_approx(fmaf(s[h][n][j], sl, -ms[j & 1]));
-                        l[n][j & 1] += s[h][n][j];
-                    }
-                }
-            }
-            // ---- V's scale and offset enter the probabilities of each group
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr) {
-                    const uint32_t pa = base + h * kTile + kv_params_at(D, G, 1) + gr * 64 + g * 4;
-                    uint32_t r0w, r1w;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r0w) : "r"(pa));
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r1w) : "r"(pa + 32));
-                    float2 vp[2] = {__half22float2(*reinterpret_cast<__half2*>(&r0w)),
-                                    __half22float2(*reinterpret_cast<__half2*>(&r1w))};
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        vp[e].x = fmaxf(vp[e].x, kTinyScale);
-                        vp[e].y *= rcp_approx(vp[e].x);             // offset in units of the scale
-                    }
+                        l[n][0] += pr[h][2 * e];
+                        l[n][1] += pr[h][2 * e + 1];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
+                        for (int gr = 0; gr < kGroups; ++gr) {
                             float x[2];
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                x[j] = s[h][n][2 * e + j] * vp[e].x;
-                                if (masked && s[h][n][2 * e + j] == 0.f) x[j] = 0.f;   // its parameters may be anything
+                                x[j] = pr[h][2 * e + j] * vp[h][gr][e].x;
+                                if (masked && pr[h][2 * e + j] == 0.f) x[j] = 0.f;
                             }
-                            const uint32_t w = pack2(x[0], x[1]);
-                            const float of[2] = {bf16lo(w), bf16hi(w)};
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                if (!masked || of[j] != 0.f) off[n][gr][j] = fmaf(of[j], vp[e].y, off[n][gr][j]);
+                            const uint32_t w = pack_f16(x[0], x[1]);
+                            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                            if (!masked || r.x != 0.f) off[n][gr][0] = fmaf(r.x, vp[h][gr][e].y, off[n][gr][0]);
+                            if (!masked || r.y != 0.f) off[n][gr][1] = fmaf(r.y, vp[h][gr][e].y, off[n][gr][1]);
                             pb[h][n][gr][e] = movmatrix_trans(w);
                         }
-                }
+                    }
+            }
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -437,16 +484,14 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                     ldmatrix4_trans(w, base + h * kTile + kv_codes_at(D, 1) + c * 256 + lane * 16);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t w0 = w[2 * e], w1 = w[2 * e + 1];
-                        const uint32_t a0[4] = {code_pair<0>(w0, kMinus8), code_pair<1>(w0, kMinus8),
-                                                code_pair<0>(w1, kMinus8), code_pair<1>(w1, kMinus8)};
-                        const uint32_t a1[4] = {code_pair<2>(w0, kMinus8), code_pair<3>(w0, kMinus8),
-                                                code_pair<2>(w1, kMinus8), code_pair<3>(w1, kMinus8)};
+                        uint32_t a[4], b[4];
+                        codes_f16(w[2 * e], a);
+                        codes_f16(w[2 * e + 1], b);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const int gr = (c + e) / kPerG;
-                            mma16816(o[n][2 * (c + e)], a0, pb[h][n][gr][0], pb[h][n][gr][1]);
-                            mma16816(o[n][2 * (c + e) + 1], a1, pb[h][n][gr][0], pb[h][n][gr][1]);
+                            mma16816_f16(o[n][2 * (c + e)], a[0], a[1], b[0], b[1], pb[h][n][gr][0], pb[h][n][gr][1]);
+                            mma16816_f16(o[n][2 * (c + e) + 1], a[2], a[3], b[2], b[3], pb[h][n][gr][0], pb[h][n][gr][1]);
                         }
                     }
                 }
@@ -505,14 +550,14 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
         float* part = p.part + ((int64_t)blockIdx.x * 2 + (body < first ? 0 : 1)) * kRows * kPitch;
         for (int e = tid; e < width * (D / 4); e += kAttThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
-            float top = -INFINITY;
+            float top = kNoRef;
 #pragma unroll
             for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, stat[w][r][0]);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kAttWarps; ++w) {
-                const float f = top == -INFINITY ? 0.f : exp2_approx((stat[w][r][0] - top) * sl);
+                const float f = exp2_approx(stat[w][r][0] - top);
                 const float4 x = *reinterpret_cast<const float4*>(ring + w * kAttStages * kStage + (r * D + d) * 4);
                 acc.x += f * x.x;
                 acc.y += f * x.y;
@@ -545,14 +590,14 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                 };
                 for (int e = tid; e < width * (D / 4); e += kAttThreads) {
                     const int r = e / (D / 4), d = e % (D / 4) * 4;
-                    float top = -INFINITY, sum = 0.f;
+                    float top = kNoRef, sum = 0.f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     for (int i0 = 0; i0 < n; i0 += kAttJoin) {  // kAttJoin parts' loads in flight
                         float2 ms[kAttJoin];
                         float4 x[kAttJoin];
 #pragma unroll
                         for (int i = 0; i < kAttJoin; ++i) {
-                            ms[i] = make_float2(-INFINITY, 0.f);
+                            ms[i] = make_float2(kNoRef, 0.f);
                             x[i] = acc;
                             if (i0 + i < n) {
                                 const float* from = src(i0 + i) + r * kPitch;
@@ -563,14 +608,14 @@ __global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel
                         float mn = top;
 #pragma unroll
                         for (int i = 0; i < kAttJoin; ++i) mn = fmaxf(mn, ms[i].x);
-                        const float f0 = mn == -INFINITY ? 0.f : exp2_approx((top - mn) * sl);
+                        const float f0 = exp2_approx(top - mn);
                         acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
                         sum *= f0;
                         top = mn;
 #pragma unroll
                         for (int i = 0; i < kAttJoin; ++i) {
                             if (i0 + i >= n) continue;
-                            const float f = mn == -INFINITY ? 0.f : exp2_approx((ms[i].x - mn) * sl);
+                            const float f = exp2_approx(ms[i].x - mn);
                             acc.x += f * x[i].x;
                             acc.y += f * x[i].y;
                             acc.z += f * x[i].z;
