@@ -40,8 +40,23 @@ namespace lora {
 constexpr int kAttWarps = 4;
 constexpr int kAttThreads = kAttWarps * 32;
 constexpr int kAttStep = 32;          // tokens of a step (two tiles)
-constexpr int kAttStages = 3;
+constexpr int kAttStages = 2;
 constexpr int kAttMaxCtas = kStepTickets;
+constexpr int kAttJoin = 8;           // parts of an item whose loads are in flight together
+// A scale below 2^-14 of its offset stands as that, so that offset / scale stays in range: a
+// constant group's codes are 8, and otherwise the value is off by less than 2^-11 of itself.
+constexpr float kScaleOfOffset = 6.1035156e-5f;
+constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40
+constexpr float kMoveAbove = 1024.f;
+constexpr float kNoRef = -3e38f;               // M before the first token
+// Units of an item beside its steps: what finding it, its first copies and its merge cost.
+// 64 requests of 17 to 8191 tokens: 79 / 72 / 68 / 65 / 65 / 70 us at 3 / 6 / 8 / 14 / 18 / 32
+// (two 131k contexts do not care: 67 / 68 / 66 / 65 / 65 / 65).
+constexpr int kAttItemCost = 16;
+constexpr int kAttMinUnits = 8;       // a CTA's range is at least this
+// An item of at most this many steps is one warp's: 256 requests of 50 to 300 tokens 40 us at
+// 8 and 36 at 12, 48 requests of 33 to 4095 tokens and up to 5 rows 26 at 8 and 29 at 12.
+constexpr int kAttSolo = 10;
 constexpr int kAttJoin = 8;           // parts of an item whose loads are in flight together
 // A scale below 2^-14 of its offset stands as that, so that offset / scale stays in range: a
 // constant group's codes are 8, and otherwise the value is off by less than 2^-11 of itself.
@@ -68,6 +83,8 @@ struct AttendParams {
 __host__ __device__ constexpr size_t attend_smem(int dim, int group) {
     return (size_t)kAttWarps * kAttStages * 2 * kv_tile_bytes(dim, group);
 }
+// CTAs of an SM that the registers are shared out for.
+__host__ __device__ constexpr int attend_ctas(int dim, int nt) { return nt == 1 ? 4 : dim == 128 ? 2 : 3; }
 // Bytes of workspace: header, tickets and partial results.
 __host__ __device__ constexpr size_t attend_part_floats(int nt, int dim) { return (size_t)2 * 8 * nt * (dim + 4); }
 __host__ __device__ constexpr size_t attend_workspace(int nt, int dim) {
@@ -129,7 +146,7 @@ __device__ __forceinline__ void att_store_lse(const AttendParams& p, int row, in
 }
 
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kAttThreads, NT == 1 ? 4 : 2) kv_attend_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kRows = 8 * NT, kChunks = D / 32, kGroups = D / G, kPerG = G / 32;
     constexpr int kTile = kv_tile_bytes(D, G), kStage = 2 * kTile, kPitch = D + 4;
     extern __shared__ __align__(128) unsigned char ring[];
