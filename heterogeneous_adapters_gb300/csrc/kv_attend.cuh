@@ -57,16 +57,6 @@ constexpr int kAttMinUnits = 8;       // a CTA's range is at least this
 // An item of at most this many steps is one warp's: 256 requests of 50 to 300 tokens 40 us at
 // 8 and 36 at 12, 48 requests of 33 to 4095 tokens and up to 5 rows 26 at 8 and 29 at 12.
 constexpr int kAttSolo = 10;
-constexpr int kAttJoin = 8;           // parts of an item whose loads are in flight together
-// A scale below 2^-14 of its offset stands as that, so that offset / scale stays in range: a
-// constant group's codes are 8, and otherwise the value is off by less than 2^-11 of itself.
-constexpr float kScaleOfOffset = 6.1035156e-5f;
-constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40
-constexpr float kMoveAbove = 1024.f;
-constexpr float kNoRef = -3e38f;               // M before the first token
-constexpr int kAttItemCost = 3;       // units of an item beside its steps
-constexpr int kAttMinUnits = 8;       // a CTA's range is at least this
-constexpr int kAttSolo = 8;           // an item of at most this many steps is one warp's
 
 struct AttendParams {
     KvView v;
