@@ -97,23 +97,76 @@ __device__ __forceinline__ AttSeq att_seq(const KvView& v, int s, bool report) {
     if (err) q.rows = 0;
     const int64_t cap = (int64_t)v.max_blocks * v.block_tokens;
     if (q.rows > 0 && len > cap) err = LORA_DERR_KV;
+    if (q.rows < v.rows_lo || q.rows > v.rows_hi) q.rows = 0;
     q.len = len;
     if (report && err) set_error(v.err, err);
     return q;
 }
 
-// Steps of the tile of packed rows [r0, r0 + width) of a request: enough for the last row.
+// Steps (of Step tokens) of the tile of packed rows [r0, r0 + width) of a request: enough for
+// the last row.
+template <int Step>
 __device__ __forceinline__ int att_steps(const KvView& v, const AttSeq& q, int rep, int r0, int width) {
     const int i = (min(r0 + width, q.rows * rep) - 1) / rep;
     const int64_t tokens = min((int64_t)q.len - q.rows + i + 1, (int64_t)v.max_blocks * v.block_tokens);
-    return tokens <= 0 ? 1 : (int)((tokens + kAttStep - 1) / kAttStep);
+    return tokens <= 0 ? 1 : (int)((tokens + Step - 1) / Step);
 }
 
-// Units of one KV head of a request.
-__device__ __forceinline__ int64_t att_head_units(const KvView& v, const AttSeq& q, int rep, int width) {
+// Units of one KV head of a request: its items' steps and fixed parts.
+template <int Step, int Width, int Cost>
+__device__ __forceinline__ int64_t att_head_units(const KvView& v, const AttSeq& q, int rep) {
     int64_t n = 0;
-    for (int r0 = 0; r0 < q.rows * rep; r0 += width) n += att_steps(v, q, rep, r0, width) + kAttItemCost;
+    for (int r0 = 0; r0 < q.rows * rep; r0 += Width) n += att_steps<Step>(v, q, rep, r0, Width) + Cost;
     return n;
+}
+
+// The deal, by all threads of a CTA: the units before each request by a scan over the
+// requests, and of them this CTA's range [first, end) of `per` units; false if it is empty.
+// found: request and KV head that hold the first unit, and the units before that head.
+template <int Threads, int Step, int Width, int Cost, int MinUnits>
+__device__ __forceinline__ bool att_deal(const KvView& v, int rep, int64_t* scan, int64_t* found, int64_t& per, int64_t& first,
+                                         int64_t& end) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int chunk = (v.n_seq + Threads - 1) / Threads;
+    const int s_lo = min(tid * chunk, v.n_seq), s_hi = min(s_lo + chunk, v.n_seq);
+    int64_t mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) mine += v.heads * att_head_units<Step, Width, Cost>(v, att_seq(v, s, blockIdx.x == 0), rep);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t n = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += n;
+    }
+    if (lane == 31) scan[warp + 1] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < Threads / 32; ++w) {
+        if (w < warp) before += scan[w + 1];
+        total += scan[w + 1];
+    }
+    per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)MinUnits);
+    first = per * blockIdx.x;
+    end = min(first + per, total);
+    if (first >= end) return false;
+    if (before <= first && first < before + mine) {   // this thread's requests hold the first unit
+        int s = s_lo;
+        int64_t n;
+        for (;; ++s) {
+            n = att_head_units<Step, Width, Cost>(v, att_seq(v, s, false), rep);
+            if (first < before + v.heads * n) break;
+            before += v.heads * n;
+        }
+        int head = 0;
+        while (first >= before + n) {
+            before += n;
+            ++head;
+        }
+        found[0] = (int64_t)s << 32 | head;
+        found[1] = before;
+    }
+    __syncthreads();
+    return true;
 }
 
 __device__ __forceinline__ void att_store(const AttendParams& p, int row, int hq, int D, int d, float4 x, float sum) {
@@ -150,48 +203,8 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
     if (tid < kAttWarps * kAttStages) mbar_init(smem_addr(&bars[0][0]) + tid * 8, 1);
     fence_mbar_init();
 
-    // ---- the schedule: the units before each request, by a scan over the requests
-    const int chunk = (v.n_seq + kAttThreads - 1) / kAttThreads;
-    const int s_lo = min(tid * chunk, v.n_seq), s_hi = min(s_lo + chunk, v.n_seq);
-    int64_t mine = 0;
-    for (int s = s_lo; s < s_hi; ++s)
-        mine += v.heads * att_head_units(v, att_seq(v, s, blockIdx.x == 0), p.rep, kRows);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t n = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += n;
-    }
-    if (lane == 31) scan[warp + 1] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttWarps; ++w) {
-        if (w < warp) before += scan[w + 1];
-        total += scan[w + 1];
-    }
-    const int64_t per = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kAttMinUnits);
-    const int64_t first = per * blockIdx.x, end = min(first + per, total);
-    if (first >= end) return;
-    if (before <= first && first < before + mine) {   // this thread's requests hold the first unit
-        int s = s_lo;
-        AttSeq q;
-        int64_t n;
-        for (;; ++s) {
-            q = att_seq(v, s, false);
-            n = att_head_units(v, q, p.rep, kRows);
-            if (first < before + v.heads * n) break;
-            before += v.heads * n;
-        }
-        int head = 0;
-        while (first >= before + n) {
-            before += n;
-            ++head;
-        }
-        found[0] = (int64_t)s << 32 | head;
-        found[1] = before;                              // units before the head
-    }
-    __syncthreads();
+    int64_t per, first, end;
+    if (!att_deal<kAttThreads, kAttStep, kRows, kAttItemCost, kAttMinUnits>(v, p.rep, scan, found, per, first, end)) return;
     int seq = (int)(found[0] >> 32), head = (int)found[0], r0 = 0;
     int64_t item = found[1];                            // first unit of the item
     AttSeq q = att_seq(v, seq, false);
@@ -204,7 +217,7 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
 
     while (item < end) {
         // ---- the item (seq, head, r0) and this CTA's steps of it
-        const int steps = att_steps(v, q, p.rep, r0, kRows);
+        const int steps = att_steps<kAttStep>(v, q, p.rep, r0, kRows);
         const int64_t body = item + kAttItemCost;
         const int cur_seq = seq, cur_head = head, cur_r0 = r0;
         const AttSeq cq = q;

@@ -31,6 +31,7 @@ struct KvView {
     int32_t T;
     int32_t max_blocks;
     int32_t max_q;
+    int32_t rows_lo, rows_hi;   // requests with rows_lo .. rows_hi rows are this launch's (attention)
     uint32_t* err;
 };
 

@@ -1,0 +1,533 @@
+// Causal attention over the 4-bit cache for many rows per request (chunks of prompts), on the
+// fifth-generation tensor cores; one scale per head vector (group = head_dim).
+//
+// A tile is 128 packed rows (rows times query heads of one KV head) of one request; a block is
+// 128 tokens.  As in kv_attend.cuh the products run on the codes: with q in bf16 and c in
+// -8 .. 7,
+//     S = q C_K^T (128 x 128, tensor memory),   t = S k_t + kq_t sum(q) - M,   p = 2^t,
+// where k_t and kq_t are the token's K scale and offset times softmax_scale log2 e; then
+//     O += X C_V,   X = f16(p v_t),   and   E += X r_t,   r_t = V offset / V scale,
+// X from tensor memory, C_V in f16, and r in two f16 columns (r = hi + lo), so that the offsets
+// cost no work per element.  The output is (O + E) / sum p.  The reference M is moved, and O
+// and E multiplied, only when a p v_t exceeds 2^10.
+//
+// Warps 0-3 hold a row a thread: they bring q, turn S into X and write the output.  Warps 4-11
+// unpack a block's codes into the operands' swizzled rows (within eight values in the order
+// 0 4 1 5 2 6 3 7, q alike, and the output put back).  Warp 12 issues the MMAs, S of the next
+// block before X C_V of this one; warp 13 brings the codes.  A block costs 1024 clocks of MMA
+// and as many of exponentials.  Tiles are dealt, split and joined as kv_attend.cuh's items.
+#pragma once
+#include "kv_attend.cuh"
+
+namespace lora {
+
+constexpr int kPreRows = 128, kPreStep = 128, kPreThreads = 14 * 32;
+constexpr int kPreItemCost = 3;      // blocks' worth of a tile's fixed part
+constexpr int kPreMinUnits = 4;
+constexpr int kPreMaxCtas = 192;
+// A request's packed rows per KV head from which this kernel serves it.
+constexpr int kPreMinPacked = 48;
+
+__host__ __device__ constexpr int pre_code_bytes(int dim) { return kPreStep / kKvTile * kv_tile_bytes(dim, dim); }
+struct PreSmem {
+    int q, k, v, ext, codes, table, mask, total;
+};
+__host__ __device__ constexpr PreSmem pre_smem(int dim) {
+    PreSmem L{};
+    int o = 0;
+    L.q = o;      o += kPreRows * dim * 2;
+    L.k = o;      o += 2 * kPreStep * dim * 2;
+    L.v = o;      o += 2 * kPreStep * dim * 2;
+    L.ext = o;    o += 2 * 4096;                     // [2 x 64 tokens][16 rows][128 bytes]: r hi, r lo, zeros
+    L.codes = o;  o += 2 * pre_code_bytes(dim);
+    L.table = o;  o += 4 * kPreStep * 16;            // (k, kq, v) of a block's tokens
+    L.mask = o;   o += 16;
+    L.total = o + 1024;
+    return L;
+}
+__host__ __device__ constexpr size_t pre_workspace(int dim) {
+    return kStepPartAt + (size_t)kPreMaxCtas * 2 * kPreRows * (dim + 2) * 4;
+}
+
+// kind::f16 with f16 operands: idesc_bf16 without its two type bits.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
+    return idesc_bf16(m, n, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Walks the parts of tiles in a CTA's range, the same for every role.
+struct PrePart {
+    AttSeq q;
+    int seq, head, r0, width, st0, st1, steps;
+    int64_t body;
+    __device__ __forceinline__ bool whole() const { return st0 == 0 && st1 == steps; }
+};
+struct PreWalk {
+    int64_t item, first, end;
+    int seq, head, r0;
+    AttSeq q;
+    // the next part; false at the end of the range
+    __device__ __forceinline__ bool next(const KvView& v, int rep, PrePart& c) {
+        while (item < end) {
+            c.q = q;
+            c.seq = seq;
+            c.head = head;
+            c.r0 = r0;
+            c.steps = att_steps<kPreStep>(v, q, rep, r0, kPreRows);
+            c.width = min(kPreRows, q.rows * rep - r0);
+            c.body = item + kPreItemCost;
+            c.st0 = (int)max(first - c.body, (int64_t)0);
+            c.st1 = (int)min(max(end - c.body, (int64_t)0), (int64_t)c.steps);
+            item = c.body + c.steps;
+            r0 += kPreRows;
+            if (r0 >= q.rows * rep) {
+                r0 = 0;
+                if (++head == v.heads) {
+                    head = 0;
+                    do q = att_seq(v, min(++seq, v.n_seq - 1), false);
+                    while (seq < v.n_seq && q.rows == 0);
+                }
+            }
+            if (c.st1 > c.st0) return true;
+        }
+        return false;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid_constant__ AttendParams p) {
+    constexpr int kTile = kv_tile_bytes(D, D), kHalves = D / 64;
+    constexpr PreSmem L = pre_smem(D);
+    constexpr uint32_t kSCol = 0, kOCol = 256, kXCol = 384, kECol = 448;    // S twice, O, X, E
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t code_full[2], code_empty[2], k_full[2], v_full[2], v_empty[2], s_full[2], s_empty[2],
+        x_full, q_full, o_empty, join, final_bar;
+    __shared__ int64_t scan[kPreThreads / 32 + 1], found[2];
+    __shared__ uint32_t tmem_slot, last_in;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const KvView& v = p.v;
+    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sm = smem_addr(base);
+    auto bar = [](uint64_t& b) { return smem_addr(&b); };
+
+    PreWalk walk;
+    int64_t per;
+    if (!att_deal<kPreThreads, kPreStep, kPreRows, kPreItemCost, kPreMinUnits>(v, p.rep, scan, found, per, walk.first, walk.end)) return;
+    walk.seq = (int)(found[0] >> 32);
+    walk.head = (int)found[0];
+    walk.r0 = 0;
+    walk.item = found[1];
+    walk.q = att_seq(v, walk.seq, false);
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(code_full[i]), 1);
+            mbar_init(bar(code_empty[i]), 8);
+            mbar_init(bar(k_full[i]), 8);
+            mbar_init(bar(v_full[i]), 8);
+            mbar_init(bar(v_empty[i]), 1);
+            mbar_init(bar(s_full[i]), 1);
+            mbar_init(bar(s_empty[i]), 4);
+        }
+        mbar_init(bar(x_full), 4);
+        mbar_init(bar(q_full), 4);
+        mbar_init(bar(o_empty), 4);
+        mbar_init(bar(join), 4);
+        mbar_init(bar(final_bar), 1);
+        fence_mbar_init();
+    }
+    for (int i = tid; i < 2 * 4096 / 16; i += kPreThreads) sts128(sm + L.ext + i * 16, 0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 12) {
+        tmem_alloc(smem_addr(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+    bool ok = true;
+    PrePart c;
+    uint32_t n = 0;              // blocks so far: n % 2 is the buffer, n / 2 the phase
+
+    if (warp < 4) {
+        // ------------------------------------------------------------------ rows
+        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+        uint32_t ij = 0;
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(join));
+            return mbar_wait_quiet(bar(join), ij++ & 1, kWaitLimitNs);
+        };
+        const int cap = (int)((int64_t)v.max_blocks * v.block_tokens);
+        while (ok && walk.next(v, p.rep, c)) {
+            // ---- q into its swizzled rows (every S of the part before is done), and its sum
+            const int pr = c.r0 + tid, row = c.q.row0 + pr / p.rep, hq = c.head * p.rep + pr % p.rep;
+            const bool live = tid < c.width;
+            const int lead = c.q.len - c.q.rows, low = lead + c.r0 / p.rep;
+            const int last = live ? min(lead + pr / p.rep, cap - 1) : -1;
+            float qs = 0.f;
+            const __nv_bfloat16* src = p.q + (int64_t)row * p.ldq + (int64_t)hq * D;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 w = live ? ld16(src + i * 8) : make_uint4(0, 0, 0, 0);
+                float f[8];
+                unpack8(w, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) qs += f[j];
+                sts128(sm + L.q + (i / 8) * (kPreRows * 128) + tid * 128 + ((i % 8 ^ (tid & 7)) << 4), __byte_perm(w.x, w.z, 0x5410),
+                       __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(q_full));
+            float m = kNoRef, l = 0.f;
+            for (int st = c.st0; st < c.st1; ++st, ++n) {
+                const uint32_t b = n & 1, sb = lanes + kSCol + b * 128;
+                const float4* table = reinterpret_cast<const float4*>(base + L.table) + (n & 3) * kPreStep;
+                const int tok0 = st * kPreStep;
+                if (!mbar_wait_quiet(bar(k_full[b]), (n >> 1) & 1, kWaitLimitNs) ||
+                    !mbar_wait_quiet(bar(s_full[b]), (n >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
+                tc_fence_after();
+                // causal, or with tiles absent (the table's fourth number: 1, and 2 more at its
+                // head); the same for every row of the tile
+                const bool masked = tok0 + kPreStep - 1 > low || table[0].w >= 2.f;
+                // the scores' exponents of 32 tokens
+                auto exponents = [&](int j0, float (&t)[32], float ref) {
+                    tmem_ld32(sb + j0, t);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float4 k = table[j0 + j];
+                        t[j] = fmaf(k.x, t[j], fmaf(k.y, qs, -ref));
+                        if (masked && (tok0 + j0 + j > last || k.w == 1.f || k.w == 3.f)) t[j] = -INFINITY;
+                    }
+                };
+                // the reference at the largest p v_t of this block, if that is larger
+                auto move = [&]() {
+                    float mn = m;
+                    for (int j0 = 0; j0 < kPreStep; j0 += 32) {
+                        float t[32];
+                        exponents(j0, t, 0.f);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (t[j] != -INFINITY) mn = fmaxf(mn, t[j] + log2_approx(table[j0 + j].z));
+                    }
+                    const float f = exp2_approx(m - mn);
+                    m = mn;
+                    l *= f;
+                    return f;
+                };
+                bool first = st == c.st0;
+                if (first) move();
+                for (;;) {
+                    float top = 0.f, sum = 0.f;
+                    bool waited = false;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < kPreStep; j0 += 32) {
+                        float t[32];
+                        exponents(j0, t, m);
+                        uint32_t x[16];
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float p0 = exp2_approx(t[j]), p1 = exp2_approx(t[j + 1]);
+                            sum += p0 + p1;
+                            float x0 = p0 * table[j0 + j].z, x1 = p1 * table[j0 + j + 1].z;
+                            if (masked && p0 == 0.f) x0 = 0.f;         // a masked token's scale may be NaN
+                            if (masked && p1 == 0.f) x1 = 0.f;
+                            top = fmaxf(top, fmaxf(x0, x1));
+                            x[j / 2] = pack_f16(x0, x1);
+                        }
+                        // X is free once the last block's X C_V is done
+                        if (!waited && n > 0 && !mbar_wait_quiet(bar(v_empty[b ^ 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
+                        if (!waited) tc_fence_after();
+                        waited = true;
+                        tmem_st16(lanes + kXCol + j0 / 2, x);
+                    }
+                    if (!ok) break;
+                    if (!__any_sync(0xffffffffu, top > kMoveAbove)) {
+                        l += sum;
+                        break;
+                    }
+                    // ---- a new reference: O and E (complete, see the wait above) follow
+                    const float f = move();
+                    if (!first) {
+                        tmem_st_wait();
+                        for (int j0 = 0; j0 < D; j0 += 16) {
+                            float o[16];
+                            uint32_t w[16];
+                            tmem_ld16(lanes + kOCol + j0, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * f);
+                            tmem_st16(lanes + kOCol + j0, w);
+                        }
+                        float o[16];
+                        uint32_t w[16];
+                        tmem_ld16(lanes + kECol, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * f);
+                        tmem_st16(lanes + kECol, w);
+                    }
+                }
+                if (!ok) break;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(s_empty[b]));
+                    mbar_arrive(bar(x_full));
+                }
+            }
+            if (!ok) break;
+            // ---- the part's sums
+            if (!mbar_wait_quiet(bar(v_empty[(n - 1) & 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
+            tc_fence_after();
+            float e[16];
+            tmem_ld16(lanes + kECol, e);
+            tmem_ld_wait();
+            const float off = e[0] + e[1];
+            const bool whole = c.whole();
+            // 32 values of the row (eight by eight in the operands' order) to the output
+            auto store = [&](int j0, const float (&o)[32], float f) {
+                __nv_bfloat16* dst = p.out + (int64_t)row * p.ldo + (int64_t)hq * D + j0;
+#pragma unroll
+                for (int i = 0; i < 32; i += 8)
+                    if (live)
+                        st16(dst + i, make_uint4(pack2(o[i] * f, o[i + 2] * f), pack2(o[i + 4] * f, o[i + 6] * f),
+                                                 pack2(o[i + 1] * f, o[i + 3] * f), pack2(o[i + 5] * f, o[i + 7] * f)));
+            };
+            const int slot = c.body < walk.first ? 0 : 1;
+            float* part = p.part + ((int64_t)blockIdx.x * 2 + slot) * kPreRows * (D + 2) + tid;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            for (int j0 = 0; j0 < D; j0 += 32) {
+                float o[32];
+                tmem_ld32(lanes + kOCol + j0, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] += off;
+                if (whole) {
+                    store(j0, o, inv);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) part[(j0 + j) * kPreRows] = o[j];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(o_empty));
+            if (whole) {
+                if (live) att_store_lse(p, row, hq, m, l);
+                continue;
+            }
+            part[D * kPreRows] = m;
+            part[(D + 1) * kPreRows] = l;
+            const int64_t c0 = c.body / per, c1 = (c.body + c.steps - 1) / per;
+            __threadfence();
+            if (!(ok = meet())) break;
+            if (tid == 0) last_in = atomicAdd(&p.tickets[c0], 1u) == (uint32_t)(c1 - c0);
+            if (!(ok = meet())) break;
+            if (*reinterpret_cast<volatile uint32_t*>(&last_in)) {
+                __threadfence();
+                if (tid == 0) p.tickets[c0] = 0;
+                auto from = [&](int64_t i) {
+                    return p.part + (i * 2 + (c.body < i * per ? 0 : 1)) * kPreRows * (D + 2) + tid;
+                };
+                m = kNoRef;
+                for (int64_t i = c0; i <= c1; ++i) m = fmaxf(m, __ldcg(from(i) + D * kPreRows));
+                l = 0.f;
+                for (int64_t i = c0; i <= c1; ++i)
+                    l += __ldcg(from(i) + (D + 1) * kPreRows) * exp2_approx(__ldcg(from(i) + D * kPreRows) - m);
+                const float f = l != 0.f ? 1.f / l : 0.f;
+                for (int j0 = 0; j0 < D; j0 += 32) {
+                    float o[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                    for (int64_t i = c0; i <= c1; ++i) {
+                        const float* s = from(i) + j0 * kPreRows;
+                        const float w = exp2_approx(__ldcg(from(i) + D * kPreRows) - m);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = fmaf(w, __ldcg(s + j * kPreRows), o[j]);
+                    }
+                    store(j0, o, f);
+                }
+                if (live) att_store_lse(p, row, hq, m, l);
+            }
+            if (!(ok = meet())) break;
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------------ unpacking: a token, half of its values
+        const int tok = tid & 127, half = (tid - 128) >> 7;
+        const float sl = p.scale * 1.44269504f;
+        while (ok && walk.next(v, p.rep, c)) {
+            for (int st = c.st0; st < c.st1; ++st, ++n) {
+                const uint32_t b = n & 1, ph = (n >> 1) & 1;
+                if (!mbar_wait_quiet(bar(code_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
+                const uint32_t src = sm + L.codes + b * pre_code_bytes(D) + (tok / kKvTile) * kTile;
+                const uint32_t at = src + (tok % kKvTile) * 16;
+                // the buffer's last S is done (and with it the rows' use of the table four blocks ago)
+                if (!mbar_wait_quiet(bar(s_full[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
+                // K: 16-byte pieces of 32 values; a row of 64 values is 128 bytes, swizzled
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const int chunk = half * (D / 64) + i;
+                    const uint4 w4 = lds128(at + chunk * 256);
+                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    const uint32_t dst = sm + L.k + b * (kPreStep * D * 2) + (chunk / 2) * (kPreStep * 128) + tok * 128;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sts128(dst + (((chunk % 2 * 4 + j) ^ (tok & 7)) << 4), code_pair<0>(w[j], kMinus8), code_pair<1>(w[j], kMinus8),
+                               code_pair<2>(w[j], kMinus8), code_pair<3>(w[j], kMinus8));
+                }
+                uint32_t present;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(sm + L.mask + b * 4));
+                const bool here = present >> (tok / kKvTile) & 1;
+                float r = 0.f;
+                if (half == 0) {
+                    // the token's parameters; of a token that is not there nothing is used
+                    uint32_t kw, vw;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(src + kv_params_at(D, D, 0) + tok % kKvTile * 4));
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(src + kv_params_at(D, D, 1) + tok % kKvTile * 4));
+                    const float2 ks = __half22float2(*reinterpret_cast<__half2*>(&kw));
+                    const float2 vs = __half22float2(*reinterpret_cast<__half2*>(&vw));
+                    float sc = fmaxf(fmaxf(vs.x, fabsf(vs.y) * kScaleOfOffset), kTinyScale);
+                    r = vs.y * rcp_approx(sc);
+                    if (!(fabsf(r) < 65000.f)) {        // a group that is not a number
+                        r = 0.f;
+                        sc = NAN;
+                    }
+                    if (!here) r = 0.f;
+                    *(reinterpret_cast<float4*>(base + L.table) + (n & 3) * kPreStep + tok) =
+                        here ? make_float4(ks.x * sl, ks.y * sl, sc, 0.f) : make_float4(0.f, 0.f, 0.f, 1.f);
+                    if (tok == 0 && present != 0xFFu) (reinterpret_cast<float4*>(base + L.table) + (n & 3) * kPreStep)->w += 2.f;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(k_full[b]));
+                if (!mbar_wait_quiet(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
+                // V: rows of tokens, [token / 8][64 values][token % 8]
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const int chunk = half * (D / 64) + i;
+                    const uint4 w4 = lds128(at + kv_codes_at(D, 1) + chunk * 256);
+                    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    const uint32_t dst = sm + L.v + b * (kPreStep * D * 2) + (tok / 8) * (kHalves * 1024) + (chunk / 2) * 1024 + tok % 8 * 128;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+                        codes_f16(w[j], o);
+                        sts128(dst + (((chunk % 2 * 4 + j) ^ (tok & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (half == 0) {                        // r in rows 0 and 1 of 64 tokens each
+                    const __half hi = __float2half_rn(r);
+                    const __half lo = __float2half_rn(r - __half2float(hi));
+                    const uint32_t dst = sm + L.ext + b * 4096 + (tok / 64) * 2048 + tok % 8 * 2;
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + (tok % 64 / 8 << 4)), "h"(__half_as_ushort(hi)) : "memory");
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 128 + ((tok % 64 / 8 ^ 1) << 4)), "h"(__half_as_ushort(lo)) : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(v_full[b]));
+                    mbar_arrive(bar(code_empty[b]));
+                }
+            }
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------------------------ MMA issue, one thread
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1), id_e = idesc_f16(128, 16, 0, 0);
+            uint32_t parts = 0;
+            // S of block i
+            auto scores = [&](uint32_t i) {
+                const uint32_t b = i & 1, ph = (i >> 1) & 1;
+                if (!mbar_wait_quiet(bar(k_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(s_empty[b]), ph ^ 1, kWaitLimitNs)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_f16(tmem + kSCol + b * 128, smem_desc(sm + L.q + (k / 4) * (kPreRows * 128) + (k % 4) * 32, 16, 1024, 2),
+                               smem_desc(sm + L.k + b * (kPreStep * D * 2) + (k / 4) * (kPreStep * 128) + (k % 4) * 32, 16, 1024, 2), id_s,
+                               k != 0);
+                tc_commit(bar(s_full[b]));
+                return true;
+            };
+            while (ok && walk.next(v, p.rep, c)) {
+                if (!mbar_wait_quiet(bar(q_full), parts & 1, kWaitLimitNs) || !scores(n)) { ok = false; break; }
+                for (int st = c.st0; st < c.st1; ++st, ++n) {
+                    const uint32_t b = n & 1, ph = (n >> 1) & 1;
+                    if (st + 1 < c.st1 && !scores(n + 1)) { ok = false; break; }
+                    if (!mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(x_full), n & 1, kWaitLimitNs)) { ok = false; break; }
+                    // the part before has been read out of O and E
+                    if (st == c.st0 && !mbar_wait_quiet(bar(o_empty), (parts & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kPreStep / 16; ++k) {
+                        const uint32_t acc = st != c.st0 || k != 0;
+                        tc_mma_f16_ts(tmem + kOCol, tmem + kXCol + k * 8,
+                                      smem_desc(sm + L.v + b * (kPreStep * D * 2) + k * (kHalves * 2048), 1024, kHalves * 1024, 2), id_o, acc);
+                        tc_mma_f16_ts(tmem + kECol, tmem + kXCol + k * 8,
+                                      smem_desc(sm + L.ext + b * 4096 + (k / 4) * 2048 + (k % 4) * 32, 16, 1024, 2), id_e, acc);
+                    }
+                    tc_commit(bar(v_empty[b]));
+                }
+                ++parts;
+            }
+            tc_commit(bar(final_bar));         // the MMAs are done before tensor memory is given back
+            mbar_wait_quiet(bar(final_bar), 0, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ codes: eight tiles a block, a lane each
+        while (ok && walk.next(v, p.rep, c)) {
+            const int lead = c.q.len - c.q.rows;
+            const int tokens = (int)min((int64_t)lead + (c.r0 + c.width - 1) / p.rep + 1, (int64_t)v.max_blocks * v.block_tokens);
+            for (int st = c.st0; st < c.st1; ++st, ++n) {
+                const uint32_t b = n & 1;
+                const int t = st * kPreStep + lane * kKvTile;
+                const unsigned char* tile = lane < 8 && t < tokens ? kv_tile_of(v, c.seq, t, c.head, kTile) : nullptr;
+                const uint32_t present = __ballot_sync(0xffffffffu, tile != nullptr);
+                if (!mbar_wait_quiet(bar(code_empty[b]), ((n >> 1) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (lane == 0) {
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sm + L.mask + b * 4), "r"(present) : "memory");
+                    mbar_arrive_expect_tx(bar(code_full[b]), __popc(present) * kTile);
+                }
+                __syncwarp();
+                if (tile) bulk_g2s(sm + L.codes + b * pre_code_bytes(D) + lane * kTile, tile, kTile, bar(code_full[b]));
+            }
+        }
+        for (uint32_t k = n > 2 ? n - 2 : 0; k < n; ++k) mbar_wait_quiet(bar(code_full[k & 1]), (k >> 1) & 1, 100000000ull);
+    }
+    if (!ok && lane == 0) set_error(v.err, LORA_DERR_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace lora

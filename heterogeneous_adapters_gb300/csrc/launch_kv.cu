@@ -6,6 +6,7 @@
 #include "host.h"
 #include "kv_append.cuh"
 #include "kv_attend.cuh"
+#include "kv_prefill.cuh"
 
 using namespace lora;
 using namespace lora::host;
@@ -35,13 +36,7 @@ lora_status check_sizes(const lora_kv_cache_desc* c, const lora_kv_batch* b) {
     return LORA_OK;
 }
 
-// Packed rows a KV head has per request at most, and the row tiles (of 8) a CTA of the
-// attention takes at a time.
-int attend_nt(const lora_kv_cache_desc* c, const lora_kv_batch* b, int32_t q_heads) {
-    return (int64_t)b->max_q * (q_heads / c->num_kv_heads) <= 8 ? 1 : 2;
-}
-
-size_t workspace_bytes() { return align256(attend_workspace(2, 128)); }
+size_t workspace_bytes() { return align256(std::max(attend_workspace(2, 128), pre_workspace(128))); }
 
 lora_status check_call(const lora_kv_cache_desc* c, const lora_kv_batch* b, const void* ws, size_t ws_bytes, size_t need) {
     lora_status st = check_sizes(c, b);
@@ -77,6 +72,8 @@ KvView view_of(const lora_kv_cache_desc* c, const lora_kv_batch* b, void* ws) {
     v.T = b->T;
     v.max_blocks = b->max_blocks;
     v.max_q = b->max_q;
+    v.rows_lo = 0;
+    v.rows_hi = INT32_MAX;
     v.err = &reinterpret_cast<WsHeader*>(ws)->err;
     return v;
 }
@@ -128,6 +125,25 @@ lora_status attend(const AttendParams& p, cudaStream_t s) {
     }
     const int grid = std::min(di->sm_count * std::max(per_sm, 1), kAttMaxCtas);
     kern<<<grid, kAttThreads, smem, s>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+lora_status prefill(const AttendParams& p, cudaStream_t s) {
+    DeviceInfo* di = nullptr;
+    lora_status st = device_info(&di);
+    if (st != LORA_OK) return st;
+    constexpr size_t smem = pre_smem(D).total;
+    auto kern = kv_prefill_kernel<D>;
+    static thread_local int ready_dev = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (ready_dev != dev) {
+        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        if (st != LORA_OK) return st;
+        ready_dev = dev;
+    }
+    kern<<<std::min(di->sm_count, kPreMaxCtas), kPreThreads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -263,8 +279,18 @@ lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch*
     p.scale = softmax_scale;
     p.tickets = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + sizeof(WsHeader));
     p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kStepPartAt);
-    if (attend_nt(cache, batch, num_q_heads) == 1) return attend_by_shape<1>(cache, p, (cudaStream_t)stream);
-    return attend_by_shape<2>(cache, p, (cudaStream_t)stream);
+    cudaStream_t cs = (cudaStream_t)stream;
+    // requests with many packed rows take the tensor-core tiles, the others the decode kernel:
+    // a launch each (how many rows a request has only the device knows)
+    const int32_t many = (kPreMinPacked + p.rep - 1) / p.rep;
+    if (cache->group == cache->head_dim && batch->max_q >= many) {
+        p.v.rows_lo = many;
+        if ((st = cache->head_dim == 128 ? prefill<128>(p, cs) : prefill<64>(p, cs)) != LORA_OK) return st;
+        p.v.rows_lo = 0;
+        p.v.rows_hi = many - 1;
+    }
+    const bool narrow = std::min<int64_t>(batch->max_q, p.v.rows_hi) * p.rep <= 8;
+    return narrow ? attend_by_shape<1>(cache, p, cs) : attend_by_shape<2>(cache, p, cs);
 }
 
 }  // extern "C"
