@@ -28,6 +28,7 @@ constexpr int kPreMaxCtas = 192;
 // A request's packed rows per KV head from which this kernel serves it.
 constexpr int kPreMinPacked = 48;
 
+constexpr int kPreTable = 3 * kPreStep * 4 + 16;
 __host__ __device__ constexpr int pre_code_bytes(int dim) { return kPreStep / kKvTile * kv_tile_bytes(dim, dim); }
 struct PreSmem {
     int q, k, v, ext, codes, table, mask, total;
@@ -40,7 +41,7 @@ __host__ __device__ constexpr PreSmem pre_smem(int dim) {
     L.v = o;      o += 2 * kPreStep * dim * 2;
     L.ext = o;    o += 2 * 4096;                     // [2 x 64 tokens][16 rows][128 bytes]: r hi, r lo, zeros
     L.codes = o;  o += 2 * pre_code_bytes(dim);
-    L.table = o;  o += 4 * kPreStep * 16;            // (k, kq, v) of a block's tokens
+    L.table = o;  o += 4 * kPreTable;                // k, kq, v of a block's tokens, and its tiles that are there
     L.mask = o;   o += 16;
     L.total = o + 1024;
     return L;
@@ -77,6 +78,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ float lds32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    return v;
+}
+// Pairs of fp32 values in one register pair: each half rounded as the scalar operation rounds.
+__device__ __forceinline__ ulonglong2 lds2x64(uint32_t addr) {
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2f(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Walks the parts of tiles in a CTA's range, the same for every role.
@@ -189,7 +223,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             const int pr = c.r0 + tid, row = c.q.row0 + pr / p.rep, hq = c.head * p.rep + pr % p.rep;
             const bool live = tid < c.width;
             const int lead = c.q.len - c.q.rows, low = lead + c.r0 / p.rep;
-            const int last = live ? min(lead + pr / p.rep, cap - 1) : -1;
+            // (a row past the tile's end goes along with the last one)
+            const int last = min(lead + min(pr, c.r0 + c.width - 1) / p.rep, cap - 1);
             float qs = 0.f;
             const __nv_bfloat16* src = p.q + (int64_t)row * p.ldq + (int64_t)hq * D;
 #pragma unroll
@@ -208,93 +243,108 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             float m = kNoRef, l = 0.f;
             for (int st = c.st0; st < c.st1; ++st, ++n) {
                 const uint32_t b = n & 1, sb = lanes + kSCol + b * 128;
-                const float4* table = reinterpret_cast<const float4*>(base + L.table) + (n & 3) * kPreStep;
+                const uint32_t table = sm + L.table + (n & 3) * kPreTable;
                 const int tok0 = st * kPreStep;
                 if (!mbar_wait_quiet(bar(k_full[b]), (n >> 1) & 1, kWaitLimitNs) ||
                     !mbar_wait_quiet(bar(s_full[b]), (n >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
                 tc_fence_after();
-                // causal, or with tiles absent (the table's fourth number: 1, and 2 more at its
-                // head); the same for every row of the tile
-                const bool masked = tok0 + kPreStep - 1 > low || table[0].w >= 2.f;
-                // the scores' exponents of 32 tokens
-                auto exponents = [&](int j0, float (&t)[32], float ref) {
-                    tmem_ld32(sb + j0, t);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float4 k = table[j0 + j];
-                        t[j] = fmaf(k.x, t[j], fmaf(k.y, qs, -ref));
-                        if (masked && (tok0 + j0 + j > last || k.w == 1.f || k.w == 3.f)) t[j] = -INFINITY;
-                    }
-                };
+                uint32_t present;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(table + 3 * kPreStep * 4));
                 // the reference at the largest p v_t of this block, if that is larger
                 auto move = [&]() {
                     float mn = m;
-                    for (int j0 = 0; j0 < kPreStep; j0 += 32) {
-                        float t[32];
-                        exponents(j0, t, 0.f);
+#pragma unroll 1
+                    for (int j0 = 0; j0 < kPreStep; j0 += 16) {
+                        float t[16];
+                        tmem_ld16(sb + j0, t);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (t[j] != -INFINITY) mn = fmaxf(mn, t[j] + log2_approx(table[j0 + j].z));
+                        for (int j = 0; j < 16; ++j) {
+                            const float k = lds32(table + (j0 + j) * 4), kq = lds32(table + (kPreStep + j0 + j) * 4);
+                            const float x = fmaf(k, t[j], kq * qs) + log2_approx(lds32(table + (2 * kPreStep + j0 + j) * 4));
+                            if (tok0 + j0 + j <= last && (present >> (j0 / 16) & 1)) mn = fmaxf(mn, x);
+                        }
                     }
                     const float f = exp2_approx(m - mn);
                     m = mn;
                     l *= f;
                     return f;
                 };
-                bool first = st == c.st0;
-                if (first) move();
-                for (;;) {
-                    float top = 0.f, sum = 0.f;
-                    bool waited = false;
-#pragma unroll 1
+                // X of the block, and the sum of its p; false where X does not fit the reference
+                float sum = 0.f;
+                auto weigh = [&](auto some_masked) {
+                    constexpr bool masked = decltype(some_masked)::value;
+                    const uint64_t qs2 = pack2f(qs, qs), ref2 = pack2f(-m, -m);
+                    float top = 0.f;
+                    uint64_t sum2 = 0;
+#pragma unroll
                     for (int j0 = 0; j0 < kPreStep; j0 += 32) {
                         float t[32];
-                        exponents(j0, t, m);
+                        tmem_ld32(sb + j0, t);
+                        tmem_ld_wait();
                         uint32_t x[16];
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float p0 = exp2_approx(t[j]), p1 = exp2_approx(t[j + 1]);
-                            sum += p0 + p1;
-                            float x0 = p0 * table[j0 + j].z, x1 = p1 * table[j0 + j + 1].z;
-                            if (masked && p0 == 0.f) x0 = 0.f;         // a masked token's scale may be NaN
-                            if (masked && p1 == 0.f) x1 = 0.f;
-                            top = fmaxf(top, fmaxf(x0, x1));
-                            x[j / 2] = pack_f16(x0, x1);
+                        for (int j = 0; j < 32; j += 4) {
+                            const ulonglong2 k = lds2x64(table + (j0 + j) * 4), kq = lds2x64(table + (kPreStep + j0 + j) * 4),
+                                             sc = lds2x64(table + (2 * kPreStep + j0 + j) * 4);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint64_t e = fma2(h ? k.y : k.x, pack2f(t[j + 2 * h], t[j + 2 * h + 1]), fma2(h ? kq.y : kq.x, qs2, ref2));
+                                float e0, e1, x0, x1;
+                                unpack2f(e, e0, e1);
+                                if (masked) {
+                                    const int tok = tok0 + j0 + j + 2 * h;
+                                    const bool here = present >> ((j0 + j) / 16) & 1;
+                                    if (tok > last || !here) e0 = -INFINITY;
+                                    if (tok + 1 > last || !here) e1 = -INFINITY;
+                                }
+                                e0 = exp2_approx(e0);
+                                e1 = exp2_approx(e1);
+                                const uint64_t pr = pack2f(e0, e1);
+                                sum2 = add2(sum2, pr);
+                                unpack2f(mul2(pr, h ? sc.y : sc.x), x0, x1);
+                                if (masked) {                  // a masked token's scale may be anything
+                                    if (e0 == 0.f) x0 = 0.f;
+                                    if (e1 == 0.f) x1 = 0.f;
+                                }
+                                top = fmaxf(top, fmaxf(x0, x1));
+                                x[(j + 2 * h) / 2] = pack_f16(x0, x1);
+                            }
                         }
                         // X is free once the last block's X C_V is done
-                        if (!waited && n > 0 && !mbar_wait_quiet(bar(v_empty[b ^ 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
-                        if (!waited) tc_fence_after();
-                        waited = true;
+                        if (j0 == 0) {
+                            if (n > 0 && !mbar_wait_quiet(bar(v_empty[b ^ 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
+                            tc_fence_after();
+                        }
                         tmem_st16(lanes + kXCol + j0 / 2, x);
                     }
-                    if (!ok) break;
-                    if (!__any_sync(0xffffffffu, top > kMoveAbove)) {
-                        l += sum;
-                        break;
-                    }
-                    // ---- a new reference: O and E (complete, see the wait above) follow
+                    float s0, s1;
+                    unpack2f(sum2, s0, s1);
+                    sum = s0 + s1;
+                    return !__any_sync(0xffffffffu, top > kMoveAbove);
+                };
+                // causal, or with tiles absent: the same for every row of the tile
+                const bool masked = tok0 + kPreStep - 1 > low || present != 0xFFu;
+                const bool first = st == c.st0;
+                if (first) move();
+                if (!(masked ? weigh(std::true_type{}) : weigh(std::false_type{})) && ok) {
+                    // a new reference: O and E (complete, see the wait above) follow, and X once more
                     const float f = move();
-                    if (!first) {
-                        tmem_st_wait();
-                        for (int j0 = 0; j0 < D; j0 += 16) {
-                            float o[16];
-                            uint32_t w[16];
-                            tmem_ld16(lanes + kOCol + j0, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * f);
-                            tmem_st16(lanes + kOCol + j0, w);
-                        }
+                    tmem_st_wait();
+#pragma unroll 1
+                    for (int j0 = 0; j0 < (first ? 0 : D + 16); j0 += 16) {
+                        const uint32_t at = lanes + (j0 < D ? kOCol + j0 : kECol);
                         float o[16];
                         uint32_t w[16];
-                        tmem_ld16(lanes + kECol, o);
+                        tmem_ld16(at, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * f);
-                        tmem_st16(lanes + kECol, w);
+                        tmem_st16(at, w);
                     }
+                    weigh(std::true_type{});
                 }
+                l += sum;
                 if (!ok) break;
                 tmem_st_wait();
                 tc_fence_before();
@@ -422,9 +472,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                         sc = NAN;
                     }
                     if (!here) r = 0.f;
-                    *(reinterpret_cast<float4*>(base + L.table) + (n & 3) * kPreStep + tok) =
-                        here ? make_float4(ks.x * sl, ks.y * sl, sc, 0.f) : make_float4(0.f, 0.f, 0.f, 1.f);
-                    if (tok == 0 && present != 0xFFu) (reinterpret_cast<float4*>(base + L.table) + (n & 3) * kPreStep)->w += 2.f;
+                    float* table = reinterpret_cast<float*>(base + L.table + (n & 3) * kPreTable);
+                    table[tok] = here ? ks.x * sl : 0.f;
+                    table[kPreStep + tok] = here ? ks.y * sl : 0.f;
+                    table[2 * kPreStep + tok] = here ? sc : 0.f;
+                    if (tok == 0) reinterpret_cast<uint32_t*>(table)[3 * kPreStep] = present;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
