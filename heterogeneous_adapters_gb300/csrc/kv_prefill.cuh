@@ -11,17 +11,17 @@
 // cost no work per element.  The output is (O + E) / sum p.  The reference M is moved, and O
 // and E multiplied, only when a p v_t exceeds 2^10.
 //
-// Warps 0-3 hold a row a thread: they bring q, turn S into X and write the output.  Warps 4-11
-// unpack a block's codes into the operands' swizzled rows (within eight values in the order
-// 0 4 1 5 2 6 3 7, q alike, and the output put back).  Warp 12 issues the MMAs, S of the next
-// block before X C_V of this one; warp 13 brings the codes.  A block costs 1024 clocks of MMA
+// Warps 0-7 hold half of a row a thread (64 of a block's tokens, half of the output): they
+// bring q, turn S into X and write the output.  Warps 8-15 unpack a block's codes into the operands' swizzled rows (within eight values in the order
+// 0 4 1 5 2 6 3 7, q alike, and the output put back).  Warp 16 issues the MMAs, S of the next
+// block before X C_V of this one; warp 17 brings the codes.  A block costs 1024 clocks of MMA
 // and as many of exponentials.  Tiles are dealt, split and joined as kv_attend.cuh's items.
 #pragma once
 #include "kv_attend.cuh"
 
 namespace lora {
 
-constexpr int kPreRows = 128, kPreStep = 128, kPreThreads = 14 * 32;
+constexpr int kPreRows = 128, kPreStep = 128, kPreThreads = 18 * 32;
 constexpr int kPreItemCost = 3;      // blocks' worth of a tile's fixed part
 constexpr int kPreMinUnits = 4;
 constexpr int kPreMaxCtas = 192;
@@ -31,7 +31,7 @@ constexpr int kPreMinPacked = 48;
 constexpr int kPreTable = 3 * kPreStep * 4 + 16;
 __host__ __device__ constexpr int pre_code_bytes(int dim) { return kPreStep / kKvTile * kv_tile_bytes(dim, dim); }
 struct PreSmem {
-    int q, k, v, ext, codes, table, mask, total;
+    int q, k, v, ext, codes, table, mask, pair, total;
 };
 __host__ __device__ constexpr PreSmem pre_smem(int dim) {
     PreSmem L{};
@@ -43,6 +43,7 @@ __host__ __device__ constexpr PreSmem pre_smem(int dim) {
     L.codes = o;  o += 2 * pre_code_bytes(dim);
     L.table = o;  o += 4 * kPreTable;                // k, kq, v of a block's tokens, and its tiles that are there
     L.mask = o;   o += 16;
+    L.pair = o;   o += 2 * kPreRows * 4 + 64;        // what a row's two threads exchange; flags [4 pairs][4]
     L.total = o + 1024;
     return L;
 }
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     constexpr uint32_t kSCol = 0, kOCol = 256, kXCol = 384, kECol = 448;    // S twice, O, X, E
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t code_full[2], code_empty[2], k_full[2], v_full[2], v_empty[2], s_full[2], s_empty[2],
-        x_full, q_full, o_empty, join, final_bar;
+        x_full, q_full, o_empty, join, pair[4], final_bar;
     __shared__ int64_t scan[kPreThreads / 32 + 1], found[2];
     __shared__ uint32_t tmem_slot, last_in;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -185,18 +186,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             mbar_init(bar(v_full[i]), 8);
             mbar_init(bar(v_empty[i]), 1);
             mbar_init(bar(s_full[i]), 1);
-            mbar_init(bar(s_empty[i]), 4);
+            mbar_init(bar(s_empty[i]), 8);
         }
-        mbar_init(bar(x_full), 4);
-        mbar_init(bar(q_full), 4);
-        mbar_init(bar(o_empty), 4);
-        mbar_init(bar(join), 4);
+        mbar_init(bar(x_full), 8);
+        mbar_init(bar(q_full), 8);
+        mbar_init(bar(o_empty), 8);
+        mbar_init(bar(join), 8);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(pair[i]), 2);
         mbar_init(bar(final_bar), 1);
         fence_mbar_init();
     }
     for (int i = tid; i < 2 * 4096 / 16; i += kPreThreads) sts128(sm + L.ext + i * 16, 0, 0, 0, 0);
+    if (tid < 4) sts128(sm + L.pair + 2 * kPreRows * 4 + tid * 16, 0, 0, 0, 0);
     fence_proxy_async_smem();
-    if (warp == 12) {
+    if (warp == 16) {
         tmem_alloc(smem_addr(&tmem_slot), 512);
         tmem_relinquish();
     }
@@ -208,53 +211,74 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     PrePart c;
     uint32_t n = 0;              // blocks so far: n % 2 is the buffer, n / 2 the phase
 
-    if (warp < 4) {
+    if (warp < 8) {
         // ------------------------------------------------------------------ rows
-        const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-        uint32_t ij = 0;
+        const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t flags = sm + L.pair + 2 * kPreRows * 4 + quad * 16;
+        uint32_t ij = 0, ip = 0;
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(join));
             return mbar_wait_quiet(bar(join), ij++ & 1, kWaitLimitNs);
         };
+        // the two warps of the same rows meet
+        auto meet_pair = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(pair[quad]));
+            return mbar_wait_quiet(bar(pair[quad]), ip++ & 1, kWaitLimitNs);
+        };
+        // the other thread's value for the row (the second meeting keeps the buffer whole)
+        auto exchange = [&](float x) {
+            float* buf = reinterpret_cast<float*>(base + L.pair);
+            buf[half * kPreRows + r] = x;
+            ok = ok && meet_pair();
+            const float y = *reinterpret_cast<volatile float*>(&buf[(half ^ 1) * kPreRows + r]);
+            ok = ok && meet_pair();
+            return y;
+        };
         const int cap = (int)((int64_t)v.max_blocks * v.block_tokens);
         while (ok && walk.next(v, p.rep, c)) {
             // ---- q into its swizzled rows (every S of the part before is done), and its sum
-            const int pr = c.r0 + tid, row = c.q.row0 + pr / p.rep, hq = c.head * p.rep + pr % p.rep;
-            const bool live = tid < c.width;
+            const int pr = c.r0 + r, row = c.q.row0 + pr / p.rep, hq = c.head * p.rep + pr % p.rep;
+            const bool live = r < c.width;
             const int lead = c.q.len - c.q.rows, low = lead + c.r0 / p.rep;
             // (a row past the tile's end goes along with the last one)
             const int last = min(lead + min(pr, c.r0 + c.width - 1) / p.rep, cap - 1);
             float qs = 0.f;
             const __nv_bfloat16* src = p.q + (int64_t)row * p.ldq + (int64_t)hq * D;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
+            for (int k = 0; k < D / 16; ++k) {
+                const int i = half * (D / 16) + k;
                 const uint4 w = live ? ld16(src + i * 8) : make_uint4(0, 0, 0, 0);
                 float f[8];
                 unpack8(w, f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) qs += f[j];
-                sts128(sm + L.q + (i / 8) * (kPreRows * 128) + tid * 128 + ((i % 8 ^ (tid & 7)) << 4), __byte_perm(w.x, w.z, 0x5410),
+                sts128(sm + L.q + (i / 8) * (kPreRows * 128) + r * 128 + ((i % 8 ^ (r & 7)) << 4), __byte_perm(w.x, w.z, 0x5410),
                        __byte_perm(w.x, w.z, 0x7632), __byte_perm(w.y, w.w, 0x5410), __byte_perm(w.y, w.w, 0x7632));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(q_full));
+            const float qo = exchange(qs);
+            qs = half ? qo + qs : qs + qo;              // the same sum for both
             float m = kNoRef, l = 0.f;
-            for (int st = c.st0; st < c.st1; ++st, ++n) {
-                const uint32_t b = n & 1, sb = lanes + kSCol + b * 128;
-                const uint32_t table = sm + L.table + (n & 3) * kPreTable;
-                const int tok0 = st * kPreStep;
+            for (int st = c.st0; st < c.st1 && ok; ++st, ++n) {
+                const uint32_t b = n & 1, sb = lanes + kSCol + b * 128 + half * 64;
+                const uint32_t table = sm + L.table + (n & 3) * kPreTable + half * 256;
+                const int tok0 = st * kPreStep + half * 64;
                 if (!mbar_wait_quiet(bar(k_full[b]), (n >> 1) & 1, kWaitLimitNs) ||
                     !mbar_wait_quiet(bar(s_full[b]), (n >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t present;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(table + 3 * kPreStep * 4));
-                // the reference at the largest p v_t of this block, if that is larger
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(table - half * 256 + 3 * kPreStep * 4));
+                const uint32_t here = present >> (half * 4);        // this half's four tiles
+                // the reference at the row's largest p v_t of this block, if that is larger
                 auto move = [&]() {
                     float mn = m;
 #pragma unroll 1
-                    for (int j0 = 0; j0 < kPreStep; j0 += 16) {
+                    for (int j0 = 0; j0 < 64; j0 += 16) {
                         float t[16];
                         tmem_ld16(sb + j0, t);
                         tmem_ld_wait();
@@ -262,15 +286,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                         for (int j = 0; j < 16; ++j) {
                             const float k = lds32(table + (j0 + j) * 4), kq = lds32(table + (kPreStep + j0 + j) * 4);
                             const float x = fmaf(k, t[j], kq * qs) + log2_approx(lds32(table + (2 * kPreStep + j0 + j) * 4));
-                            if (tok0 + j0 + j <= last && (present >> (j0 / 16) & 1)) mn = fmaxf(mn, x);
+                            if (tok0 + j0 + j <= last && (here >> (j0 / 16) & 1)) mn = fmaxf(mn, x);
                         }
                     }
+                    mn = fmaxf(mn, exchange(mn));
                     const float f = exp2_approx(m - mn);
                     m = mn;
                     l *= f;
                     return f;
                 };
-                // X of the block, and the sum of its p; false where X does not fit the reference
+                // X of the half, and the sum of its p; false where X does not fit the reference
                 float sum = 0.f;
                 auto weigh = [&](auto some_masked) {
                     constexpr bool masked = decltype(some_masked)::value;
@@ -278,7 +303,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     float top = 0.f;
                     uint64_t sum2 = 0;
 #pragma unroll
-                    for (int j0 = 0; j0 < kPreStep; j0 += 32) {
+                    for (int j0 = 0; j0 < 64; j0 += 32) {
                         float t[32];
                         tmem_ld32(sb + j0, t);
                         tmem_ld_wait();
@@ -294,9 +319,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                                 unpack2f(e, e0, e1);
                                 if (masked) {
                                     const int tok = tok0 + j0 + j + 2 * h;
-                                    const bool here = present >> ((j0 + j) / 16) & 1;
-                                    if (tok > last || !here) e0 = -INFINITY;
-                                    if (tok + 1 > last || !here) e1 = -INFINITY;
+                                    const bool in = here >> ((j0 + j) / 16) & 1;
+                                    if (tok > last || !in) e0 = -INFINITY;
+                                    if (tok + 1 > last || !in) e1 = -INFINITY;
                                 }
                                 e0 = exp2_approx(e0);
                                 e1 = exp2_approx(e1);
@@ -316,7 +341,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                             if (n > 0 && !mbar_wait_quiet(bar(v_empty[b ^ 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
                             tc_fence_after();
                         }
-                        tmem_st16(lanes + kXCol + j0 / 2, x);
+                        tmem_st16(lanes + kXCol + half * 32 + j0 / 2, x);
                     }
                     float s0, s1;
                     unpack2f(sum2, s0, s1);
@@ -324,15 +349,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     return !__any_sync(0xffffffffu, top > kMoveAbove);
                 };
                 // causal, or with tiles absent: the same for every row of the tile
-                const bool masked = tok0 + kPreStep - 1 > low || present != 0xFFu;
+                const bool masked = st * kPreStep + kPreStep - 1 > low || present != 0xFFu;
                 const bool first = st == c.st0;
                 if (first) move();
-                if (!(masked ? weigh(std::true_type{}) : weigh(std::false_type{})) && ok) {
+                // whether either warp of the rows has an X that does not fit (a flag a block, four in turn)
+                const bool fits = masked ? weigh(std::true_type{}) : weigh(std::false_type{});
+                if (!fits && lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(flags + (n & 3) * 4), "r"(1u) : "memory");
+                if (lane == 0 && half == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(flags + ((n + 2) & 3) * 4), "r"(0u) : "memory");
+                ok = ok && meet_pair();
+                uint32_t again;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(again) : "r"(flags + (n & 3) * 4));
+                if (again && ok) {
                     // a new reference: O and E (complete, see the wait above) follow, and X once more
                     const float f = move();
                     tmem_st_wait();
 #pragma unroll 1
-                    for (int j0 = 0; j0 < (first ? 0 : D + 16); j0 += 16) {
+                    for (int j0 = half * (D / 2); j0 < (first ? 0 : half ? D + 16 : D / 2); j0 += 16) {
                         const uint32_t at = lanes + (j0 < D ? kOCol + j0 : kECol);
                         float o[16];
                         uint32_t w[16];
@@ -355,6 +387,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 }
             }
             if (!ok) break;
+            const float lo = exchange(l);
+            l = half ? lo + l : l + lo;
             // ---- the part's sums
             if (!mbar_wait_quiet(bar(v_empty[(n - 1) & 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
             tc_fence_after();
@@ -373,9 +407,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                                                  pack2(o[i + 1] * f, o[i + 3] * f), pack2(o[i + 5] * f, o[i + 7] * f)));
             };
             const int slot = c.body < walk.first ? 0 : 1;
-            float* part = p.part + ((int64_t)blockIdx.x * 2 + slot) * kPreRows * (D + 2) + tid;
+            float* part = p.part + ((int64_t)blockIdx.x * 2 + slot) * kPreRows * (D + 2) + r;
             const float inv = l != 0.f ? 1.f / l : 0.f;
-            for (int j0 = 0; j0 < D; j0 += 32) {
+            for (int j0 = half * (D / 2); j0 < (half + 1) * (D / 2); j0 += 32) {
                 float o[32];
                 tmem_ld32(lanes + kOCol + j0, o);
                 tmem_ld_wait();
@@ -392,11 +426,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(o_empty));
             if (whole) {
-                if (live) att_store_lse(p, row, hq, m, l);
+                if (live && half == 0) att_store_lse(p, row, hq, m, l);
                 continue;
             }
-            part[D * kPreRows] = m;
-            part[(D + 1) * kPreRows] = l;
+            if (half == 0) {
+                part[D * kPreRows] = m;
+                part[(D + 1) * kPreRows] = l;
+            }
             const int64_t c0 = c.body / per, c1 = (c.body + c.steps - 1) / per;
             __threadfence();
             if (!(ok = meet())) break;
@@ -406,7 +442,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 __threadfence();
                 if (tid == 0) p.tickets[c0] = 0;
                 auto from = [&](int64_t i) {
-                    return p.part + (i * 2 + (c.body < i * per ? 0 : 1)) * kPreRows * (D + 2) + tid;
+                    return p.part + (i * 2 + (c.body < i * per ? 0 : 1)) * kPreRows * (D + 2) + r;
                 };
                 m = kNoRef;
                 for (int64_t i = c0; i <= c1; ++i) m = fmaxf(m, __ldcg(from(i) + D * kPreRows));
@@ -414,7 +450,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 for (int64_t i = c0; i <= c1; ++i)
                     l += __ldcg(from(i) + (D + 1) * kPreRows) * exp2_approx(__ldcg(from(i) + D * kPreRows) - m);
                 const float f = l != 0.f ? 1.f / l : 0.f;
-                for (int j0 = 0; j0 < D; j0 += 32) {
+                for (int j0 = half * (D / 2); j0 < (half + 1) * (D / 2); j0 += 32) {
                     float o[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) o[j] = 0.f;
@@ -426,13 +462,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     }
                     store(j0, o, f);
                 }
-                if (live) att_store_lse(p, row, hq, m, l);
+                if (live && half == 0) att_store_lse(p, row, hq, m, l);
             }
             if (!(ok = meet())) break;
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------------------------------ unpacking: a token, half of its values
-        const int tok = tid & 127, half = (tid - 128) >> 7;
+        const int tok = tid & 127, half = (tid - 256) >> 7;
         const float sl = p.scale * 1.44269504f;
         while (ok && walk.next(v, p.rep, c)) {
             for (int st = c.st0; st < c.st1; ++st, ++n) {
@@ -511,7 +547,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 }
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == 16) {
         // ------------------------------------------------------------------ MMA issue, one thread
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1), id_e = idesc_f16(128, 16, 0, 0);
@@ -579,7 +615,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace lora
