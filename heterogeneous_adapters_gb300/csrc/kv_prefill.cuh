@@ -6,15 +6,15 @@
 // -8 .. 7,
 //     S = q C_K^T (128 x 128, tensor memory),   t = S k_t + kq_t sum(q) - M,   p = 2^t,
 // where k_t and kq_t are the token's K scale and offset times softmax_scale log2 e; then
-//     O += X C_V,   X = f16(p v_t),   and   E += X r_t,   r_t = V offset / V scale,
-// X from tensor memory, C_V in f16, and r in two f16 columns (r = hi + lo), so that the offsets
-// cost no work per element.  The output is (O + E) / sum p.  The reference M is moved, and O
-// and E multiplied, only when a p v_t exceeds 2^10.
+//     O += X W,   X = f16(p v_t),   W = f16((c - 8) + V offset / V scale) = f16(v / V scale),
+// the offset added in two parts (hi + lo) so that W is off by 2^-11 of itself even where the
+// two nearly cancel; X takes the place of S in tensor memory.  The output is O / sum p.  The
+// reference M is moved, and O multiplied, only when a p v_t exceeds 2^10.
 //
 // Warps 0-7 hold half of a row a thread (64 of a block's tokens, half of the output): they
 // bring q, turn S into X and write the output.  Warps 8-15 unpack a block's codes into the operands' swizzled rows (within eight values in the order
 // 0 4 1 5 2 6 3 7, q alike, and the output put back).  Warp 16 issues the MMAs, S of the next
-// block before X C_V of this one; warp 17 brings the codes.  A block costs 1024 clocks of MMA
+// block before X W of this one; warp 17 brings the codes.  A block costs 1024 clocks of MMA
 // and as many of exponentials.  Tiles are dealt, split and joined as kv_attend.cuh's items.
 #pragma once
 #include "kv_attend.cuh"
@@ -31,7 +31,7 @@ constexpr int kPreMinPacked = 48;
 constexpr int kPreTable = 3 * kPreStep * 4 + 16;
 __host__ __device__ constexpr int pre_code_bytes(int dim) { return kPreStep / kKvTile * kv_tile_bytes(dim, dim); }
 struct PreSmem {
-    int q, k, v, ext, codes, table, mask, pair, total;
+    int q, k, v, codes, table, mask, pair, total;
 };
 __host__ __device__ constexpr PreSmem pre_smem(int dim) {
     PreSmem L{};
@@ -39,7 +39,6 @@ __host__ __device__ constexpr PreSmem pre_smem(int dim) {
     L.q = o;      o += kPreRows * dim * 2;
     L.k = o;      o += 2 * kPreStep * dim * 2;
     L.v = o;      o += 2 * kPreStep * dim * 2;
-    L.ext = o;    o += 2 * 4096;                     // [2 x 64 tokens][16 rows][128 bytes]: r hi, r lo, zeros
     L.codes = o;  o += 2 * pre_code_bytes(dim);
     L.table = o;  o += 4 * kPreTable;                // k, kq, v of a block's tokens, and its tiles that are there
     L.mask = o;   o += 16;
@@ -56,27 +55,6 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t m, uint32_t n, uint32_
     return idesc_bf16(m, n, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -157,10 +135,11 @@ template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kTile = kv_tile_bytes(D, D), kHalves = D / 64;
     constexpr PreSmem L = pre_smem(D);
-    constexpr uint32_t kSCol = 0, kOCol = 256, kXCol = 384, kECol = 448;    // S twice, O, X, E
+    // tensor memory: S twice (X of tokens 0-63 in a buffer's columns 0-31, of 64-127 in 64-95), O
+    constexpr uint32_t kSCol = 0, kOCol = 256;
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t code_full[2], code_empty[2], k_full[2], v_full[2], v_empty[2], s_full[2], s_empty[2],
-        x_full, q_full, o_empty, join, pair[4], final_bar;
+    __shared__ __align__(8) uint64_t code_full[2], code_empty[2], k_full[2], v_full[2], v_empty[2], s_full[2],
+        x_full, q_full, o_empty, final_bar;
     __shared__ int64_t scan[kPreThreads / 32 + 1], found[2];
     __shared__ uint32_t tmem_slot, last_in;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -186,19 +165,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             mbar_init(bar(v_full[i]), 8);
             mbar_init(bar(v_empty[i]), 1);
             mbar_init(bar(s_full[i]), 1);
-            mbar_init(bar(s_empty[i]), 8);
         }
         mbar_init(bar(x_full), 8);
         mbar_init(bar(q_full), 8);
         mbar_init(bar(o_empty), 8);
-        mbar_init(bar(join), 8);
-        for (int i = 0; i < 4; ++i) mbar_init(bar(pair[i]), 2);
         mbar_init(bar(final_bar), 1);
         fence_mbar_init();
     }
-    for (int i = tid; i < 2 * 4096 / 16; i += kPreThreads) sts128(sm + L.ext + i * 16, 0, 0, 0, 0);
     if (tid < 4) sts128(sm + L.pair + 2 * kPreRows * 4 + tid * 16, 0, 0, 0, 0);
-    fence_proxy_async_smem();
     if (warp == 16) {
         tmem_alloc(smem_addr(&tmem_slot), 512);
         tmem_relinquish();
@@ -216,29 +190,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t flags = sm + L.pair + 2 * kPreRows * 4 + quad * 16;
-        uint32_t ij = 0, ip = 0;
-        auto meet = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(join));
-            return mbar_wait_quiet(bar(join), ij++ & 1, kWaitLimitNs);
+        // These warps meet at named barriers, so none of them leaves early: after a wait that ran
+        // out, `wait` returns at once and the rest of the range goes by (with the error set).
+        auto wait = [&](uint64_t& which, uint32_t parity) {
+            if (ok && !mbar_wait_quiet(bar(which), parity, kWaitLimitNs)) {
+                ok = false;
+                if (lane == 0) set_error(v.err, LORA_DERR_TIMEOUT);
+            }
         };
-        // the two warps of the same rows meet
-        auto meet_pair = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(pair[quad]));
-            return mbar_wait_quiet(bar(pair[quad]), ip++ & 1, kWaitLimitNs);
-        };
+        auto meet = [&]() { named_bar_sync(1, 256); };
+        auto meet_pair = [&]() { named_bar_sync(2 + quad, 64); };    // the two warps of the same rows
         // the other thread's value for the row (the second meeting keeps the buffer whole)
         auto exchange = [&](float x) {
             float* buf = reinterpret_cast<float*>(base + L.pair);
             buf[half * kPreRows + r] = x;
-            ok = ok && meet_pair();
+            meet_pair();
             const float y = *reinterpret_cast<volatile float*>(&buf[(half ^ 1) * kPreRows + r]);
-            ok = ok && meet_pair();
+            meet_pair();
             return y;
         };
         const int cap = (int)((int64_t)v.max_blocks * v.block_tokens);
-        while (ok && walk.next(v, p.rep, c)) {
+        while (walk.next(v, p.rep, c)) {
             // ---- q into its swizzled rows (every S of the part before is done), and its sum
             const int pr = c.r0 + r, row = c.q.row0 + pr / p.rep, hq = c.head * p.rep + pr % p.rep;
             const bool live = r < c.width;
@@ -264,12 +236,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             const float qo = exchange(qs);
             qs = half ? qo + qs : qs + qo;              // the same sum for both
             float m = kNoRef, l = 0.f;
-            for (int st = c.st0; st < c.st1 && ok; ++st, ++n) {
+            for (int st = c.st0; st < c.st1; ++st, ++n) {
                 const uint32_t b = n & 1, sb = lanes + kSCol + b * 128 + half * 64;
                 const uint32_t table = sm + L.table + (n & 3) * kPreTable + half * 256;
                 const int tok0 = st * kPreStep + half * 64;
-                if (!mbar_wait_quiet(bar(k_full[b]), (n >> 1) & 1, kWaitLimitNs) ||
-                    !mbar_wait_quiet(bar(s_full[b]), (n >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
+                wait(s_full[b], (n >> 1) & 1);
                 tc_fence_after();
                 uint32_t present;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(table - half * 256 + 3 * kPreStep * 4));
@@ -297,6 +268,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 };
                 // X of the half, and the sum of its p; false where X does not fit the reference
                 float sum = 0.f;
+                uint32_t x[32];
                 auto weigh = [&](auto some_masked) {
                     constexpr bool masked = decltype(some_masked)::value;
                     const uint64_t qs2 = pack2f(qs, qs), ref2 = pack2f(-m, -m);
@@ -307,7 +279,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                         float t[32];
                         tmem_ld32(sb + j0, t);
                         tmem_ld_wait();
-                        uint32_t x[16];
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const ulonglong2 k = lds2x64(table + (j0 + j) * 4), kq = lds2x64(table + (kPreStep + j0 + j) * 4),
@@ -333,15 +304,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                                     if (e1 == 0.f) x1 = 0.f;
                                 }
                                 top = fmaxf(top, fmaxf(x0, x1));
-                                x[(j + 2 * h) / 2] = pack_f16(x0, x1);
+                                x[(j0 + j + 2 * h) / 2] = pack_f16(x0, x1);
                             }
                         }
-                        // X is free once the last block's X C_V is done
-                        if (j0 == 0) {
-                            if (n > 0 && !mbar_wait_quiet(bar(v_empty[b ^ 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) ok = false;
-                            tc_fence_after();
-                        }
-                        tmem_st16(lanes + kXCol + half * 32 + j0 / 2, x);
                     }
                     float s0, s1;
                     unpack2f(sum2, s0, s1);
@@ -356,46 +321,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 const bool fits = masked ? weigh(std::true_type{}) : weigh(std::false_type{});
                 if (!fits && lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(flags + (n & 3) * 4), "r"(1u) : "memory");
                 if (lane == 0 && half == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(flags + ((n + 2) & 3) * 4), "r"(0u) : "memory");
-                ok = ok && meet_pair();
+                meet_pair();
                 uint32_t again;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(again) : "r"(flags + (n & 3) * 4));
-                if (again && ok) {
-                    // a new reference: O and E (complete, see the wait above) follow, and X once more
+                if (again) {
+                    // a new reference: O (of the blocks before) follows, and X once more
                     const float f = move();
-                    tmem_st_wait();
+                    if (!first) wait(v_empty[b ^ 1], ((n - 1) >> 1) & 1);
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int j0 = half * (D / 2); j0 < (first ? 0 : half ? D + 16 : D / 2); j0 += 16) {
-                        const uint32_t at = lanes + (j0 < D ? kOCol + j0 : kECol);
+                    for (int j0 = half * (D / 2); j0 < (first ? 0 : (half + 1) * (D / 2)); j0 += 16) {
                         float o[16];
                         uint32_t w[16];
-                        tmem_ld16(at, o);
+                        tmem_ld16(lanes + kOCol + j0, o);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(o[j] * f);
-                        tmem_st16(at, w);
+                        tmem_st16(lanes + kOCol + j0, w);
                     }
                     weigh(std::true_type{});
                 }
                 l += sum;
-                if (!ok) break;
+                tmem_st32(sb, x);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(s_empty[b]));
-                    mbar_arrive(bar(x_full));
-                }
+                if (lane == 0) mbar_arrive(bar(x_full));
             }
-            if (!ok) break;
             const float lo = exchange(l);
             l = half ? lo + l : l + lo;
             // ---- the part's sums
-            if (!mbar_wait_quiet(bar(v_empty[(n - 1) & 1]), ((n - 1) >> 1) & 1, kWaitLimitNs)) { ok = false; break; }
+            wait(v_empty[(n - 1) & 1], ((n - 1) >> 1) & 1);
             tc_fence_after();
-            float e[16];
-            tmem_ld16(lanes + kECol, e);
-            tmem_ld_wait();
-            const float off = e[0] + e[1];
             const bool whole = c.whole();
             // 32 values of the row (eight by eight in the operands' order) to the output
             auto store = [&](int j0, const float (&o)[32], float f) {
@@ -413,8 +370,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 float o[32];
                 tmem_ld32(lanes + kOCol + j0, o);
                 tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] += off;
                 if (whole) {
                     store(j0, o, inv);
                 } else {
@@ -435,9 +390,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             }
             const int64_t c0 = c.body / per, c1 = (c.body + c.steps - 1) / per;
             __threadfence();
-            if (!(ok = meet())) break;
+            meet();
             if (tid == 0) last_in = atomicAdd(&p.tickets[c0], 1u) == (uint32_t)(c1 - c0);
-            if (!(ok = meet())) break;
+            meet();
             if (*reinterpret_cast<volatile uint32_t*>(&last_in)) {
                 __threadfence();
                 if (tid == 0) p.tickets[c0] = 0;
@@ -464,7 +419,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 }
                 if (live && half == 0) att_store_lse(p, row, hq, m, l);
             }
-            if (!(ok = meet())) break;
+            meet();
         }
     } else if (warp < 16) {
         // ------------------------------------------------------------------ unpacking: a token, half of its values
@@ -493,21 +448,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 uint32_t present;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(sm + L.mask + b * 4));
                 const bool here = present >> (tok / kKvTile) & 1;
-                float r = 0.f;
+                uint32_t vw;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(src + kv_params_at(D, D, 1) + tok % kKvTile * 4));
+                const float2 vs = __half22float2(*reinterpret_cast<__half2*>(&vw));
+                float sc = fmaxf(fmaxf(vs.x, fabsf(vs.y) * kScaleOfOffset), kTinyScale), r = vs.y * rcp_approx(sc);
+                if (!(fabsf(r) < 65000.f)) {            // a group that is not a number
+                    r = 0.f;
+                    sc = NAN;
+                }
                 if (half == 0) {
                     // the token's parameters; of a token that is not there nothing is used
-                    uint32_t kw, vw;
+                    uint32_t kw;
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(src + kv_params_at(D, D, 0) + tok % kKvTile * 4));
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(src + kv_params_at(D, D, 1) + tok % kKvTile * 4));
                     const float2 ks = __half22float2(*reinterpret_cast<__half2*>(&kw));
-                    const float2 vs = __half22float2(*reinterpret_cast<__half2*>(&vw));
-                    float sc = fmaxf(fmaxf(vs.x, fabsf(vs.y) * kScaleOfOffset), kTinyScale);
-                    r = vs.y * rcp_approx(sc);
-                    if (!(fabsf(r) < 65000.f)) {        // a group that is not a number
-                        r = 0.f;
-                        sc = NAN;
-                    }
-                    if (!here) r = 0.f;
                     float* table = reinterpret_cast<float*>(base + L.table + (n & 3) * kPreTable);
                     table[tok] = here ? ks.x * sl : 0.f;
                     table[kPreStep + tok] = here ? ks.y * sl : 0.f;
@@ -518,7 +471,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(k_full[b]));
                 if (!mbar_wait_quiet(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
-                // V: rows of tokens, [token / 8][64 values][token % 8]
+                // W: rows of tokens, [token / 8][64 values][token % 8]
+                const __half hi = __float2half_rn(here ? r : 0.f);
+                const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(__float2half_rn((here ? r : 0.f) - __half2float(hi)));
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                     const int chunk = half * (D / 64) + i;
@@ -529,15 +484,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     for (int j = 0; j < 4; ++j) {
                         uint32_t o[4];
                         codes_f16(w[j], o);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __half2 x = __hadd2(__hadd2(*reinterpret_cast<__half2*>(&o[k]), hi2), lo2);
+                            o[k] = *reinterpret_cast<const uint32_t*>(&x);
+                        }
                         sts128(dst + (((chunk % 2 * 4 + j) ^ (tok & 7)) << 4), o[0], o[1], o[2], o[3]);
                     }
-                }
-                if (half == 0) {                        // r in rows 0 and 1 of 64 tokens each
-                    const __half hi = __float2half_rn(r);
-                    const __half lo = __float2half_rn(r - __half2float(hi));
-                    const uint32_t dst = sm + L.ext + b * 4096 + (tok / 64) * 2048 + tok % 8 * 2;
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + (tok % 64 / 8 << 4)), "h"(__half_as_ushort(hi)) : "memory");
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + 128 + ((tok % 64 / 8 ^ 1) << 4)), "h"(__half_as_ushort(lo)) : "memory");
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -550,12 +503,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     } else if (warp == 16) {
         // ------------------------------------------------------------------ MMA issue, one thread
         if (lane == 0) {
-            constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1), id_e = idesc_f16(128, 16, 0, 0);
+            constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1);
             uint32_t parts = 0;
-            // S of block i
+            // S of block i, in the place of X of block i - 2, whose X W has to be done
             auto scores = [&](uint32_t i) {
                 const uint32_t b = i & 1, ph = (i >> 1) & 1;
-                if (!mbar_wait_quiet(bar(k_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(s_empty[b]), ph ^ 1, kWaitLimitNs)) return false;
+                if (!mbar_wait_quiet(bar(k_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
@@ -571,16 +524,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     const uint32_t b = n & 1, ph = (n >> 1) & 1;
                     if (st + 1 < c.st1 && !scores(n + 1)) { ok = false; break; }
                     if (!mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(x_full), n & 1, kWaitLimitNs)) { ok = false; break; }
-                    // the part before has been read out of O and E
+                    // the part before has been read out of O
                     if (st == c.st0 && !mbar_wait_quiet(bar(o_empty), (parts & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < kPreStep / 16; ++k) {
-                        const uint32_t acc = st != c.st0 || k != 0;
-                        tc_mma_f16_ts(tmem + kOCol, tmem + kXCol + k * 8,
-                                      smem_desc(sm + L.v + b * (kPreStep * D * 2) + k * (kHalves * 2048), 1024, kHalves * 1024, 2), id_o, acc);
-                        tc_mma_f16_ts(tmem + kECol, tmem + kXCol + k * 8,
-                                      smem_desc(sm + L.ext + b * 4096 + (k / 4) * 2048 + (k % 4) * 32, 16, 1024, 2), id_e, acc);
+                        tc_mma_f16_ts(tmem + kOCol, tmem + kSCol + b * 128 + (k / 4) * 64 + k % 4 * 8,
+                                      smem_desc(sm + L.v + b * (kPreStep * D * 2) + k * (kHalves * 2048), 1024, kHalves * 1024, 2), id_o,
+                                      st != c.st0 || k != 0);
                     }
                     tc_commit(bar(v_empty[b]));
                 }
