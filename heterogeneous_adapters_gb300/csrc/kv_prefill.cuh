@@ -135,8 +135,9 @@ template <int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kTile = kv_tile_bytes(D, D), kHalves = D / 64;
     constexpr PreSmem L = pre_smem(D);
-    // tensor memory: S twice (X of tokens 0-63 in a buffer's columns 0-31, of 64-127 in 64-95), O
-    constexpr uint32_t kSCol = 0, kOCol = 256;
+    // tensor memory: S three times (X of tokens 0-63 in a buffer's columns 0-31, of 64-127 in
+    // 64-95), so that S of the next block need not wait for X W of the block before; O
+    constexpr uint32_t kSCol = 0, kOCol = 384;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t code_full[2], code_empty[2], k_full[2], v_full[2], v_empty[2], s_full[2],
         x_full, q_full, o_empty, final_bar;
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             qs = half ? qo + qs : qs + qo;              // the same sum for both
             float m = kNoRef, l = 0.f;
             for (int st = c.st0; st < c.st1; ++st, ++n) {
-                const uint32_t b = n & 1, sb = lanes + kSCol + b * 128 + half * 64;
+                const uint32_t b = n & 1, sb = lanes + kSCol + n % 3 * 128 + half * 64;
                 const uint32_t table = sm + L.table + (n & 3) * kPreTable + half * 256;
                 const int tok0 = st * kPreStep + half * 64;
                 wait(s_full[b], (n >> 1) & 1);
@@ -274,23 +275,25 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     const uint64_t qs2 = pack2f(qs, qs), ref2 = pack2f(-m, -m);
                     float top = 0.f;
                     uint64_t sum2 = 0;
+                    float t[2][16];
+                    tmem_ld16(sb, t[0]);
 #pragma unroll
-                    for (int j0 = 0; j0 < 64; j0 += 32) {
-                        float t[32];
-                        tmem_ld32(sb + j0, t);
+                    for (int j0 = 0; j0 < 64; j0 += 16) {
                         tmem_ld_wait();
+                        if (j0 < 48) tmem_ld16(sb + j0 + 16, t[j0 / 16 + 1 & 1]);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
+                        for (int j = 0; j < 16; j += 4) {
                             const ulonglong2 k = lds2x64(table + (j0 + j) * 4), kq = lds2x64(table + (kPreStep + j0 + j) * 4),
                                              sc = lds2x64(table + (2 * kPreStep + j0 + j) * 4);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const uint64_t e = fma2(h ? k.y : k.x, pack2f(t[j + 2 * h], t[j + 2 * h + 1]), fma2(h ? kq.y : kq.x, qs2, ref2));
+                                const float* s = t[j0 / 16 & 1] + j + 2 * h;
+                                const uint64_t e = fma2(h ? k.y : k.x, pack2f(s[0], s[1]), fma2(h ? kq.y : kq.x, qs2, ref2));
                                 float e0, e1, x0, x1;
                                 unpack2f(e, e0, e1);
                                 if (masked) {
                                     const int tok = tok0 + j0 + j + 2 * h;
-                                    const bool in = here >> ((j0 + j) / 16) & 1;
+                                    const bool in = here >> (j0 / 16) & 1;
                                     if (tok > last || !in) e0 = -INFINITY;
                                     if (tok + 1 > last || !in) e1 = -INFINITY;
                                 }
@@ -505,31 +508,34 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1);
             uint32_t parts = 0;
-            // S of block i, in the place of X of block i - 2, whose X W has to be done
-            auto scores = [&](uint32_t i) {
+            // S of block i, in the place of X of block i - 3, whose X W has to be done; `past`: the
+            // last block whose X W was issued into that barrier (i - 3, or i - 1 at a part's start,
+            // where every block before has been issued)
+            auto scores = [&](uint32_t i, uint32_t past) {
                 const uint32_t b = i & 1, ph = (i >> 1) & 1;
-                if (!mbar_wait_quiet(bar(k_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) return false;
+                if (!mbar_wait_quiet(bar(k_full[b]), ph, kWaitLimitNs) ||
+                    (i > 2 && !mbar_wait_quiet(bar(v_empty[past & 1]), (past >> 1) & 1, kWaitLimitNs))) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc_mma_f16(tmem + kSCol + b * 128, smem_desc(sm + L.q + (k / 4) * (kPreRows * 128) + (k % 4) * 32, 16, 1024, 2),
+                    tc_mma_f16(tmem + kSCol + i % 3 * 128, smem_desc(sm + L.q + (k / 4) * (kPreRows * 128) + (k % 4) * 32, 16, 1024, 2),
                                smem_desc(sm + L.k + b * (kPreStep * D * 2) + (k / 4) * (kPreStep * 128) + (k % 4) * 32, 16, 1024, 2), id_s,
                                k != 0);
                 tc_commit(bar(s_full[b]));
                 return true;
             };
             while (ok && walk.next(v, p.rep, c)) {
-                if (!mbar_wait_quiet(bar(q_full), parts & 1, kWaitLimitNs) || !scores(n)) { ok = false; break; }
+                if (!mbar_wait_quiet(bar(q_full), parts & 1, kWaitLimitNs) || !scores(n, n - 1)) { ok = false; break; }
                 for (int st = c.st0; st < c.st1; ++st, ++n) {
                     const uint32_t b = n & 1, ph = (n >> 1) & 1;
-                    if (st + 1 < c.st1 && !scores(n + 1)) { ok = false; break; }
+                    if (st + 1 < c.st1 && !scores(n + 1, n - 2)) { ok = false; break; }
                     if (!mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(x_full), n & 1, kWaitLimitNs)) { ok = false; break; }
                     // the part before has been read out of O
                     if (st == c.st0 && !mbar_wait_quiet(bar(o_empty), (parts & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < kPreStep / 16; ++k) {
-                        tc_mma_f16_ts(tmem + kOCol, tmem + kSCol + b * 128 + (k / 4) * 64 + k % 4 * 8,
+                        tc_mma_f16_ts(tmem + kOCol, tmem + kSCol + n % 3 * 128 + (k / 4) * 64 + k % 4 * 8,
                                       smem_desc(sm + L.v + b * (kPreStep * D * 2) + k * (kHalves * 2048), 1024, kHalves * 1024, 2), id_o,
                                       st != c.st0 || k != 0);
                     }
