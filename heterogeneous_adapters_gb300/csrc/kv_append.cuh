@@ -23,9 +23,10 @@ struct AppendParams {
 // all of them turn by the same angles, read once per row.  A lane's partner values of the
 // halves style are whole pieces of another lane.  What bounds it is the stream of q, k and v;
 // a step is a few hundred clocks of work behind a load, so a warp has kAppendBatch steps'
-// loads in flight.
+// loads in flight.  Three CTAs an SM with four loads measured 51 us on 8.7k prompt rows (197
+// MB, 58% of the copy rate), two CTAs 59, four (64 registers) 61, four with two loads 56.
 template <int D, int G>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendWarps * 32, 3) kv_append_kernel(const __grid_constant__ AppendParams p) {
     constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
     const int lane = threadIdx.x & 31;
     const int sub = lane / kLanes, piece = lane % kLanes, d0 = piece * 8;

@@ -79,10 +79,10 @@ KvView view_of(const lora_kv_cache_desc* c, const lora_kv_batch* b, void* ws) {
 }
 
 // Heads a warp of the row kernels (append, read) takes, in steps of 256 values: as few as
-// keep every SM's warp slots filled once, so that a single token still uses many warps, and
+// give every SM 32 warps, so that a single token still uses many warps, and
 // a prompt's rows read their angles and look their request up once for several heads.
 int steps_per_warp(const DeviceInfo* di, int T, int steps) {
-    const int64_t slots = (int64_t)di->sm_count * 64;
+    const int64_t slots = (int64_t)di->sm_count * 32;
     return (int)std::min<int64_t>(std::max<int64_t>((int64_t)T * steps / slots, 1), steps);
 }
 
