@@ -26,6 +26,18 @@ lora_status check_sizes(const lora_w4_problem* probs, int32_t nprob, int32_t T) 
 
 size_t workspace_bytes() { return align256(std::max(w4_workspace(2), wide_workspace(128))); }
 
+// Blocks of a CTA: an equal share of all, or whole row tiles where the largest share of them
+// is at most `join` blocks more (what joining a tile from parts costs a CTA).  Whole tiles
+// need one K for all projections.
+int32_t w4_per(const W4Params& p, int grid, int rows, int join) {
+    const int32_t share = (p.total + grid - 1) / grid;
+    const int32_t kb = p.prob[0].kblocks;
+    for (int32_t i = 1; i < p.nprob; ++i)
+        if (p.prob[i].kblocks != kb) return share;
+    const int32_t whole = (p.total / kb + grid - 1) / grid * kb;
+    return whole <= share + join ? whole : share;
+}
+
 template <int G, int NT>
 lora_status launch(W4Params& p, cudaStream_t s) {
     DeviceInfo* di = nullptr;
@@ -44,7 +56,7 @@ lora_status launch(W4Params& p, cudaStream_t s) {
         ready_dev = dev;
     }
     const int grid = std::min(di->sm_count * std::max(per_sm, 1), kW4MaxCtas);
-    p.per = (p.total + grid - 1) / grid;
+    p.per = w4_per(p, grid, kW4Rows, kW4JoinCost);
     kern<<<grid, kW4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
 }

@@ -1,10 +1,12 @@
 // y = x W^T with 4-bit weights and group scales, up to 16 rows of x a launch.
 //
-// A group's part of an output is  scale * sum_k (c - zero) x: the differences of codes and
-// zero point are whole numbers, exact in bf16, so the tensor core sums exact products and the
-// scale enters once per group in fp32.  The weights are the long side: 16 rows of W are an
-// MMA's rows and 8 rows of x its columns.  What bounds it is the stream of W (half a byte a
-// weight), next the unpacking (11 / 8 instructions a weight and lane).
+// A group's part of an output is  scale (sum_k (128 + c) x - (128 + zero) sum_k x): 128 + c is
+// the bf16 whose last mantissa bits are the code, so that a code costs 7 / 8 instructions on
+// its way to the tensor core (taking 128 + zero off each one would be 11 / 8), products are
+// exact, and a column of sums of x comes from one more MMA row tile of ones.  Sums of a
+// group are fp32 from zero: the 128s cost at most 2^-17 of sum |x w| per group.  The weights
+// are the long side: 16 rows of W are an MMA's rows and 8 rows of x its columns.  What bounds
+// it is the stream of W (half a byte a weight), next the unpacking.
 //
 // Work.  A block of work is 32 rows of W by 256 of K (4 KB of codes); blocks of all
 // projections lie in a row, K fastest, and the CTAs take equal contiguous ranges, a CTA's
@@ -27,7 +29,10 @@ constexpr int kW4Threads = kW4Warps * 32;
 constexpr int kW4NarrowRows = 16;  // rows of x up to which this kernel serves
 constexpr int kW4Rows = 32;        // rows of W of a block
 constexpr int kW4K = 256;          // K of a block (128 bytes of codes a row)
-constexpr int kW4Stages = 3;
+constexpr int kW4Stages = 2;
+// Blocks that joining a tile from several CTAs costs: one row of 4096 x 4096 9.9 us shared out
+// evenly (7 blocks a CTA), 7.8 by whole tiles (16).
+constexpr int kW4JoinCost = 16;
 constexpr int kW4MaxCtas = 512;
 static_assert(kW4MaxCtas <= kStepTickets, "a counter per CTA");
 
@@ -77,6 +82,11 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Block u of the launch, and steps of kW4Warps blocks from it.
+struct W4At {
+    int prob, row0, kb;
+};
+
 // The projection that holds block u.
 __device__ __forceinline__ int w4_prob_of(const W4Params& p, int u) {
     int i = 0;
@@ -95,35 +105,52 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_matvec_kernel(const __grid_c
     const int first = blockIdx.x * p.per, end = min(first + p.per, p.total);
     if (first >= end) return;
 
-    // copies of block u into a stage
+    // the block that is copied next
+    W4At nx = {0, 0, 0};
+    if (first + warp < end) {
+        nx.prob = w4_prob_of(p, first + warp);
+        const int b = first + warp - p.prob[nx.prob].first;
+        nx.row0 = b / p.prob[nx.prob].kblocks * kW4Rows;
+        nx.kb = b - nx.row0 / kW4Rows * p.prob[nx.prob].kblocks;
+    }
+    // copies of block u (at nx) into a stage, and nx eight blocks on
     auto put = [&](int u, uint32_t stage) {
         if (u < end) {
-            const W4Prob& pr = p.prob[w4_prob_of(p, u)];
-            const int b = u - pr.first, row0 = b / pr.kblocks * kW4Rows, kb = b % pr.kblocks;
+            const W4Prob& pr = p.prob[nx.prob];
             const uint32_t dst = ring + stage * kStage;
             const int half = pr.K / 2;                         // bytes of a row
-            const int col = (lane & 7) * 16, at = kb * 128 + col;
+            const int col = (lane & 7) * 16, at = nx.kb * 128 + col;
+            const unsigned char* src = pr.codes + (int64_t)(nx.row0 + (lane >> 3)) * half + at;
+            const int rows = at < half ? pr.N - nx.row0 - (lane >> 3) : 0;
+            const uint32_t to = dst + (lane >> 3) * 128;
+            // rows i * 4 + lane / 8: the swizzle of row r is r % 8, which alternates with i
+            const uint32_t c0 = col ^ ((lane >> 3) << 4), c1 = col ^ ((lane >> 3) + 4) << 4;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int r = i * 4 + (lane >> 3), row = row0 + r;
-                const bool in = row < pr.N && at < half;
-                cp_async16(dst + r * 128 + (col ^ ((r & 7) << 4)), pr.codes + (in ? (int64_t)row * half + at : 0), in ? 16 : 0);
+                cp_async16(to + i * 512 + (i & 1 ? c1 : c0), rows > i * 4 ? src : pr.codes, rows > i * 4 ? 16 : 0);
+                src += 4 * (int64_t)half;
             }
 #pragma unroll
             for (int j0 = 0; j0 < kGroups * 8; j0 += 32) {     // per group 4 pieces of scales, 4 of zeros
                 const int j = j0 + lane, gr = j >> 3, piece = j & 3;
-                const int grp = kb * kGroups + gr;
+                const int grp = nx.kb * kGroups + gr;
                 if (kGroups * 8 >= 32 || j < kGroups * 8) {
-                    const bool in = grp * G < pr.K;
-                    if (!(j & 4)) {
-                        const bool ok = in && row0 + piece * 8 < pr.N;
+                    const bool ok = grp * G < pr.K && nx.row0 + piece * 8 < pr.N;
+                    if (!(j & 4))
                         cp_async16(dst + kW4Codes + gr * 64 + piece * 16,
-                                   pr.scales + (ok ? ((int64_t)grp * pr.N + row0 + piece * 8) * 2 : 0), ok ? 16 : 0);
-                    } else if (pr.zeros) {
-                        const bool ok = in && row0 + piece * 8 < pr.N;
+                                   pr.scales + (ok ? ((int64_t)grp * pr.N + nx.row0 + piece * 8) * 2 : 0), ok ? 16 : 0);
+                    else if (pr.zeros)
                         cp_async4(dst + kW4Codes + kGroups * 64 + gr * 16 + piece * 4,
-                                  pr.zeros + (ok ? (int64_t)grp * (pr.N / 2) + row0 / 2 + piece * 4 : 0), ok ? 4 : 0);
-                    }
+                                  pr.zeros + (ok ? (int64_t)grp * (pr.N / 2) + nx.row0 / 2 + piece * 4 : 0), ok ? 4 : 0);
+                }
+            }
+            nx.kb += kW4Warps;
+            while (nx.kb >= p.prob[nx.prob].kblocks && u + kW4Warps < end) {
+                nx.kb -= p.prob[nx.prob].kblocks;
+                nx.row0 += kW4Rows;
+                if (nx.row0 >= p.prob[nx.prob].N) {
+                    nx.row0 = 0;
+                    ++nx.prob;
                 }
             }
         }
@@ -148,54 +175,69 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_matvec_kernel(const __grid_c
         for (; u < stop; u += kW4Warps, ++it) {
             const int k0 = (u - tile_first) * kW4K;
             put(u + (kW4Stages - 1) * kW4Warps, (it + kW4Stages - 1) % kW4Stages);
-            // this lane's x: row 8 n + g, eight values of every 32
-            uint4 xr[NT][8];
+            // this lane's x of a group: row 8 n + g, eight values of every 32
+            uint4 xr[NT][G / 32];
+            auto load_x = [&](int gr) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int k = k0 + c * 32 + t * 8;
-                    xr[n][c] = n * 8 + g < p.T && k < pr.K ? ld16(pr.x + (n * 8 + g) * pr.ldx + k) : make_uint4(0, 0, 0, 0);
-                }
+                    for (int c = 0; c < G / 32; ++c) {
+                        const int k = k0 + gr * G + c * 32 + t * 8;
+                        xr[n][c] = n * 8 + g < p.T && k < pr.K ? ld16(pr.x + (n * 8 + g) * pr.ldx + k) : make_uint4(0, 0, 0, 0);
+                    }
+            };
+            load_x(0);
             cp_async_wait<kW4Stages - 1>();
             __syncwarp();
             const uint32_t st = ring + (it % kW4Stages) * kStage;
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
-                // scales and zero points of rows g, g + 8, g + 16, g + 24
-                float sc[4];
-                uint32_t minus[4];
+                // scales and 128 + zero of rows g, g + 8, g + 16, g + 24
+                float sc[4], zf[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     unsigned short h;
                     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(st + kW4Codes + gr * 64 + (r * 8 + g) * 2));
                     sc[r] = __half2float(__ushort_as_half(h));
-                    minus[r] = kMinus8;
+                    zf[r] = 136.f;
                     if (pr.zeros) {
                         uint32_t z;
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z) : "r"(st + kW4Codes + kGroups * 64 + gr * 16 + r * 4));
-                        minus[r] = 0x43004300u + ((z >> (4 * g)) & 15u) * 0x00010001u;
+                        zf[r] = __uint_as_float((z >> (4 * g) & 15u) << 16 | 0x43000000u);
                     }
                 }
-                float s[2][NT][4];
+                float s[2][NT][4], sx[NT][4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int n = 0; n < NT; ++n) {
+                    sx[n][0] = sx[n][1] = sx[n][2] = sx[n][3] = 0.f;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
+                    for (int m = 0; m < 2; ++m) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
+                }
 #pragma unroll
                 for (int c = gr * (G / 32); c < (gr + 1) * (G / 32); ++c) {
+                    uint32_t xb[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const uint4 x = xr[n][c - gr * (G / 32)];
+                        xb[n][0] = __byte_perm(x.x, x.z, 0x5410);
+                        xb[n][1] = __byte_perm(x.x, x.z, 0x7632);
+                        xb[n][2] = __byte_perm(x.y, x.w, 0x5410);
+                        xb[n][3] = __byte_perm(x.y, x.w, 0x7632);
+                        const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+                        mma16816(sx[n], ones, xb[n][0], xb[n][1]);
+                        mma16816(sx[n], ones, xb[n][2], xb[n][3]);
+                    }
                     uint32_t w[4];
                     ldmatrix4(w, st + lane * 128 + ((c ^ (lane & 7)) << 4));
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const uint32_t w0 = w[2 * m], w1 = w[2 * m + 1], z0 = minus[2 * m], z1 = minus[2 * m + 1];
-                        const uint32_t a0[4] = {code_pair<0>(w0, z0), code_pair<0>(w1, z1), code_pair<1>(w0, z0), code_pair<1>(w1, z1)};
-                        const uint32_t a1[4] = {code_pair<2>(w0, z0), code_pair<2>(w1, z1), code_pair<3>(w0, z0), code_pair<3>(w1, z1)};
+                        const uint32_t w0 = w[2 * m], w1 = w[2 * m + 1];
+                        const uint32_t a0[4] = {code_plus<0>(w0), code_plus<0>(w1), code_plus<1>(w0), code_plus<1>(w1)};
+                        const uint32_t a1[4] = {code_plus<2>(w0), code_plus<2>(w1), code_plus<3>(w0), code_plus<3>(w1)};
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint4 x = xr[n][c];
-                            mma16816(s[m][n], a0, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632));
-                            mma16816(s[m][n], a1, __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                            mma16816(s[m][n], a0, xb[n][0], xb[n][1]);
+                            mma16816(s[m][n], a1, xb[n][2], xb[n][3]);
                         }
                     }
                 }
@@ -204,7 +246,11 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_matvec_kernel(const __grid_c
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[m][n][j] = fmaf(sc[2 * m + (j >> 1)], s[m][n][j], acc[m][n][j]);
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 2 * m + (j >> 1);
+                            acc[m][n][j] = fmaf(sc[r], fmaf(-zf[r], sx[n][j & 1], s[m][n][j]), acc[m][n][j]);
+                        }
+                if (gr + 1 < kGroups) load_x(gr + 1);
             }
             __syncwarp();                                      // the stage may be filled again
         }
