@@ -237,9 +237,9 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                 const int c = turn;
                 const uint32_t i = kSpan == kWideK ? ic : 2 * ic + c, b = i % kSpans;   // span
                 const uint32_t acol = tmem + lane_base + kACol + b * (kSpan / 2) + (kSpan == kWideK ? c * 64 : 0);
+                uint32_t out[2][32];                               // 64 of K: 32 columns of tensor memory
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {                      // 64 of K: 32 columns of tensor memory
-                    uint32_t out[32];
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int col = c * 4 + h * 2 + j;         // 16-byte column of the row
@@ -252,18 +252,15 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                                          : "r"(params0 + s * kParams + kBlockGroups * kWideRows * 2 + g * (kWideRows / 2) + r / 2));
                             m = 0x43004300u + (z >> (r & 1) * 4 & 15u) * 0x00010001u;
                         }
-                        codes_in_order(w.x, m, out + j * 16);
-                        codes_in_order(w.y, m, out + j * 16 + 4);
-                        codes_in_order(w.z, m, out + j * 16 + 8);
-                        codes_in_order(w.w, m, out + j * 16 + 12);
+                        codes_in_order(w.x, m, out[h] + j * 16);
+                        codes_in_order(w.y, m, out[h] + j * 16 + 4);
+                        codes_in_order(w.z, m, out[h] + j * 16 + 8);
+                        codes_in_order(w.w, m, out[h] + j * 16 + 12);
                     }
-                    if (h == 0) {
-                        if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((i / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-                        tc_fence_after();
-                    }
-                    tmem_st32(acol + h * 32, out);
-                }
-                if (!ok) break;
+                if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((i / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                tc_fence_after();
+                tmem_st32(acol, out[0]);
+                tmem_st32(acol + 32, out[1]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
