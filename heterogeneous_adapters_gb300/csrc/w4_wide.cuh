@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
     // d_full[set % kDone]; the commit of a span's last set also says that its A buffer and x
     // stage are free.
     constexpr uint32_t kDCols = 128, kACol = 256;
-    constexpr int kDone = kSpans * kSets;
+    constexpr int kDone = kSpans * kSets, kJoin = N > 64 ? 16 : 32;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t code_full[kCodeStages], code_empty[kCodeStages], a_full[kSpans], d_full[kDone], d_empty[2],
         join, final_bar;
@@ -237,6 +237,17 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                 const int c = turn;
                 const uint32_t i = kSpan == kWideK ? ic : 2 * ic + c, b = i % kSpans;   // span
                 const uint32_t acol = tmem + lane_base + kACol + b * (kSpan / 2) + (kSpan == kWideK ? c * 64 : 0);
+                uint32_t minus[128 / G];                           // 128 + zero twice, of the row's groups
+#pragma unroll
+                for (int g = 0; g < 128 / G; ++g) {
+                    minus[g] = kMinus8;
+                    if (zeros) {
+                        uint32_t z;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z)
+                                     : "r"(params0 + s * kParams + kBlockGroups * kWideRows * 2 + (c * (128 / G) + g) * (kWideRows / 2) + r / 2));
+                        minus[g] = 0x43004300u + (z >> (r & 1) * 4 & 15u) * 0x00010001u;
+                    }
+                }
                 uint32_t out[2][32];                               // 64 of K: 32 columns of tensor memory
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -244,14 +255,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                     for (int j = 0; j < 2; ++j) {
                         const int col = c * 4 + h * 2 + j;         // 16-byte column of the row
                         const uint4 w = lds128(codes0 + s * kWideCodeBytes + r * 128 + ((col ^ (r & 7)) << 4));
-                        uint32_t m = kMinus8;
-                        if (zeros) {
-                            uint32_t z;
-                            const int g = (c * 128 + h * 64 + j * 32) / G;
-                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z)
-                                         : "r"(params0 + s * kParams + kBlockGroups * kWideRows * 2 + g * (kWideRows / 2) + r / 2));
-                            m = 0x43004300u + (z >> (r & 1) * 4 & 15u) * 0x00010001u;
-                        }
+                        const uint32_t m = minus[(h * 64 + j * 32) / G];
                         codes_in_order(w.x, m, out[h] + j * 16);
                         codes_in_order(w.y, m, out[h] + j * 16 + 4);
                         codes_in_order(w.z, m, out[h] + j * 16 + 8);
@@ -312,7 +316,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                             tmem_ld16(tmem + lane_base + (id & 1) * kDCols + g * N + half * kMine + j, v);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) acc[j + i] = fmaf(s[g], v[i], acc[j + i]);
+                            for (int i = 0; i < 16; i += 2) fma2_f32(acc[j + i], acc[j + i + 1], s[g], v[i], v[i + 1]);
                         }
                     tc_fence_before();
                     __syncwarp();
@@ -365,7 +369,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                         const float* from = p.part + (((int64_t)c * 2 + (tile_first < c * p.per ? 0 : 1)) * N + half * kMine) * kWideRows + r;
 #pragma unroll
                         for (int j = 0; j < kMine; ++j) {
-                            if (j % 8 == 0) asm volatile("" ::: "memory");     // eight loads at a time: registers
+                            if (j % kJoin == 0) asm volatile("" ::: "memory"); // so many loads at a time: registers
                             acc[j] += __ldcg(from + j * kWideRows);
                         }
                     }
