@@ -110,10 +110,9 @@ lora_status launch_wide(WideParams& w, cudaStream_t s) {
 }
 
 template <int G>
-lora_status launch_group(WideParams& w, cudaStream_t s) {
+lora_status launch_group(WideParams& w, bool narrow, cudaStream_t s) {
     const int T = w.p.T;
-    if (T <= 8) return launch<G, 1>(w.p, s);
-    if (T <= kW4NarrowRows) return launch<G, 2>(w.p, s);
+    if (narrow) return T <= 8 ? launch<G, 1>(w.p, s) : launch<G, 2>(w.p, s);
     if (T <= 32) return launch_wide<G, 32>(w, s);
     return T <= 64 ? launch_wide<G, 64>(w, s) : launch_wide<G, 128>(w, s);
 }
@@ -147,12 +146,19 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
     // one launch per group size of the call and 128 rows
     static_assert(kW4K == kWideK, "both kernels' blocks are 256 of K");
     static thread_local WideParams w;
+    DeviceInfo* di = nullptr;
+    if ((st = device_info(&di)) != LORA_OK) return st;
     for (const int32_t group : {32, 64, 128}) {
         for (int32_t t0 = 0; t0 < T; t0 += 128) {
             memset(&w, 0, sizeof w);
             W4Params& p = w.p;
             p.T = std::min(T - t0, 128);
-            const int32_t block_rows = p.T <= kW4NarrowRows ? kW4Rows : kWideRows;
+            int64_t wide_blocks = 0;
+            for (int32_t i = 0; i < nprob; ++i)
+                if (probs[i].group == group)
+                    wide_blocks += (int64_t)((probs[i].N + kWideRows - 1) / kWideRows) * ((probs[i].K + kWideK - 1) / kWideK);
+            const bool narrow = p.T <= 8 || (p.T <= kW4NarrowRows && wide_blocks < (int64_t)kW4WideBlocks * di->sm_count);
+            const int32_t block_rows = narrow ? kW4Rows : kWideRows;
             int64_t total = 0;
             for (int32_t i = 0; i < nprob; ++i) {
                 const lora_w4_problem& pr = probs[i];
@@ -179,7 +185,7 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
             p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kStepPartAt);
             w.err = &reinterpret_cast<WsHeader*>(ws)->err;
             cudaStream_t s = (cudaStream_t)stream;
-            st = group == 32 ? launch_group<32>(w, s) : group == 64 ? launch_group<64>(w, s) : launch_group<128>(w, s);
+            st = group == 32 ? launch_group<32>(w, narrow, s) : group == 64 ? launch_group<64>(w, narrow, s) : launch_group<128>(w, narrow, s);
             if (st != LORA_OK) return st;
         }
     }

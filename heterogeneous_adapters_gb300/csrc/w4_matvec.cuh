@@ -26,7 +26,11 @@ namespace lora {
 
 constexpr int kW4Warps = 8;
 constexpr int kW4Threads = kW4Warps * 32;
-constexpr int kW4NarrowRows = 16;  // rows of x up to which this kernel serves
+// Rows of x up to which this kernel serves: always up to 8, and up to 16 where an SM has fewer
+// than kW4WideBlocks blocks of w4_wide.cuh to itself, whose fixed part then weighs more (13
+// rows: 5 blocks an SM 11.6 us here and 13.8 there, 24 blocks 31.6 here and 27.9 there).
+constexpr int kW4NarrowRows = 16;
+constexpr int kW4WideBlocks = 8;
 constexpr int kW4Rows = 32;        // rows of W of a block
 constexpr int kW4K = 256;          // K of a block (128 bytes of codes a row)
 constexpr int kW4Stages = 2;

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
     // d_full[set % kDone]; the commit of a span's last set also says that its A buffer and x
     // stage are free.
     constexpr uint32_t kDCols = 128, kACol = 256;
-    constexpr int kDone = kSpans * kSets, kJoin = N > 64 ? 16 : 32;
+    constexpr int kDone = kSpans * kSets, kJoin = N > 64 ? 32 : 64;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t code_full[kCodeStages], code_empty[kCodeStages], a_full[kSpans], d_full[kDone], d_empty[2],
         join, final_bar;
@@ -123,6 +123,11 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         mbar_init(bar(join), kDrain);
         mbar_init(bar(final_bar), 1);
         fence_mbar_init();
+    }
+    if (tid == 0 || tid == 11 * 32) {          // the first tiles' descriptors
+        const int i = w4_prob_of(p, first);
+        if (tid == 0) prefetch_tmap(&prm.codes[i]);
+        else prefetch_tmap(&prm.x[i]);
     }
     if (warp == 1) {
         tmem_alloc(smem_addr(&tmem_slot), 512);
@@ -330,6 +335,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             if (!ok) break;
             // ---- the row tile's sums: y, or a part of them
             const bool whole = at == tile_first && stop == tile_end;
+            auto part_of = [&](int64_t slot) { return reinterpret_cast<float4*>(p.part + (slot * N + half * kMine) * kWideRows) + r; };
             // y's tile, [column][row of W], through shared memory and one bulk store (what lies
             // outside y is not written).  False on a timeout.
             auto store = [&]() {
@@ -350,9 +356,10 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             if (whole) {
                 if (!(ok = store())) break;
             } else {
-                float* part = p.part + (((int64_t)blockIdx.x * 2 + (tile_first < first ? 0 : 1)) * N + half * kMine) * kWideRows + r;
+                // a part lies [column / 4][row][4]
+                float4* part = part_of((int64_t)blockIdx.x * 2 + (tile_first < first ? 0 : 1));
 #pragma unroll
-                for (int j = 0; j < kMine; ++j) part[j * kWideRows] = acc[j];
+                for (int j = 0; j < kMine; j += 4) part[j / 4 * kWideRows] = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             }
             if (!whole) {
                 const int c0 = tile_first / p.per, c1 = (tile_end - 1) / p.per;
@@ -366,11 +373,15 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
 #pragma unroll
                     for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
                     for (int c = c0; c <= c1; ++c) {
-                        const float* from = p.part + (((int64_t)c * 2 + (tile_first < c * p.per ? 0 : 1)) * N + half * kMine) * kWideRows + r;
+                        const float4* from = part_of((int64_t)c * 2 + (tile_first < c * p.per ? 0 : 1));
 #pragma unroll
-                        for (int j = 0; j < kMine; ++j) {
-                            if (j % kJoin == 0) asm volatile("" ::: "memory"); // so many loads at a time: registers
-                            acc[j] += __ldcg(from + j * kWideRows);
+                        for (int j = 0; j < kMine; j += 4) {
+                            if (j % kJoin == 0) asm volatile("" ::: "memory"); // so many values in flight: registers
+                            const float4 x = __ldcg(from + j / 4 * kWideRows);
+                            acc[j] += x.x;
+                            acc[j + 1] += x.y;
+                            acc[j + 2] += x.z;
+                            acc[j + 3] += x.w;
                         }
                     }
                     if (!(ok = store())) break;
