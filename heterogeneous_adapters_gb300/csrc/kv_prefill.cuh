@@ -186,8 +186,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     PrePart c;
     uint32_t n = 0;              // blocks so far: n % 2 is the buffer, n / 2 the phase
 
+    // Registers: 576 threads start with 96; the unpacking warps give 24 each of theirs to the
+    // rows' (256 x 120 + 256 x 72 + 64 x 96 = 576 x 96).
     if (warp < 8) {
         // ------------------------------------------------------------------ rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
         const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t flags = sm + L.pair + 2 * kPreRows * 4 + quad * 16;
@@ -426,6 +429,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         }
     } else if (warp < 16) {
         // ------------------------------------------------------------------ unpacking: a token, half of its values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int tok = tid & 127, half = (tid - 256) >> 7;
         const float sl = p.scale * 1.44269504f;
         while (ok && walk.next(v, p.rep, c)) {
