@@ -32,11 +32,6 @@ struct WsHeader {
 };
 static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 
-// The calls of lora_kv.h and lora_w4.h keep arrival counters after the header, zero between
-// calls, and their partial results after those.
-constexpr int kStepTickets = 1024;
-constexpr size_t kStepPartAt = sizeof(WsHeader) + kStepTickets * 4;
-
 // Work item of the CUDA-core path: up to 4 rows of one adapter, with everything the
 // delta kernels need about it except the projection (48 bytes, read with 3 vector loads).
 struct Chunk {

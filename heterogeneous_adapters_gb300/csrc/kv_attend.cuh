@@ -33,7 +33,6 @@
 
 #include "kv_layout.cuh"
 #include "mma_legacy.cuh"
-#include "ptx.cuh"
 
 namespace lora {
 
@@ -269,6 +268,17 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
                 if (tile_b) bulk_g2s(wring + stage * kStage + kTile, tile_b, kTile, wbar + stage * 8);
             }
         };
+        // q's loads are under way while the tiles are looked up
+        uint4 qw[NT][kChunks];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = cur_r0 + n * 8 + g;
+            const bool live = n * 8 + g < width;
+            const __nv_bfloat16* src = p.q + (int64_t)(cq.row0 + (live ? r / p.rep : 0)) * p.ldq +
+                                       (int64_t)(cur_head * p.rep + (live ? r % p.rep : 0)) * D;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) qw[n][c] = live ? ld16(src + c * 32 + t * 8) : make_uint4(0, 0, 0, 0);
+        }
         for (int i = 0; i < min(kAttStages, mine_n); ++i) put(i, (it + i) % kAttStages);
 
         // ---- q as the right-hand operand, and its sums per group, both times 2^13 over the
@@ -278,16 +288,10 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
         int32_t last[NT][2];                            // last token of this lane's columns
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = cur_r0 + n * 8 + g;
-            const bool live = n * 8 + g < width;
-            const __nv_bfloat16* src = p.q + (int64_t)(cq.row0 + (live ? r / p.rep : 0)) * p.ldq +
-                                       (int64_t)(cur_head * p.rep + (live ? r % p.rep : 0)) * D;
-            uint4 w[kChunks];
             uint32_t big = 0;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-                w[c] = live ? ld16(src + c * 32 + t * 8) : make_uint4(0, 0, 0, 0);
-                const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                const uint32_t x[4] = {qw[n][c].x, qw[n][c].y, qw[n][c].z, qw[n][c].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) big = max(big, max(x[j] << 16 & 0x7F800000u, x[j] & 0x7F800000u));
             }
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
 #pragma unroll
                 for (int c = gr * kPerG; c < (gr + 1) * kPerG; ++c) {
                     float f[8];
-                    unpack8(w[c], f);
+                    unpack8(qw[n][c], f);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         f[j] *= up;

@@ -3,7 +3,7 @@
 #pragma once
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "step.cuh"
 #include "lora_kv.h"
 
 namespace lora {

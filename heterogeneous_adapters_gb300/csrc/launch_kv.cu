@@ -113,15 +113,14 @@ lora_status attend(const AttendParams& p, cudaStream_t s) {
     if (st != LORA_OK) return st;
     constexpr size_t smem = attend_smem(D, G);
     auto kern = kv_attend_kernel<D, G, NT>;
-    static thread_local int ready_dev = -1, per_sm = 0;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (ready_dev != dev) {
+    static thread_local const DeviceInfo* ready = nullptr;
+    static thread_local int per_sm = 0;
+    if (ready != di) {
         st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (st != LORA_OK) return st;
         st = cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kAttThreads, smem));
         if (st != LORA_OK) return st;
-        ready_dev = dev;
+        ready = di;
     }
     const int grid = std::min(di->sm_count * std::max(per_sm, 1), kAttMaxCtas);
     kern<<<grid, kAttThreads, smem, s>>>(p);
@@ -135,13 +134,11 @@ lora_status prefill(const AttendParams& p, cudaStream_t s) {
     if (st != LORA_OK) return st;
     constexpr size_t smem = pre_smem(D).total;
     auto kern = kv_prefill_kernel<D>;
-    static thread_local int ready_dev = -1;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (ready_dev != dev) {
+    static thread_local const DeviceInfo* ready = nullptr;
+    if (ready != di) {
         st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (st != LORA_OK) return st;
-        ready_dev = dev;
+        ready = di;
     }
     kern<<<std::min(di->sm_count, kPreMaxCtas), kPreThreads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());

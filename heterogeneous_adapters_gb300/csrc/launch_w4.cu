@@ -45,15 +45,14 @@ lora_status launch(W4Params& p, cudaStream_t s) {
     if (st != LORA_OK) return st;
     constexpr size_t smem = w4_smem(G, NT);
     auto kern = w4_matvec_kernel<G, NT>;
-    static thread_local int ready_dev = -1, per_sm = 0;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (ready_dev != dev) {
+    static thread_local const DeviceInfo* ready = nullptr;
+    static thread_local int per_sm = 0;
+    if (ready != di) {
         st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (st != LORA_OK) return st;
         st = cuda_status(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kW4Threads, smem));
         if (st != LORA_OK) return st;
-        ready_dev = dev;
+        ready = di;
     }
     const int grid = std::min(di->sm_count * std::max(per_sm, 1), kW4MaxCtas);
     p.per = w4_per(p, grid, kW4Rows, kW4JoinCost);
@@ -95,13 +94,11 @@ lora_status launch_wide(WideParams& w, cudaStream_t s) {
     }
     constexpr size_t smem = wide_smem(N, G);
     auto kern = w4_wide_kernel<G, N>;
-    static thread_local int ready_dev = -1;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (ready_dev != dev) {
+    static thread_local const DeviceInfo* ready = nullptr;
+    if (ready != di) {
         st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
         if (st != LORA_OK) return st;
-        ready_dev = dev;
+        ready = di;
     }
     const int grid = std::min(di->sm_count, kWideMaxCtas);
     w.p.per = (w.p.total + grid - 1) / grid;

@@ -17,10 +17,9 @@
 #pragma once
 #include <cuda_fp16.h>
 
-#include "common.cuh"
 #include "lora_w4.h"
 #include "mma_legacy.cuh"
-#include "ptx.cuh"
+#include "step.cuh"
 
 namespace lora {
 
