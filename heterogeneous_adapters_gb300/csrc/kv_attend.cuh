@@ -72,8 +72,12 @@ struct AttendParams {
 __host__ __device__ constexpr size_t attend_smem(int dim, int group) {
     return (size_t)kAttWarps * kAttStages * 2 * kv_tile_bytes(dim, group);
 }
-// CTAs of an SM that the registers are shared out for.
-__host__ __device__ constexpr int attend_ctas(int dim, int nt) { return nt == 1 ? 4 : dim == 128 ? 2 : 3; }
+// CTAs of an SM that the registers are shared out for: four of 128 a thread, fewer where the
+// step holds more (one query head per KV head with groups of 32: 96 us with four, 89.5 with
+// three).
+__host__ __device__ constexpr int attend_ctas(int dim, int group, int nt) {
+    return nt == 1 ? (dim == 128 && group == 32 ? 3 : 4) : dim == 128 ? 2 : 3;
+}
 // Bytes of workspace: header, tickets and partial results.
 __host__ __device__ constexpr size_t attend_part_floats(int nt, int dim) { return (size_t)2 * 8 * nt * (dim + 4); }
 __host__ __device__ constexpr size_t attend_workspace(int nt, int dim) {
@@ -188,7 +192,7 @@ __device__ __forceinline__ void att_store_lse(const AttendParams& p, int row, in
 }
 
 template <int D, int G, int NT>
-__global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kAttThreads, attend_ctas(D, G, NT)) kv_attend_kernel(const __grid_constant__ AttendParams p) {
     constexpr int kRows = 8 * NT, kChunks = D / 32, kGroups = D / G, kPerG = G / 32;
     constexpr int kTile = kv_tile_bytes(D, G), kStage = 2 * kTile, kPitch = D + 4;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -196,6 +200,7 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
     __shared__ int64_t scan[kAttWarps + 1];
     __shared__ int64_t found[2];
     __shared__ float stat[kAttWarps][kRows][2];
+    __shared__ float2 vscale[kAttWarps][32 * kGroups];
     __shared__ uint32_t last_in;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const KvView& v = p.v;
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
     int64_t item = found[1];                            // first unit of the item
     AttSeq q = att_seq(v, seq, false);
     const uint32_t wring = smem_addr(ring) + warp * kAttStages * kStage;
-    const uint32_t wbar = smem_addr(&bars[warp][0]);
+    const uint32_t wbar = smem_addr(&bars[warp][0]), vparams = smem_addr(&vscale[warp][0]);
     const int cap = (int)((int64_t)v.max_blocks * v.block_tokens);
     uint32_t it = 0;                                    // steps this warp has consumed
     uint32_t solos = 0;
@@ -412,20 +417,29 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, NT)) kv_attend_ker
                             if (tok > last[n][j & 1] || !(h ? has_b : has_a)) s[h][n][j] = -INFINITY;
                         }
             }
-            // ---- V's scales, and offsets in units of them
+            // ---- V's scales, and offsets in units of them: worked out once per token and group,
+            // (32 of them or 128 by the lanes), and read back by the lanes that need them
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int e = i * 32 + lane, h = e / (16 * kGroups), at = e % (16 * kGroups);
+                uint32_t w;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(base + h * kTile + kv_params_at(D, G, 1) + at * 4));
+                float2 q = __half22float2(*reinterpret_cast<__half2*>(&w));
+                q.x = fmaxf(fmaxf(q.x, fabsf(q.y) * kScaleOfOffset), kTinyScale);
+                q.y *= rcp_approx(q.x);
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(vparams + e * 8), "f"(q.x), "f"(q.y) : "memory");
+            }
+            __syncwarp();
             float2 vp[2][kGroups][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr) {
-                    att_params(vp[h][gr], base + h * kTile + kv_params_at(D, G, 1) + gr * 64 + g * 4);
+                for (int gr = 0; gr < kGroups; ++gr)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float2& q = vp[h][gr][e];
-                        q.x = fmaxf(fmaxf(q.x, fabsf(q.y) * kScaleOfOffset), kTinyScale);
-                        q.y *= rcp_approx(q.x);
-                    }
-                }
+                    for (int e = 0; e < 2; ++e)
+                        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                                     : "=f"(vp[h][gr][e].x), "=f"(vp[h][gr][e].y)
+                                     : "r"(vparams + ((h * kGroups + gr) * 16 + e * 8 + g) * 8));
             // ---- probabilities, and with each group's scale the right-hand operand of V
             uint32_t pb[2][NT][kGroups][2];
 #pragma unroll
