@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     constexpr uint32_t kSCol = 0, kOCol = 384;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t code_full[2], code_empty[2], k_full[2], v_full[2], v_empty[2], s_full[2],
-        x_full, q_full, o_empty, final_bar;
+        x_full[2], q_full, o_empty, final_bar;
     __shared__ int64_t scan[kPreThreads / 32 + 1], found[2];
     __shared__ uint32_t tmem_slot, last_in;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             mbar_init(bar(v_full[i]), 8);
             mbar_init(bar(v_empty[i]), 1);
             mbar_init(bar(s_full[i]), 1);
+            mbar_init(bar(x_full[i]), 8);
         }
-        mbar_init(bar(x_full), 8);
         mbar_init(bar(q_full), 8);
         mbar_init(bar(o_empty), 8);
         mbar_init(bar(final_bar), 1);
@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(x_full));
+                // (two in turn: rows that need no new reference are a block ahead of others by then)
+                if (lane == 0) mbar_arrive(bar(x_full[b]));
             }
             const float lo = exchange(l);
             l = half ? lo + l : l + lo;
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 for (int st = c.st0; st < c.st1; ++st, ++n) {
                     const uint32_t b = n & 1, ph = (n >> 1) & 1;
                     if (st + 1 < c.st1 && !scores(n + 1, n - 2)) { ok = false; break; }
-                    if (!mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(x_full), n & 1, kWaitLimitNs)) { ok = false; break; }
+                    if (!mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(x_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
                     // the part before has been read out of O
                     if (st == c.st0 && !mbar_wait_quiet(bar(o_empty), (parts & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
                     tc_fence_after();

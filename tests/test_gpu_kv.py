@@ -99,14 +99,15 @@ class Case:
                        self.ws, self.size, self.stream)
         return out, ls
 
-    def fill(self, gain=1.0):
-        """Every token of every request appended (a call with all of them as rows)."""
+    def fill(self, gain=1.0, k=None):
+        """Every token of every request appended (a call with all of them as rows), with random K or the given."""
         total = sum(max(n, 0) for n in self.lens)
         t = self.torch
         start = t.tensor(np.concatenate([[0], np.cumsum([max(n, 0) for n in self.lens])]), dtype=t.int32, device="cuda")
         lens = self.kv_len.clamp(min=0).int()
         batch = lora.KvBatch(start, lens, self.table, self.n, total, self.max_blocks, max(max(self.lens), 0))
-        k, v = self.normal(total, self.kv_heads * self.dim, gain=gain), self.normal(total, self.kv_heads * self.dim)
+        k = self.normal(total, self.kv_heads * self.dim, gain=gain) if k is None else k
+        v = self.normal(total, self.kv_heads * self.dim)
         lora.kv_append(self.kv, batch, None, 0, None, 0, 0, k, k.shape[1], v, v.shape[1], self.rope(0), self.ws, self.size, self.stream)
 
     def check_attend(self, q, out, lse, scale=None):
@@ -309,6 +310,26 @@ def test_attend_chunk_of_a_prompt(cuda):
     case = Case([150, 1, 37, 1], [290, 500, 37, 3], heads=8, kv_heads=2, block=32, seed=6)
     case.fill()
     q = case.normal(case.T, 8 * 128)
+    out, lse = case.attend(q)
+    assert case.error() == 0
+    case.check_attend(q, out, lse)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("which", [0, 2])
+def test_attend_chunk_where_some_rows_rise_with_every_block(cuda, dim, which):
+    """Eight rows' scores rise by 8 with every 128 tokens and the others' stay: rows that take a
+    new reference at every block beside rows that never do."""
+    case = Case([32, 24], [2048, 1500], heads=8, kv_heads=2, dim=dim, group=dim, block=32, seed=8)
+    d = cuda.where(cuda.arange(dim, device="cuda") % 2 == 0, 1.0, -1.0) * dim ** -0.5
+    at = cuda.cat([cuda.arange(n, device="cuda") for n in case.lens]) // 128
+    k = case.normal(sum(case.lens), 2, dim, gain=0.5).float() + (at * 8.0)[:, None, None] * d * dim ** 0.5 / 32.0
+    case.fill(k=k.bfloat16().reshape(-1, 2 * dim))
+    q = case.normal(case.T, 8, dim).float()
+    for first in (0, 32):
+        rows = slice(first + 8 * which, first + 8 * which + 8)
+        q[rows] = 32.0 * d + 0.25 * q[rows]
+    q = q.bfloat16().reshape(case.T, 8 * dim)
     out, lse = case.attend(q)
     assert case.error() == 0
     case.check_attend(q, out, lse)
