@@ -170,7 +170,9 @@ struct ReadParams {
     int32_t per_warp;
 };
 
-// The stored values of the batch's rows, laid out as the append reads them.
+// The stored values of the batch's rows, laid out as the append reads them: 15 us for 8.7k rows
+// of 8 heads (55 MB, from L2 after the append; 55% of the copy rate, instructions at 66% of the
+// issue slots).
 template <int D, int G>
 __global__ void __launch_bounds__(kAppendWarps * 32) kv_read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int kLanes = D / 8, kHeads = 32 / kLanes, kTileBytes = kv_tile_bytes(D, G);

@@ -12,10 +12,15 @@
 // reference M is moved, and O multiplied, only when a p v_t exceeds 2^10.
 //
 // Warps 0-7 hold half of a row a thread (64 of a block's tokens, half of the output): they
-// bring q, turn S into X and write the output.  Warps 8-15 unpack a block's codes into the operands' swizzled rows (within eight values in the order
-// 0 4 1 5 2 6 3 7, q alike, and the output put back).  Warp 16 issues the MMAs, S of the next
-// block before X W of this one; warp 17 brings the codes.  A block costs 1024 clocks of MMA
-// and as many of exponentials.  Tiles are dealt, split and joined as kv_attend.cuh's items.
+// bring q, turn S into X and write the output.  Warps 8-15 unpack a block's codes into the
+// operands' swizzled rows (within eight values in the order 0 4 1 5 2 6 3 7, q alike, and the
+// output put back).  Warp 16 issues the MMAs, S of the next block before X W of this one; warp
+// 17 brings the codes.  Tiles are dealt, split and joined as kv_attend.cuh's items.
+//
+// A block costs 1024 clocks of MMA and as many of exponentials, but takes about 3300: some
+// 7,400 instructions (rows 3,600, unpacking 2,750) at 55% of the issue slots.  Three requests
+// of 400 to 512 rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 146 us for
+// 89 GFLOP, 32% of the measured bf16 rate.
 #pragma once
 #include "kv_attend.cuh"
 
@@ -25,7 +30,9 @@ constexpr int kPreRows = 128, kPreStep = 128, kPreThreads = 18 * 32;
 constexpr int kPreItemCost = 3;      // blocks' worth of a tile's fixed part
 constexpr int kPreMinUnits = 4;
 constexpr int kPreMaxCtas = 192;
-// A request's packed rows per KV head from which this kernel serves it.
+// A request's packed rows per KV head from which this kernel serves it.  16 requests over 4000
+// tokens: 32 rows 56 us in kv_attend.cuh and 66 here, 48 rows 77 and 67, 64 rows 95 and 66 (heads
+// of 64: 48 rows 32 and 37, 64 rows 41 and 38).
 constexpr int kPreMinPacked = 48;
 
 constexpr int kPreTable = 3 * kPreStep * 4 + 16;

@@ -6,7 +6,9 @@
 // exact, and a column of sums of x comes from one more MMA row tile of ones.  Sums of a
 // group are fp32 from zero: the 128s cost at most 2^-17 of sum |x w| per group.  The weights
 // are the long side: 16 rows of W are an MMA's rows and 8 rows of x its columns.  What bounds
-// it is the stream of W (half a byte a weight), next the unpacking.
+// it is the stream of W (half a byte a weight), next the unpacking: one row of 4096 x 4096 takes
+// 7.8 us (two of launch, three to the first data), of two 14336 x 4096 21.8 us, 41% of the copy
+// rate, where the copies alone take 12.6 and the products alone 16.
 //
 // Work.  A block of work is 32 rows of W by 256 of K (4 KB of codes); blocks of all
 // projections lie in a row, K fastest, and the CTAs take equal contiguous ranges, a CTA's

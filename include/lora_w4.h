@@ -43,7 +43,7 @@ typedef struct {
 lora_status lora_w4_workspace_size(const lora_w4_problem* probs, int32_t nprob, int32_t T, size_t* bytes);
 
 /* All projections of the call, at most LORA_W4_MAX_PROBLEMS, over the same T <=
- * LORA_W4_MAX_ROWS rows (their x may differ), in one launch per group size. */
+ * LORA_W4_MAX_ROWS rows (their x may differ), in one launch per group size and 128 rows. */
 lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
                            void* stream);
 
