@@ -19,7 +19,7 @@
 //
 // A block costs 1024 clocks of MMA and as many of exponentials, but takes about 3300: some
 // 7,400 instructions (rows 3,600, unpacking 2,750) at 55% of the issue slots.  Three requests
-// of 400 to 512 rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 146 us for
+// of 300 to 512 rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 146 us for
 // 89 GFLOP, 32% of the measured bf16 rate.
 #pragma once
 #include "kv_attend.cuh"

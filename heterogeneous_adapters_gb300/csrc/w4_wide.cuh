@@ -1,4 +1,4 @@
-// y = x W^T with 4-bit weights for 17 rows of x and more (up to 128 a launch).
+// y = x W^T with 4-bit weights for more rows of x than w4_matvec.cuh takes (up to 128 a launch).
 //
 // The same sums as w4_matvec.cuh (exact differences of codes and zero points, one scale per
 // group in fp32), with the fifth-generation tensor cores: 128 rows of W are the M of a
