@@ -193,18 +193,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
     PrePart c;
     uint32_t n = 0;              // blocks so far: n % 2 is the buffer, n / 2 the phase
 
-    // Registers: 576 threads start with 96; the unpacking warps give 24 each of theirs to the
-    // rows' (256 x 120 + 256 x 72 + 64 x 96 = 576 x 96).
+    // Registers: 576 threads start with 96; the unpacking warps give 40 each of theirs to the
+    // rows' (256 x 136 + 256 x 56 + 64 x 96 = 576 x 96).
     if (warp < 8) {
         // ------------------------------------------------------------------ rows
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
         const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t flags = sm + L.pair + 2 * kPreRows * 4 + quad * 16;
         // These warps meet at named barriers, so none of them leaves early: after a wait that ran
         // out, `wait` returns at once and the rest of the range goes by (with the error set).
         auto wait = [&](uint64_t& which, uint32_t parity) {
-            if (ok && !mbar_wait_quiet(bar(which), parity, kWaitLimitNs)) {
+            if (ok && !mbar_wait(bar(which), parity, kWaitLimitNs)) {
                 ok = false;
                 if (lane == 0) set_error(v.err, LORA_DERR_TIMEOUT);
             }
@@ -437,17 +437,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         }
     } else if (warp < 16) {
         // ------------------------------------------------------------------ unpacking: a token, half of its values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int tok = tid & 127, half = (tid - 256) >> 7;
         const float sl = p.scale * 1.44269504f;
         while (ok && walk.next(v, p.rep, c)) {
             for (int st = c.st0; st < c.st1; ++st, ++n) {
                 const uint32_t b = n & 1, ph = (n >> 1) & 1;
-                if (!mbar_wait_quiet(bar(code_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait(bar(code_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
                 const uint32_t src = sm + L.codes + b * pre_code_bytes(D) + (tok / kKvTile) * kTile;
                 const uint32_t at = src + (tok % kKvTile) * 16;
                 // the buffer's last S is done (and with it the rows' use of the table four blocks ago)
-                if (!mbar_wait_quiet(bar(s_full[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait(bar(s_full[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
                 // K: 16-byte pieces of 32 values; a row of 64 values is 128 bytes, swizzled
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(k_full[b]));
-                if (!mbar_wait_quiet(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
                 // W: rows of tokens, [token / 8][64 values][token % 8]
                 const __half hi = __float2half_rn(here ? r : 0.f);
                 const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(__float2half_rn((here ? r : 0.f) - __half2float(hi)));
@@ -520,37 +520,37 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         if (lane == 0) {
             constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1);
             uint32_t parts = 0;
-            // S of block i, in the place of X of block i - 3, whose X W has to be done; `past`: the
-            // last block whose X W was issued into that barrier (i - 3, or i - 1 at a part's start,
-            // where every block before has been issued)
-            auto scores = [&](uint32_t i, uint32_t past) {
-                const uint32_t b = i & 1, ph = (i >> 1) & 1;
-                if (!mbar_wait_quiet(bar(k_full[b]), ph, kWaitLimitNs) ||
-                    (i > 2 && !mbar_wait_quiet(bar(v_empty[past & 1]), (past >> 1) & 1, kWaitLimitNs))) return false;
+            const uint64_t q_desc = smem_desc(sm + L.q, 16, 1024, 2), k_desc = smem_desc(sm + L.k, 16, 1024, 2),
+                           w_desc = smem_desc(sm + L.v, 1024, kHalves * 1024, 2);
+            // S of block i, in the place of X of block i - 3.  K of block i comes after V of i - 1,
+            // and that after X W of i - 3: one wait stands for all of them.
+            auto scores = [&](uint32_t i) {
+                const uint32_t b = i & 1, d = tmem + kSCol + i % 3 * 128;
+                const uint64_t kb = desc_at(k_desc, b * (kPreStep * D * 2));
+                if (!mbar_wait_quiet(bar(k_full[b]), (i >> 1) & 1, kWaitLimitNs)) return false;
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc_mma_f16(tmem + kSCol + i % 3 * 128, smem_desc(sm + L.q + (k / 4) * (kPreRows * 128) + (k % 4) * 32, 16, 1024, 2),
-                               smem_desc(sm + L.k + b * (kPreStep * D * 2) + (k / 4) * (kPreStep * 128) + (k % 4) * 32, 16, 1024, 2), id_s,
-                               k != 0);
+                    tc_mma_f16(d, desc_at(q_desc, (k / 4) * (kPreRows * 128) + (k % 4) * 32),
+                               desc_at(kb, (k / 4) * (kPreStep * 128) + (k % 4) * 32), id_s, k != 0);
                 tc_commit(bar(s_full[b]));
                 return true;
             };
             while (ok && walk.next(v, p.rep, c)) {
-                if (!mbar_wait_quiet(bar(q_full), parts & 1, kWaitLimitNs) || !scores(n, n - 1)) { ok = false; break; }
+                if (!mbar_wait_quiet(bar(q_full), parts & 1, kWaitLimitNs) || !scores(n)) { ok = false; break; }
                 for (int st = c.st0; st < c.st1; ++st, ++n) {
-                    const uint32_t b = n & 1, ph = (n >> 1) & 1;
-                    if (st + 1 < c.st1 && !scores(n + 1, n - 2)) { ok = false; break; }
-                    if (!mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs) || !mbar_wait_quiet(bar(x_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
+                    const uint32_t b = n & 1, ph = (n >> 1) & 1, x = tmem + kSCol + n % 3 * 128;
+                    const uint64_t wb = desc_at(w_desc, b * (kPreStep * D * 2));
+                    // (K of the next block came after V of this one)
+                    if (!(st + 1 < c.st1 ? scores(n + 1) : mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs))) { ok = false; break; }
+                    if (!mbar_wait_quiet(bar(x_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
                     // the part before has been read out of O
                     if (st == c.st0 && !mbar_wait_quiet(bar(o_empty), (parts & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kPreStep / 16; ++k) {
-                        tc_mma_f16_ts(tmem + kOCol, tmem + kSCol + n % 3 * 128 + (k / 4) * 64 + k % 4 * 8,
-                                      smem_desc(sm + L.v + b * (kPreStep * D * 2) + k * (kHalves * 2048), 1024, kHalves * 1024, 2), id_o,
-                                      st != c.st0 || k != 0);
-                    }
+                    for (int k = 0; k < kPreStep / 16; ++k)
+                        tc_mma_f16_ts(tmem + kOCol, x + (k / 4) * 64 + k % 4 * 8, desc_at(wb, k * (kHalves * 2048)), id_o,
+                                      k != 0 || st != c.st0);
                     tc_commit(bar(v_empty[b]));
                 }
                 ++parts;

@@ -31,6 +31,15 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity, u
     }
 }
 
+// The descriptor of the matrix `bytes` after d's: its address field, 14 bits wide, does not carry.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+    uint32_t lo, hi;
+    uint64_t r;
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(d));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo + (bytes >> 4)), "r"(hi));
+    return r;
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     uint32_t r[32];
     asm volatile(
