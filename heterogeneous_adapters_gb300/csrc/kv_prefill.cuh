@@ -516,48 +516,58 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
             }
         }
     } else if (warp == 16) {
-        // ------------------------------------------------------------------ MMA issue, one thread
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1);
-            uint32_t parts = 0;
-            const uint64_t q_desc = smem_desc(sm + L.q, 16, 1024, 2), k_desc = smem_desc(sm + L.k, 16, 1024, 2),
-                           w_desc = smem_desc(sm + L.v, 1024, kHalves * 1024, 2);
-            // S of block i, in the place of X of block i - 3.  K of block i comes after V of i - 1,
-            // and that after X W of i - 3: one wait stands for all of them.
-            auto scores = [&](uint32_t i) {
-                const uint32_t b = i & 1, d = tmem + kSCol + i % 3 * 128;
-                const uint64_t kb = desc_at(k_desc, b * (kPreStep * D * 2));
-                if (!mbar_wait_quiet(bar(k_full[b]), (i >> 1) & 1, kWaitLimitNs)) return false;
-                tc_fence_after();
+        // ------------------------------------------------------------------ MMA issue: the warp in step, one lane issues
+        constexpr uint32_t id_s = idesc_bf16(128, kPreStep, 0, 0), id_o = idesc_f16(128, D, 0, 1);
+        uint32_t parts = 0;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sb = __shfl_sync(0xffffffffu, sm, 0);
+        const uint64_t q_desc = smem_desc(sb + L.q, 16, 1024, 2), k_desc = smem_desc(sb + L.k, 16, 1024, 2),
+                       w_desc = smem_desc(sb + L.v, 1024, kHalves * 1024, 2);
+        auto wait = [&](uint64_t& which, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait_quiet(bar(which), parity, kWaitLimitNs));
+        };
+        // S of block i, in the place of X of block i - 3.  K of block i comes after V of i - 1,
+        // and that after X W of i - 3: one wait stands for all of them.
+        auto scores = [&](uint32_t i) {
+            const uint32_t b = i & 1, d = tm + kSCol + i % 3 * 128;
+            const uint64_t kb = desc_at(k_desc, b * (kPreStep * D * 2));
+            if (!wait(k_full[b], (i >> 1) & 1)) return false;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     tc_mma_f16(d, desc_at(q_desc, (k / 4) * (kPreRows * 128) + (k % 4) * 32),
                                desc_at(kb, (k / 4) * (kPreStep * 128) + (k % 4) * 32), id_s, k != 0);
                 tc_commit(bar(s_full[b]));
-                return true;
-            };
-            while (ok && walk.next(v, p.rep, c)) {
-                if (!mbar_wait_quiet(bar(q_full), parts & 1, kWaitLimitNs) || !scores(n)) { ok = false; break; }
-                for (int st = c.st0; st < c.st1; ++st, ++n) {
-                    const uint32_t b = n & 1, ph = (n >> 1) & 1, x = tmem + kSCol + n % 3 * 128;
-                    const uint64_t wb = desc_at(w_desc, b * (kPreStep * D * 2));
-                    // (K of the next block came after V of this one)
-                    if (!(st + 1 < c.st1 ? scores(n + 1) : mbar_wait_quiet(bar(v_full[b]), ph, kWaitLimitNs))) { ok = false; break; }
-                    if (!mbar_wait_quiet(bar(x_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
-                    // the part before has been read out of O
-                    if (st == c.st0 && !mbar_wait_quiet(bar(o_empty), (parts & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-                    tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        while (ok && walk.next(v, p.rep, c)) {
+            const int st0 = __shfl_sync(0xffffffffu, c.st0, 0), st1 = __shfl_sync(0xffffffffu, c.st1, 0);
+            if (!wait(q_full, parts & 1) || !scores(n)) { ok = false; break; }
+            for (int st = st0; st < st1; ++st, ++n) {
+                const uint32_t b = n & 1, ph = (n >> 1) & 1, x = tm + kSCol + n % 3 * 128;
+                const uint64_t wb = desc_at(w_desc, b * (kPreStep * D * 2));
+                // (K of the next block came after V of this one)
+                if (!(st + 1 < st1 ? scores(n + 1) : wait(v_full[b], ph))) { ok = false; break; }
+                if (!wait(x_full[b], ph)) { ok = false; break; }
+                // the part before has been read out of O
+                if (st == st0 && !wait(o_empty, (parts & 1) ^ 1)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kPreStep / 16; ++k)
-                        tc_mma_f16_ts(tmem + kOCol, x + (k / 4) * 64 + k % 4 * 8, desc_at(wb, k * (kHalves * 2048)), id_o,
-                                      k != 0 || st != c.st0);
+                        tc_mma_f16_ts(tm + kOCol, x + (k / 4) * 64 + k % 4 * 8, desc_at(wb, k * (kHalves * 2048)), id_o,
+                                      k != 0 || st != st0);
                     tc_commit(bar(v_empty[b]));
                 }
-                ++parts;
+                __syncwarp();
             }
-            tc_commit(bar(final_bar));         // the MMAs are done before tensor memory is given back
-            mbar_wait_quiet(bar(final_bar), 0, 100000000ull);
+            ++parts;
         }
+        if (elect_one()) tc_commit(bar(final_bar));     // the MMAs are done before tensor memory is given back
+        __syncwarp();
+        mbar_wait_quiet(bar(final_bar), 0, 100000000ull);
         __syncwarp();
     } else {
         // ------------------------------------------------------------------ codes: eight tiles a block, a lane each

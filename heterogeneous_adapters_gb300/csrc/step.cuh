@@ -31,6 +31,13 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity, u
     }
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+
 // The descriptor of the matrix `bytes` after d's: its address field, 14 bits wide, does not carry.
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
     uint32_t lo, hi;
