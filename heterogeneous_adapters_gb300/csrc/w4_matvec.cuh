@@ -29,7 +29,7 @@ constexpr int kW4Warps = 8;
 constexpr int kW4Threads = kW4Warps * 32;
 // Rows of x up to which this kernel serves: always up to 8, and up to 16 where an SM has fewer
 // than kW4WideBlocks blocks of w4_wide.cuh to itself, whose fixed part then weighs more (13
-// rows: 5 blocks an SM 11.6 us here and 13.8 there, 24 blocks 31.6 here and 27.9 there).
+// rows: 5 blocks an SM 11.6 us here and 12.4 there, 24 blocks 31.3 here and 23.7 there).
 constexpr int kW4NarrowRows = 16;
 constexpr int kW4WideBlocks = 8;
 constexpr int kW4Rows = 32;        // rows of W of a block

@@ -8,10 +8,10 @@
 // group: a thread per row of W reads its columns and adds scale * D to sums in registers.
 // Half a byte a weight from memory is the floor; unpacking (13 / 8 instructions a weight, in
 // the order of K) and draining (one FMA per group, row and column) fill most of the issue
-// slots of that time at 64 rows.  Measured on two 14336 x 4096 of groups of 128: 17 rows 27.9 us,
-// 64 rows 30.2 us (31% of the copy rate), 128 rows 40.8 us (39% of the bf16 rate); groups of 64
-// and 32 at 64 rows 34 and 48 us.  An MMA of 128 rows with A in tensor memory takes 64 clocks
-// for any N up to 128, so a block is 1024 clocks of MMA at least; it takes about 1700, with some
+// slots of that time at 64 rows.  Measured on two 14336 x 4096 of groups of 128: 17 rows 24.0 us,
+// 64 rows 26.5 us (36% of the copy rate), 128 rows 39.3 us (40% of the bf16 rate); groups of 64
+// and 32 at 64 rows 30 and 41 us.  An MMA of 128 rows with A in tensor memory takes 64 clocks
+// for any N up to 128, so a block is 1024 clocks of MMA at least; it takes about 1500, with some
 // 3,800 instructions.
 //
 // One CTA per SM: warp 0 streams codes (blocks of 128 rows x 256 of K) by TMA and warp 11 x,
@@ -183,31 +183,39 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issue, one thread
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16(128, N, 0, 0);
-            uint32_t id = 0;                   // D sets
-            for (uint32_t i = 0; i < spans && ok; ++i) {
-                const uint32_t b = i % kSpans;
-                if (!mbar_wait_quiet(bar(a_full[b]), (i / kSpans) & 1, kWaitLimitNs)) { ok = false; break; }
-                const uint64_t db = smem_desc(x0 + b * kXBytes, 16, 1024, 2);
+        // ------------------------------------------------------------------ MMA issue: the warp in step, one lane issues
+        constexpr uint32_t idesc = idesc_bf16(128, N, 0, 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint64_t x_desc = smem_desc(__shfl_sync(0xffffffffu, x0, 0), 16, 1024, 2);
+        const uint32_t n_spans = __shfl_sync(0xffffffffu, spans, 0);
+        auto wait = [&](uint64_t& which, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait_quiet(bar(which), parity, kWaitLimitNs));
+        };
+        uint32_t id = 0;                       // D sets
+        for (uint32_t i = 0; i < n_spans && ok; ++i) {
+            const uint32_t b = i % kSpans;
+            if (!wait(a_full[b], (i / kSpans) & 1)) { ok = false; break; }
+            const uint64_t db = desc_at(x_desc, b * kXBytes);
 #pragma unroll
-                for (int s = 0; s < kSets; ++s, ++id) {
-                    if (!mbar_wait_quiet(bar(d_empty[id & 1]), ((id >> 1) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
-                    tc_fence_after();
+            for (int s = 0; s < kSets; ++s, ++id) {
+                if (!wait(d_empty[id & 1], ((id >> 1) & 1) ^ 1)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kSet * G / 16; ++k) {
                         const int ks = s * (kSet * G / 16) + k;
-                        tc_mma_f16_ts(tmem + (id & 1) * kDCols + k / (G / 16) * N, tmem + kACol + b * (kSpan / 2) + ks * 8,
-                                      db + ((ks / 4) * (N * 128) + (ks % 4) * 32) / 16, idesc, k % (G / 16) != 0);
+                        tc_mma_f16_ts(tm + (id & 1) * kDCols + k / (G / 16) * N, tm + kACol + b * (kSpan / 2) + ks * 8,
+                                      desc_at(db, (ks / 4) * (N * 128) + (ks % 4) * 32), idesc, k % (G / 16) != 0);
                     }
                     tc_commit(bar(d_full[b * kSets + s]));
                 }
+                __syncwarp();
             }
-            if (!ok) set_error(prm.err, LORA_DERR_TIMEOUT);
-            tc_commit(bar(final_bar));         // the MMAs are done before tensor memory is given back
-            mbar_wait_quiet(bar(final_bar), 0, 100000000ull);
         }
+        if (!ok && lane == 0) set_error(prm.err, LORA_DERR_TIMEOUT);
+        if (elect_one()) tc_commit(bar(final_bar));     // the MMAs are done before tensor memory is given back
+        __syncwarp();
+        mbar_wait_quiet(bar(final_bar), 0, 100000000ull);
         __syncwarp();
     } else if (warp == 10) {
         // ------------------------------------------------------------------ scales and zero points
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             const W4Prob& pr = p.prob[a.prob];
             const bool zeros = pr.zeros != nullptr;
             const uint32_t s = ic % kCodeStages;
-            if (!mbar_wait_quiet(bar(code_full[s]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
+            if (!mbar_wait(bar(code_full[s]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
             {
                 const int c = turn;
                 const uint32_t i = kSpan == kWideK ? ic : 2 * ic + c, b = i % kSpans;   // span
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                         codes_in_order(w.z, m, out[h] + j * 16 + 8);
                         codes_in_order(w.w, m, out[h] + j * 16 + 12);
                     }
-                if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((i / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait(bar(d_full[b * kSets + kSets - 1]), ((i / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
                 tc_fence_after();
                 tmem_st32(acol, out[0]);
                 tmem_st32(acol + 32, out[1]);
@@ -293,7 +301,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         auto meet = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(join));
-            return mbar_wait_quiet(bar(join), ij++ & 1, kWaitLimitNs);
+            return mbar_wait(bar(join), ij++ & 1, kWaitLimitNs);
         };
         for (int at = first; at < end && ok;) {
             const W4Prob& pr = p.prob[a.prob];
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
             for (int u = at; u < stop && ok; ++u) {
                 const uint32_t st = ic % kCodeStages;
-                if (!mbar_wait_quiet(bar(code_full[st]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait(bar(code_full[st]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
 #pragma unroll
                 for (int c = 0; c < kBlockGroups / kSet; ++c, ++id) {
                     float s[kSet];
@@ -315,7 +323,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                                      : "r"(params0 + st * kParams + ((c * kSet + i) * kWideRows + r) * 2));
                         s[i] = __half2float(__ushort_as_half(h));
                     }
-                    if (!mbar_wait_quiet(bar(d_full[id % kDone]), (id / kDone) & 1, kWaitLimitNs)) { ok = false; break; }
+                    if (!mbar_wait(bar(d_full[id % kDone]), (id / kDone) & 1, kWaitLimitNs)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
                     for (int g = 0; g < kSet; ++g)
