@@ -17,10 +17,11 @@
 // output put back).  Warp 16 issues the MMAs, S of the next block before X W of this one; warp
 // 17 brings the codes.  Tiles are dealt, split and joined as kv_attend.cuh's items.
 //
-// A block costs 1024 clocks of MMA and as many of exponentials, but takes about 3300: some
-// 7,400 instructions (rows 3,600, unpacking 2,750) at 55% of the issue slots.  Three requests
-// of 300 to 512 rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 146 us for
-// 89 GFLOP, 32% of the measured bf16 rate.
+// A block costs 1024 clocks of MMA and as many of exponentials, but takes about 2900: a row
+// warp is 2000 of them on its 64 tokens, with the unpacking warps (2,750 of the block's some
+// 7,400 instructions, the rows 3,600) beside it on its scheduler.  Three requests of 300 to 512
+// rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 138 us for 89 GFLOP, 34%
+// of the measured bf16 rate.
 #pragma once
 #include "kv_attend.cuh"
 
@@ -31,8 +32,8 @@ constexpr int kPreItemCost = 3;      // blocks' worth of a tile's fixed part
 constexpr int kPreMinUnits = 4;
 constexpr int kPreMaxCtas = 192;
 // A request's packed rows per KV head from which this kernel serves it.  16 requests over 4000
-// tokens: 32 rows 56 us in kv_attend.cuh and 66 here, 48 rows 77 and 67, 64 rows 95 and 66 (heads
-// of 64: 48 rows 32 and 37, 64 rows 41 and 38).
+// tokens: 32 rows 56 us in kv_attend.cuh, 48 rows 77, 64 rows 95, and here 63 for 48 (heads of
+// 64: 48 rows 32 and 64 rows 41 there, 36 here for 64).
 constexpr int kPreMinPacked = 48;
 
 constexpr int kPreTable = 3 * kPreStep * 4 + 16;
