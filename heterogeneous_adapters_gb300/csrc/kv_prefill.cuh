@@ -19,7 +19,7 @@
 //
 // A block costs 1024 clocks of MMA and as many of exponentials, but takes about 2900: a row
 // warp is 2000 of them on its 64 tokens, with the unpacking warps (2,750 of the block's some
-// 7,400 instructions, the rows 3,600) beside it on its scheduler.  Three requests of 300 to 512
+// 7,000 instructions, the rows 3,600) beside it on its scheduler.  Three requests of 300 to 512
 // rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 138 us for 89 GFLOP, 34%
 // of the measured bf16 rate.
 #pragma once
