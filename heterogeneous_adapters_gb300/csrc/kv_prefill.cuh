@@ -20,7 +20,7 @@
 // A block costs 1024 clocks of MMA and as many of exponentials, but takes about 2900: a row
 // warp is 2000 of them on its 64 tokens, with the unpacking warps (2,750 of the block's some
 // 7,000 instructions, the rows 3,600) beside it on its scheduler.  Three requests of 300 to 512
-// rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 138 us for 89 GFLOP, 34%
+// rows over 3111 to 6000 tokens (32 query and 8 KV heads of 128) take 137 us for 89 GFLOP, 34%
 // of the measured bf16 rate.
 #pragma once
 #include "kv_attend.cuh"
@@ -28,11 +28,14 @@
 namespace lora {
 
 constexpr int kPreRows = 128, kPreStep = 128, kPreThreads = 18 * 32;
-constexpr int kPreItemCost = 3;      // blocks' worth of a tile's fixed part
-constexpr int kPreMinUnits = 4;
+// Blocks' worth of a tile's fixed part: three requests' chunks 139.6 / 139.2 / 136.9 / 136.5 / 137.8
+// us at 2 / 3 / 4 / 6 / 8, 16 requests of 12 rows 64.0 / 63.1 / 62.9 / 61.5 / 61.5, of 48 rows
+// 108.2 / 106.3 / 106.5 / 107.3 / 108.1.
+constexpr int kPreItemCost = 6;
+constexpr int kPreMinUnits = 8;
 constexpr int kPreMaxCtas = 192;
 // A request's packed rows per KV head from which this kernel serves it.  16 requests over 4000
-// tokens: 32 rows 56 us in kv_attend.cuh, 48 rows 77, 64 rows 95, and here 63 for 48 (heads of
+// tokens: 32 rows 56 us in kv_attend.cuh, 48 rows 77, 64 rows 95, and here 61 for 48 (heads of
 // 64: 48 rows 32 and 64 rows 41 there, 36 here for 64).
 constexpr int kPreMinPacked = 48;
 
