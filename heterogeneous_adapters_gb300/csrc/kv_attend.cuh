@@ -512,8 +512,10 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, G, NT)) kv_attend_
                             }
                             const uint32_t w = pack_f16(x[0], x[1]);
                             const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&w));
-                            if (!masked || r.x != 0.f) off[n][gr][0] = fmaf(r.x, vp[h][gr][e].y, off[n][gr][0]);
-                            if (!masked || r.y != 0.f) off[n][gr][1] = fmaf(r.y, vp[h][gr][e].y, off[n][gr][1]);
+                            // (what a row does not see is left out; a weight of zero times a token
+                            // that is not a number is not one either)
+                            if (!masked || s[h][n][2 * e] != -INFINITY) off[n][gr][0] = fmaf(r.x, vp[h][gr][e].y, off[n][gr][0]);
+                            if (!masked || s[h][n][2 * e + 1] != -INFINITY) off[n][gr][1] = fmaf(r.y, vp[h][gr][e].y, off[n][gr][1]);
                             pb[h][n][gr][e] = movmatrix_trans(w);
                         }
                     }
