@@ -9,11 +9,14 @@
 // and the scale enters once per token in fp32.  q goes in as f16 times a power of two that
 // puts a row's largest value at 2^13: its eight bits are kept for every value above 2^-27
 // of the largest.  The output is likewise
-//     O^T = C_V^T x  +  sum_t x_t (offset_t / scale_t),    x_t = f16(scale_t p_t),
+//     O^T = C_V^T f16(x)  +  sum_t x_t (offset_t / scale_t),    x_t = scale_t p_t to 11 bits,
 // where x_t is the one value that is rounded (2^-11 of itself) and both terms use it
 // rounded: the sum is over whole values v_t with weights off by that much, however large
-// scale and offset are against v_t.  p_t = 2^(score log2 e - M) has the reference M at the
-// largest scale_t p_t seen (x fits f16 whatever the scales), moved when an x exceeds 2^10.
+// scale and offset are against v_t.  The second sum takes x_t in fp32, at any size; only what
+// f16 makes of an x_t below 2^-14, a multiple of 2^-24, is less exact, and it meets codes
+// of 8 at most.  p_t = 2^(score log2 e - M) has the reference M where the largest scale_t p_t
+// seen is 2^10 (x fits f16 whatever the scales), moved when an x exceeds 2^15: what is lost
+// below f16's range is 2^-32 of the largest x a token.
 // ldmatrix hands each lane its words of codes in the operand's order (transposed for V,
 // which pairs the tokens), so a code costs 9 / 8 instructions on its way to the tensor core.
 // The tokens being the long side of both products, 8 rows fill an MMA; mma.sync serves
@@ -51,7 +54,9 @@ constexpr int kAttJoin = 8;           // parts of an item whose loads are in fli
 // constant group's codes are 8, and otherwise the value is off by less than 2^-11 of itself.
 constexpr float kScaleOfOffset = 6.1035156e-5f;
 constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40
-constexpr float kMoveAbove = 1024.f;
+// A new reference puts the largest weight at 2^kRefUp; weights above kMoveAbove, whose f16
+// range ends at 65504, make one.
+constexpr float kRefUp = 10.f, kMoveAbove = 32768.f;
 constexpr float kNoRef = -3e38f;               // M before the first token
 // Units of an item beside its steps: what finding it, its first copies and its merge cost.
 // 64 requests of 17 to 8191 tokens: 79 / 72 / 68 / 65 / 65 / 70 us at 3 / 6 / 8 / 14 / 18 / 32
@@ -175,6 +180,13 @@ __device__ __forceinline__ bool att_deal(const KvView& v, int rep, int64_t* scan
     }
     __syncthreads();
     return true;
+}
+
+// Two values of at most 2^100 rounded to 11 bits at any size: with t = (2^13 + 1) x,
+// t - (t - x) is x without its last 13 bits (Veltkamp's splitting).
+__device__ __forceinline__ void round11(float a, float b, float& ra, float& rb) {
+    const uint64_t x = pack2f(a, b), less = pack2f(-1.f, -1.f), t = mul2(x, pack2f(8193.f, 8193.f));
+    unpack2f(fma2(fma2(x, less, t), less, t), ra, rb);
 }
 
 __device__ __forceinline__ void att_store(const AttendParams& p, int row, int hq, int D, int d, float4 x, float sum) {
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, G, NT)) kv_attend_
 #pragma unroll
                                 for (int gr = 1; gr < kGroups; ++gr) sc = fmaxf(sc, vp[h][gr][e].x);
                                 const float a = s[h][n][2 * e + j];
-                                if (!masked || a != -INFINITY) mn = fmaxf(mn, fmaf(a, sl[n][j], log2_approx(sc)));
+                                if (!masked || a != -INFINITY) mn = fmaxf(mn, fmaf(a, sl[n][j], log2_approx(sc) - kRefUp));
                             }
                         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 4));
                         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 8));
@@ -510,8 +522,9 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, G, NT)) kv_attend_
                                 x[j] = pr[h][2 * e + j] * vp[h][gr][e].x;
                                 if (masked && pr[h][2 * e + j] == 0.f) x[j] = 0.f;
                             }
-                            const uint32_t w = pack_f16(x[0], x[1]);
-                            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&w));
+                            float2 r;
+                            round11(x[0], x[1], r.x, r.y);
+                            const uint32_t w = pack_f16(r.x, r.y);
                             // (what a row does not see is left out; a weight of zero times a token
                             // that is not a number is not one either)
                             if (!masked || s[h][n][2 * e] != -INFINITY) off[n][gr][0] = fmaf(r.x, vp[h][gr][e].y, off[n][gr][0]);

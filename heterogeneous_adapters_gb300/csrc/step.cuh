@@ -1,5 +1,5 @@
 // What the kernels of lora_kv.h and lora_w4.h share: the layout of their workspace, a quiet
-// barrier wait, and wider moves between registers and tensor memory.
+// barrier wait, pairs of fp32 values, and wider moves between registers and tensor memory.
 #pragma once
 #include "common.cuh"
 #include "ptx.cuh"
@@ -29,6 +29,29 @@ __device__ __forceinline__ bool mbar_wait_quiet(uint32_t bar, uint32_t parity, u
         if (t0 == 0) t0 = t;
         else if (t - t0 > limit_ns) return false;
     }
+}
+
+// Pairs of fp32 values in one register pair: each half rounded as the scalar operation rounds.
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2f(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // One lane of a converged warp.

@@ -1,5 +1,5 @@
-"""Attention over the 4-bit cache where a visible token is not a number; against 64 bits with the
-bounds of tests/kv_exact.py."""
+"""Attention over the 4-bit cache where the weights of tokens differ by many powers of two, where a
+visible token is not a number; against 64 bits with the bounds of tests/kv_exact.py."""
 import numpy as np
 import pytest
 
@@ -22,6 +22,10 @@ def fill(case, k, v):
     lora.kv_append(case.kv, batch, None, 0, None, 0, 0, k, k.shape[1], v, v.shape[1], case.rope(0), case.ws, case.size, case.stream)
 
 
+def signs(torch, dim, every=1):
+    return torch.where(torch.arange(dim, device="cuda") // every % 2 == 0, 1.0, -1.0)
+
+
 # ---------------------------------------------------------------------------- tokens that are not numbers
 
 @pytest.mark.parametrize("dim,group", FORMS)
@@ -39,4 +43,67 @@ def test_a_visible_token_that_is_not_a_number_shows(cuda, dim, group, rows, n, b
     out, lse = case.attend(q)
     assert case.error() == 0
     assert bool(out.isnan().any()) and not bool(out[:, :2 * dim].isnan().any())
+    check(case, q, out, lse)
+
+
+# ---------------------------------------------------------------------------- weights far apart
+
+GAPS = [-4.0, 4.0, 6.0, 7.0, 8.0, 10.0, 12.0, 12.7, 13.0, 15.0, 20.0, 24.0]
+
+
+def flat_beside_wide(torch, rows, n, kv_heads, repeats, dim, group, wide, flat):
+    """Tokens whose V is (nearly) constant beside one whose V is wide, at distances of their scores
+    from -4 to 24 powers of two: the many flat ones keep their share."""
+    gaps = GAPS * repeats
+    case = Case([rows] * len(gaps), [n - i % 12 for i in range(len(gaps))], heads=4 * kv_heads, kv_heads=kv_heads, dim=dim, group=group,
+                block=64, seed=1)
+    s, at, ks, vs = signs(torch, dim), n // 4, [], []
+    for gap, n in zip(gaps, case.lens):
+        k = torch.zeros(n, kv_heads, dim, device="cuda")
+        k[at] = gap * np.log(2.0) * dim ** -0.5 * s
+        noise = torch.randn(n, kv_heads, dim, generator=case.g, device="cuda")
+        v = {"constant": torch.ones_like(noise), "near": 1 + 2.0 ** -7 * noise, "offset": 3 + 0.25 * noise}[flat]
+        v[at] = wide * signs(torch, dim, 3)
+        ks.append(k.flatten(1)), vs.append(v.flatten(1))
+    fill(case, torch.cat(ks).bfloat16(), torch.cat(vs).bfloat16())
+    q = s.repeat(case.T, 4 * kv_heads).bfloat16()
+    out, lse = case.attend(q)
+    assert case.error() == 0
+    check(case, q, out, lse, heads=[0, 4 * kv_heads - 1])
+
+
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("wide", [2.6, 120.0])
+@pytest.mark.parametrize("flat", ["constant", "near", "offset"])
+@pytest.mark.parametrize("rows,n,kv_heads,repeats", [(1, 4096, 1, 1), (1, 300, 8, 16), (3, 150, 8, 16)])
+def test_flat_tokens_beside_a_wide_one_few_rows(cuda, dim, group, wide, flat, rows, n, kv_heads, repeats):
+    flat_beside_wide(cuda, rows, n, kv_heads, repeats, dim, group, wide, flat)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 16])
+def test_groups_of_different_sizes(cuda, dim, rows):
+    """Groups of one head whose V differs in size by 2^16: the small ones are exact too."""
+    case = Case([rows, 1], [700, 333], heads=4, kv_heads=2, dim=dim, group=32, block=32, seed=2)
+    total = sum(case.lens)
+    size = 2.0 ** (cuda.arange(2 * dim, device="cuda") // 32 % (dim // 32) * -(16 // (dim // 32 - 1))).float()
+    v = case.normal(total, 2 * dim).float() * 64.0 * size
+    fill(case, case.normal(total, 2 * dim, gain=1.5), v.bfloat16())
+    q = case.normal(case.T, 4 * dim)
+    out, lse = case.attend(q)
+    assert case.error() == 0
+    check(case, q, out, lse)
+
+
+# ---------------------------------------------------------------------------- ordinary values, tightly
+
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("rows,lens", [([1], [33]), ([1, 1, 1], [1000, 31, 4097]), ([3, 1, 5], [129, 2000, 64]), ([150, 1, 20], [900, 50, 20])])
+def test_ordinary_values(cuda, dim, group, rows, lens):
+    case = Case(rows, lens, heads=8, kv_heads=2, dim=dim, group=group, block=48, seed=3)
+    total = sum(lens)
+    fill(case, case.normal(total, 2 * dim), case.normal(total, 2 * dim))
+    q = case.normal(case.T, 8 * dim)
+    out, lse = case.attend(q)
+    assert case.error() == 0
     check(case, q, out, lse)
