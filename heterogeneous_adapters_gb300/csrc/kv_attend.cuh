@@ -15,8 +15,8 @@
 // scale and offset are against v_t.  The second sum takes x_t in fp32, at any size; only what
 // f16 makes of an x_t below 2^-14, a multiple of 2^-24, is less exact, and it meets codes
 // of 8 at most.  p_t = 2^(score log2 e - M) has the reference M where the largest scale_t p_t
-// seen is 2^10 (x fits f16 whatever the scales), moved when an x exceeds 2^15: what is lost
-// below f16's range is 2^-32 of the largest x a token.
+// seen is 2^6 (x fits f16 whatever the scales), moved when an x exceeds f16's range: what is
+// lost below it is 2^-31 of the largest x a token.
 // ldmatrix hands each lane its words of codes in the operand's order (transposed for V,
 // which pairs the tokens), so a code costs 9 / 8 instructions on its way to the tensor core.
 // The tokens being the long side of both products, 8 rows fill an MMA; mma.sync serves
@@ -54,9 +54,10 @@ constexpr int kAttJoin = 8;           // parts of an item whose loads are in fli
 // constant group's codes are 8, and otherwise the value is off by less than 2^-11 of itself.
 constexpr float kScaleOfOffset = 6.1035156e-5f;
 constexpr float kTinyScale = 9.0949470e-13f;   // 2^-40
-// A new reference puts the largest weight at 2^kRefUp; weights above kMoveAbove, whose f16
-// range ends at 65504, make one.
-constexpr float kRefUp = 10.f, kMoveAbove = 32768.f;
+// A new reference puts the largest weight at 2^kRefUp; weights above kMoveAbove, f16's largest
+// value, make one.  A reference higher up leaves fewer bits to f16's end, and rows take a new
+// one more often (2^10 in the chunk kernel: 149 us for 136).
+constexpr float kRefUp = 6.f, kMoveAbove = 65504.f;
 constexpr float kNoRef = -3e38f;               // M before the first token
 // Units of an item beside its steps: what finding it, its first copies and its merge cost.
 // 64 requests of 17 to 8191 tokens: 79 / 72 / 68 / 65 / 65 / 70 us at 3 / 6 / 8 / 14 / 18 / 32

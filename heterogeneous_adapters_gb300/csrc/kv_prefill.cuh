@@ -6,10 +6,13 @@
 // -8 .. 7,
 //     S = q C_K^T (128 x 128, tensor memory),   t = S k_t + kq_t sum(q) - M,   p = 2^t,
 // where k_t and kq_t are the token's K scale and offset times softmax_scale log2 e; then
-//     O += X W,   X = f16(p v_t),   W = f16((c - 8) + V offset / V scale) = f16(v / V scale),
-// the offset added in two parts (hi + lo) so that W is off by 2^-11 of itself even where the
-// two nearly cancel; X takes the place of S in tensor memory.  The output is O / sum p.  The
-// reference M is moved, and O multiplied, only when a p v_t exceeds 2^10.
+//     O += X W,   X = f16(p u_t),   W = f16((c - 8) V scale / u_t + V offset / u_t) = f16(v / u_t),
+// with u_t a power of two near the token's largest |v|: X is as large as what the token brings,
+// however its offset compares with its scale, and W, one FMA that rounds once (scale and offset
+// over u_t are exact in f16 above 2^-14), is off by 2^-11 of itself.  X takes the place of S in
+// tensor memory.  The output is O / sum p.  The reference M puts the largest p u_t at 2^6, so
+// that f16 loses 2^-31 of it a token at most; it is moved, and O multiplied, only when a p u_t
+// exceeds f16's range.
 //
 // Warps 0-7 hold half of a row a thread (64 of a block's tokens, half of the output): they
 // bring q, turn S into X and write the output.  Warps 8-15 unpack a block's codes into the
@@ -51,7 +54,7 @@ __host__ __device__ constexpr PreSmem pre_smem(int dim) {
     L.k = o;      o += 2 * kPreStep * dim * 2;
     L.v = o;      o += 2 * kPreStep * dim * 2;
     L.codes = o;  o += 2 * pre_code_bytes(dim);
-    L.table = o;  o += 4 * kPreTable;                // k, kq, v of a block's tokens, and its tiles that are there
+    L.table = o;  o += 4 * kPreTable;                // k, kq, u of a block's tokens, and its tiles that are there
     L.mask = o;   o += 16;
     L.pair = o;   o += 2 * kPreRows * 4 + 64;        // what a row's two threads exchange; flags [4 pairs][4]
     L.total = o + 1024;
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 uint32_t present;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(table - half * 256 + 3 * kPreStep * 4));
                 const uint32_t here = present >> (half * 4);        // this half's four tiles
-                // the reference at the row's largest p v_t of this block, if that is larger
+                // the reference 2^kRefUp below the row's largest p u_t of this block, if that is larger
                 auto move = [&]() {
                     float mn = m;
 #pragma unroll 1
@@ -249,7 +252,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const float k = lds32(table + (j0 + j) * 4), kq = lds32(table + (kPreStep + j0 + j) * 4);
-                            const float x = fmaf(k, t[j], kq * qs) + log2_approx(lds32(table + (2 * kPreStep + j0 + j) * 4));
+                            const float u = lds32(table + (2 * kPreStep + j0 + j) * 4);
+                            const float x = fmaf(k, t[j], kq * qs) + ((u == u ? log2_approx(u) : 0.f) - kRefUp);
                             if (tok0 + j0 + j <= last && (here >> (j0 / 16) & 1)) mn = fmaxf(mn, x);
                         }
                     }
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                                 const uint64_t pr = pack2f(e0, e1);
                                 sum2 = add2(sum2, pr);
                                 unpack2f(mul2(pr, h ? sc.y : sc.x), x0, x1);
-                                if (masked) {                  // a masked token's scale may be anything
+                                if (masked) {                  // a masked token's u may be anything
                                     if (e0 == 0.f) x0 = 0.f;
                                     if (e1 == 0.f) x1 = 0.f;
                                 }
@@ -448,11 +452,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 uint32_t vw;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw) : "r"(src + kv_params_at(D, D, 1) + tok % kKvTile * 4));
                 const float2 vs = __half22float2(*reinterpret_cast<__half2*>(&vw));
-                float sc = fmaxf(fmaxf(vs.x, fabsf(vs.y) * kScaleOfOffset), kTinyScale), r = vs.y * rcp_approx(sc);
-                if (!(fabsf(r) < 65000.f)) {            // a group that is not a number
-                    r = 0.f;
-                    sc = NAN;
-                }
+                // u: the power of two at or below the larger of 8 scale and |offset|, and over it the two
+                // (zeros for a token that is not there, and for one that is not a number, whose u says so)
+                const bool number = fabsf(vs.x) + fabsf(vs.y) < 1e6f;
+                const uint32_t ub = __float_as_uint(fmaxf(fmaxf(8.f * fabsf(vs.x), fabsf(vs.y)), kTinyScale)) & 0x7F800000u;
+                const float over = here && number ? __uint_as_float(0x7F000000u - ub) : 0.f;
+                const __half2 sc2 = __half2half2(__float2half_rn(over != 0.f ? vs.x * over : 0.f)),
+                              of2 = __half2half2(__float2half_rn(over != 0.f ? vs.y * over : 0.f));
                 if (half == 0) {
                     // the token's parameters; of a token that is not there nothing is used
                     uint32_t kw;
@@ -461,7 +467,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     float* table = reinterpret_cast<float*>(base + L.table + (n & 3) * kPreTable);
                     table[tok] = here ? ks.x * sl : 0.f;
                     table[kPreStep + tok] = here ? ks.y * sl : 0.f;
-                    table[2 * kPreStep + tok] = here ? sc : 0.f;
+                    table[2 * kPreStep + tok] = !here ? 0.f : number ? __uint_as_float(ub) : NAN;
                     if (tok == 0) reinterpret_cast<uint32_t*>(table)[3 * kPreStep] = present;
                 }
                 fence_proxy_async_smem();
@@ -469,8 +475,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 if (lane == 0) mbar_arrive(bar(k_full[b]));
                 if (!mbar_wait(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
                 // W: rows of tokens, [token / 8][64 values][token % 8]
-                const __half hi = __float2half_rn(here ? r : 0.f);
-                const __half2 hi2 = __half2half2(hi), lo2 = __half2half2(__float2half_rn((here ? r : 0.f) - __half2float(hi)));
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
                     const int chunk = half * (D / 64) + i;
@@ -483,7 +487,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                         codes_f16(w[j], o);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const __half2 x = __hadd2(__hadd2(*reinterpret_cast<__half2*>(&o[k]), hi2), lo2);
+                            const __half2 x = __hfma2(*reinterpret_cast<__half2*>(&o[k]), sc2, of2);
                             o[k] = *reinterpret_cast<const uint32_t*>(&x);
                         }
                         sts128(dst + (((chunk % 2 * 4 + j) ^ (tok & 7)) << 4), o[0], o[1], o[2], o[3]);

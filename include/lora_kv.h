@@ -124,10 +124,13 @@ lora_status lora_kv_read(const lora_kv_cache_desc* cache, const lora_kv_batch* b
  *     a_t = softmax_scale * (q . k_t),   out = sum_t exp(a_t - lse) v_t,   lse = log sum_t exp(a_t).
  *   q, out  bf16 [T][ldq], [T][ldo]; lse: f32 [T][num_q_heads], or NULL
  * A row with no token (kv_len smaller than the request's rows) gets zeros and lse = -inf.
- * Scores, softmax statistics and sums are fp32; a probability times its V scale is rounded
- * to f16 once, before its product with the V codes (and so is v over its scale where a
- * request has many rows): 2^-11 of itself each.  The result does not depend on how the device
- * schedules the work.  num_q_heads is a multiple of num_kv_heads. */
+ * Scores, softmax statistics and sums are fp32.  A token's weight in the output is rounded to 11
+ * bits once (2^-11 of itself), and v by as much (where a request has many rows, v over a power
+ * of two to f16; where it has few, a V scale below 2^-14 of its offset counts as that).  Codes
+ * meet the weights in f16, whose steps end at 2^-28 of a row's largest p |v|: a token may be
+ * off by that much beside.  The result does not depend on how the device schedules the work.
+ * A token whose V is not a number makes the outputs of its group so, for the rows that see it.
+ * num_q_heads is a multiple of num_kv_heads. */
 lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch* batch, const void* q, int64_t ldq,
                            int32_t num_q_heads, float softmax_scale, void* out, int64_t ldo, float* lse, void* ws,
                            size_t ws_bytes, void* stream);

@@ -27,7 +27,7 @@ def check(case, q, out, lse, scale=None, heads=None):
       - 2^-10 of sum p |v|: the weight rounds to f16 (2^-11 of itself), and so does v over its
         power of two, or a scale below 2^-14 of its offset stands as that (2^-11 of v);
       - fp32 sums: scores off by D 2^-24 of the sums of their parts, outputs by 2^-14;
-      - per token 2^-32 of the row's largest p (8 scale + |offset|): weights that small are
+      - per token 2^-29 of the row's largest p (scale |c - 8| + |offset|): weights that small are
         multiples of f16's smallest step.
     A token whose V is not a number makes its group of the output one, and nothing else."""
     scale = scale or case.dim ** -0.5
@@ -54,7 +54,7 @@ def check(case, q, out, lse, scale=None, heads=None):
             step = (p * parts.amax(-1)).amax(1, keepdim=True)
             got = out[row:row + m, h * case.dim:(h + 1) * case.dim].double()
             tol = (2.0 ** -8 * want.abs() + 2.0 ** -10 * weight + (2 * slack + 2.0 ** -14) * (p @ parts)
-                   + n * 2.0 ** -32 * step * 8 + 1e-9)
+                   + n * 2.0 ** -29 * step + 1e-9)
             assert bool((got.isnan() == lost).all()), (s, h, int(got.isnan().sum()), int(lost.sum()))
             err = ((got - want).abs() - tol).masked_fill(lost, -1.0)
             assert bool((err <= 0).all()), (s, h, float(err.max()), float((got - want).abs().masked_fill(lost, 0).max()))

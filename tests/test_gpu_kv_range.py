@@ -80,6 +80,13 @@ def test_flat_tokens_beside_a_wide_one_few_rows(cuda, dim, group, wide, flat, ro
     flat_beside_wide(cuda, rows, n, kv_heads, repeats, dim, group, wide, flat)
 
 
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("wide", [2.6, 120.0])
+@pytest.mark.parametrize("flat", ["constant", "near", "offset"])
+def test_flat_tokens_beside_a_wide_one_many_rows(cuda, dim, group, wide, flat):
+    flat_beside_wide(cuda, 16, 4096, 1, 1, dim, group, wide, flat)
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("rows", [1, 16])
 def test_groups_of_different_sizes(cuda, dim, rows):
