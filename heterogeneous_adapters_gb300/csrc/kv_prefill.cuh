@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 uint32_t present;
                 asm volatile("ld.shared.u32 %0, [%1];" : "=r"(present) : "r"(table - half * 256 + 3 * kPreStep * 4));
                 const uint32_t here = present >> (half * 4);        // this half's four tiles
-                // the reference 2^kRefUp below the row's largest p u_t of this block, if that is larger
+                // the reference 2^kRefUp below the row's largest p u_t of this block, if that is larger; with
+                // 1 for the u of a token whose V is not a number, so that its p stays in range
                 auto move = [&]() {
                     float mn = m;
 #pragma unroll 1
@@ -287,22 +288,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                                 const uint64_t e = fma2(h ? k.y : k.x, pack2f(s[0], s[1]), fma2(h ? kq.y : kq.x, qs2, ref2));
                                 float e0, e1, x0, x1;
                                 unpack2f(e, e0, e1);
-                                if (masked) {
-                                    const int tok = tok0 + j0 + j + 2 * h;
-                                    const bool in = here >> (j0 / 16) & 1;
-                                    if (tok > last || !in) e0 = -INFINITY;
-                                    if (tok + 1 > last || !in) e1 = -INFINITY;
-                                }
+                                const int tok = tok0 + j0 + j + 2 * h;
+                                const bool in = here >> (j0 / 16) & 1;
+                                const bool hide0 = masked && (tok > last || !in), hide1 = masked && (tok + 1 > last || !in);
+                                if (hide0) e0 = -INFINITY;
+                                if (hide1) e1 = -INFINITY;
                                 e0 = exp2_approx(e0);
                                 e1 = exp2_approx(e1);
                                 const uint64_t pr = pack2f(e0, e1);
                                 sum2 = add2(sum2, pr);
                                 unpack2f(mul2(pr, h ? sc.y : sc.x), x0, x1);
-                                if (masked) {                  // a masked token's u may be anything
-                                    if (e0 == 0.f) x0 = 0.f;
-                                    if (e1 == 0.f) x1 = 0.f;
-                                }
-                                top = fmaxf(top, fmaxf(x0, x1));
+                                if (hide0) x0 = 0.f;           // a hidden token's u may be anything
+                                if (hide1) x1 = 0.f;
+                                // (a weight that is not a number stays in the maximum)
+                                asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(x0), "f"(x1));
                                 x[(j0 + j + 2 * h) / 2] = pack_f16(x0, x1);
                             }
                         }
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     float s0, s1;
                     unpack2f(sum2, s0, s1);
                     sum = s0 + s1;
-                    return !__any_sync(0xffffffffu, top > kMoveAbove);
+                    return (bool)__all_sync(0xffffffffu, top <= kMoveAbove);
                 };
                 // causal, or with tiles absent: the same for every row of the tile
                 const bool masked = st * kPreStep + kPreStep - 1 > low || present != 0xFFu;

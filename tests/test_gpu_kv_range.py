@@ -46,6 +46,25 @@ def test_a_visible_token_that_is_not_a_number_shows(cuda, dim, group, rows, n, b
     check(case, q, out, lse)
 
 
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("back", [1, 20, 200, 290])
+@pytest.mark.parametrize("gap", [-300.0, 300.0])
+def test_a_token_that_is_not_a_number_at_any_weight(cuda, dim, group, rows, back, gap):
+    """The same where the token's weight is 2^gap of the others', beyond what fp32 holds."""
+    case = Case([rows], [300], heads=4, kv_heads=2, dim=dim, group=group, block=16, seed=5)
+    s = signs(cuda, dim)
+    k = cuda.zeros(300, 2, dim, device="cuda")
+    k[300 - back] = gap * np.log(2.0) * dim ** -0.5 * s
+    v = case.normal(300, 2 * dim)
+    v[300 - back, dim + 5] = float("nan")
+    fill(case, k.flatten(1).bfloat16(), v)
+    q = s.repeat(rows, 4).bfloat16()
+    out, lse = case.attend(q)
+    assert case.error() == 0
+    check(case, q, out, lse)
+
+
 # ---------------------------------------------------------------------------- weights far apart
 
 GAPS = [-4.0, 4.0, 6.0, 7.0, 8.0, 10.0, 12.0, 12.7, 13.0, 15.0, 20.0, 24.0]
