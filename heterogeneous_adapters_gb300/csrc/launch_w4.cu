@@ -29,7 +29,7 @@ size_t workspace_bytes() { return align256(std::max(w4_workspace(2), wide_worksp
 // Blocks of a CTA: an equal share of all, or whole row tiles where the largest share of them
 // is at most `join` blocks more (what joining a tile from parts costs a CTA).  Whole tiles
 // need one K for all projections.
-int32_t w4_per(const W4Params& p, int grid, int rows, int join) {
+int32_t w4_per(const W4Params& p, int grid, int join) {
     const int32_t share = (p.total + grid - 1) / grid;
     const int32_t kb = p.prob[0].kblocks;
     for (int32_t i = 1; i < p.nprob; ++i)
@@ -55,7 +55,7 @@ lora_status launch(W4Params& p, cudaStream_t s) {
         ready = di;
     }
     const int grid = std::min(di->sm_count * std::max(per_sm, 1), kW4MaxCtas);
-    p.per = w4_per(p, grid, kW4Rows, kW4JoinCost);
+    p.per = w4_per(p, grid, kW4JoinCost);
     kern<<<grid, kW4Threads, smem, s>>>(p);
     return cuda_status(cudaGetLastError());
 }

@@ -42,13 +42,6 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t minus) {
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(minus));
     return r;
 }
-// The same pair as 128 + code.
-template <int I>
-__device__ __forceinline__ uint32_t code_plus(uint32_t w) {
-    uint32_t t;
-    asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(t) : "r"(I ? w >> (4 * I) : w));
-    return t;
-}
 constexpr uint32_t kMinus8 = 0x43084308u;   // 136.0 twice: codes as -8 .. 7
 
 // The same in f16, whose ten bits after the point hold a second nibble in place: 0x6400 is

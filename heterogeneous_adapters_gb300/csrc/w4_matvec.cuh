@@ -1,14 +1,16 @@
 // y = x W^T with 4-bit weights and group scales, up to 16 rows of x a launch.
 //
-// A group's part of an output is  scale (sum_k (128 + c) x - (128 + zero) sum_k x): 128 + c is
-// the bf16 whose last mantissa bits are the code, so that a code costs 7 / 8 instructions on
-// its way to the tensor core (taking 128 + zero off each one would be 11 / 8), products are
-// exact, and a column of sums of x comes from one more MMA row tile of ones.  Sums of a
-// group are fp32 from zero: the 128s cost at most 2^-17 of sum |x w| per group.  The weights
-// are the long side: 16 rows of W are an MMA's rows and 8 rows of x its columns.  What bounds
-// it is the stream of W (half a byte a weight), next the unpacking: one row of 4096 x 4096 takes
-// 7.8 us (two of launch, three to the first data), of two 14336 x 4096 21.8 us, 41% of the copy
-// rate, where the copies alone take 12.6 and the products alone 16.
+// A group's part of an output is  scale sum_k (c - zero) x: the differences of codes and zero
+// point are whole numbers, exact in bf16 (128 + c is the bf16 whose last mantissa bits are the
+// code, and 128 + zero comes off exactly), so that products are exact whatever x holds, and
+// the scale enters once per group in fp32.  A code costs 11 / 8 instructions on its way to the
+// tensor core.  (128 + c itself would be 7 / 8, less (128 + zero) sum x: two large sums whose
+// difference is wrong near the zero point and for an infinite x, and not faster: 13 rows of
+// q, k, v 11.6 us, and 10.5 as it is.)  The weights are the long side: 16 rows of W are an
+// MMA's rows and 8 rows of x its columns.  What bounds it is the stream of W (half a byte a
+// weight), next the unpacking: one row of 4096 x 4096 takes 7.8 us (two of launch, three to the
+// first data), of two 14336 x 4096 21.8 us, 41% of the copy rate, where the copies alone
+// take 12.6.
 //
 // Work.  A block of work is 32 rows of W by 256 of K (4 KB of codes); blocks of all
 // projections lie in a row, K fastest, and the CTAs take equal contiguous ranges, a CTA's
@@ -29,7 +31,8 @@ constexpr int kW4Warps = 8;
 constexpr int kW4Threads = kW4Warps * 32;
 // Rows of x up to which this kernel serves: always up to 8, and up to 16 where an SM has fewer
 // than kW4WideBlocks blocks of w4_wide.cuh to itself, whose fixed part then weighs more (13
-// rows: 5 blocks an SM 11.6 us here and 12.4 there, 24 blocks 31.3 here and 23.7 there).
+// rows: 3 blocks an SM 9.8 us here and 10.2 there, 5 blocks 10.5 and 12.5, 12 blocks 19.1 and
+// 17.1, 24 blocks 28.1 and 23.7).
 constexpr int kW4NarrowRows = 16;
 constexpr int kW4WideBlocks = 8;
 constexpr int kW4Rows = 32;        // rows of W of a block
@@ -197,27 +200,26 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_matvec_kernel(const __grid_c
             const uint32_t st = ring + (it % kW4Stages) * kStage;
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
-                // scales and 128 + zero of rows g, g + 8, g + 16, g + 24
-                float sc[4], zf[4];
+                // scales, and 128 + zero twice, of rows g, g + 8, g + 16, g + 24
+                float sc[4];
+                uint32_t minus[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     unsigned short h;
                     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(st + kW4Codes + gr * 64 + (r * 8 + g) * 2));
                     sc[r] = __half2float(__ushort_as_half(h));
-                    zf[r] = 136.f;
+                    minus[r] = kMinus8;
                     if (pr.zeros) {
                         uint32_t z;
                         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z) : "r"(st + kW4Codes + kGroups * 64 + gr * 16 + r * 4));
-                        zf[r] = __uint_as_float((z >> (4 * g) & 15u) << 16 | 0x43000000u);
+                        minus[r] = 0x43004300u + (z >> (4 * g) & 15u) * 0x00010001u;
                     }
                 }
-                float s[2][NT][4], sx[NT][4];
+                float s[2][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    sx[n][0] = sx[n][1] = sx[n][2] = sx[n][3] = 0.f;
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
-                }
+                    for (int n = 0; n < NT; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
 #pragma unroll
                 for (int c = gr * (G / 32); c < (gr + 1) * (G / 32); ++c) {
                     uint32_t xb[NT][4];
@@ -228,17 +230,14 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_matvec_kernel(const __grid_c
                         xb[n][1] = __byte_perm(x.x, x.z, 0x7632);
                         xb[n][2] = __byte_perm(x.y, x.w, 0x5410);
                         xb[n][3] = __byte_perm(x.y, x.w, 0x7632);
-                        const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-                        mma16816(sx[n], ones, xb[n][0], xb[n][1]);
-                        mma16816(sx[n], ones, xb[n][2], xb[n][3]);
                     }
                     uint32_t w[4];
                     ldmatrix4(w, st + lane * 128 + ((c ^ (lane & 7)) << 4));
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const uint32_t w0 = w[2 * m], w1 = w[2 * m + 1];
-                        const uint32_t a0[4] = {code_plus<0>(w0), code_plus<0>(w1), code_plus<1>(w0), code_plus<1>(w1)};
-                        const uint32_t a1[4] = {code_plus<2>(w0), code_plus<2>(w1), code_plus<3>(w0), code_plus<3>(w1)};
+                        const uint32_t w0 = w[2 * m], w1 = w[2 * m + 1], z0 = minus[2 * m], z1 = minus[2 * m + 1];
+                        const uint32_t a0[4] = {code_pair<0>(w0, z0), code_pair<0>(w1, z1), code_pair<1>(w0, z0), code_pair<1>(w1, z1)};
+                        const uint32_t a1[4] = {code_pair<2>(w0, z0), code_pair<2>(w1, z1), code_pair<3>(w0, z0), code_pair<3>(w1, z1)};
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma16816(s[m][n], a0, xb[n][0], xb[n][1]);
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(kW4Threads, 2) w4_matvec_kernel(const __grid_c
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int r = 2 * m + (j >> 1);
-                            acc[m][n][j] = fmaf(sc[r], fmaf(-zf[r], sx[n][j & 1], s[m][n][j]), acc[m][n][j]);
+                            acc[m][n][j] = fmaf(sc[r], s[m][n][j], acc[m][n][j]);
                         }
                 if (gr + 1 < kGroups) load_x(gr + 1);
             }
