@@ -16,8 +16,8 @@ from ._binding import (DERR, LORA_ENOSPACE, LORA_MAX_PROBLEMS_PER_LAUNCH, LORA_M
                        lib, segment, sgmv, stage_pages, stage_pages_ce, workspace_init, workspace_size,
                        workspace_view)
 from ._binding import (LORA_KV_MAX_HEADS, LORA_KV_MAX_SEQS, LORA_ROPE_HALVES, LORA_ROPE_PAIRS,
-                       LORA_W4_MAX_PROBLEMS, LORA_W4_MAX_ROWS, KvBatch, KvCache, Rope, kv_append, kv_attend,
-                       kv_block_bytes, kv_read, kv_workspace_init, kv_workspace_size, w4_matvec, w4_problems,
+                       LORA_W4_MAX_PROBLEMS, LORA_W4_MAX_ROWS, KvBatch, KvCache, Rope, debug_w4_lost_block, kv_append,
+                       kv_attend, kv_block_bytes, kv_read, kv_workspace_init, kv_workspace_size, w4_matvec, w4_problems,
                        w4_workspace_size)
 
 __all__ = ["costmodel", "DERR", "LORA_ENOSPACE", "LORA_MAX_PROBLEMS_PER_LAUNCH", "LORA_MAX_RANK",
@@ -29,6 +29,6 @@ __all__ = ["costmodel", "DERR", "LORA_ENOSPACE", "LORA_MAX_PROBLEMS_PER_LAUNCH",
            "get_device_error", "lib", "segment", "sgmv", "stage_pages", "stage_pages_ce", "workspace_init",
            "workspace_size", "workspace_view",
            "LORA_KV_MAX_HEADS", "LORA_KV_MAX_SEQS", "LORA_ROPE_HALVES", "LORA_ROPE_PAIRS",
-           "LORA_W4_MAX_PROBLEMS", "LORA_W4_MAX_ROWS", "KvBatch", "KvCache", "Rope", "kv_append", "kv_attend",
-           "kv_block_bytes", "kv_read", "kv_workspace_init", "kv_workspace_size", "w4_matvec", "w4_problems",
+           "LORA_W4_MAX_PROBLEMS", "LORA_W4_MAX_ROWS", "KvBatch", "KvCache", "Rope", "debug_w4_lost_block",
+           "kv_append", "kv_attend", "kv_block_bytes", "kv_read", "kv_workspace_init", "kv_workspace_size", "w4_matvec", "w4_problems",
            "w4_workspace_size"]

@@ -39,7 +39,7 @@ EXPORTED = ["lora_pool_create", "lora_pool_destroy", "lora_pool_set_tuning", "lo
             "lora_sched_destroy", "lora_sched_enqueue", "lora_sched_pick", "lora_sched_pending",
             # the 4-bit KV cache (include/lora_kv.h) and 4-bit weights (include/lora_w4.h)
             "lora_kv_block_bytes", "lora_kv_workspace_size", "lora_kv_workspace_init", "lora_kv_append",
-            "lora_kv_read", "lora_kv_attend", "lora_w4_workspace_size", "lora_w4_matvec"]
+            "lora_kv_read", "lora_kv_attend", "lora_w4_workspace_size", "lora_w4_matvec", "lora_debug_w4_lost_block"]
 
 
 class lora_pool_desc(ctypes.Structure):
@@ -164,6 +164,7 @@ def lib():
             "lora_kv_attend": [p, p, p, i64, i32, ctypes.c_float, p, i64, p, p, sz, p],
             "lora_w4_workspace_size": [p, i32, i32, ctypes.POINTER(sz)],
             "lora_w4_matvec": [p, i32, i32, p, sz, p],
+            "lora_debug_w4_lost_block": [p, i32, i32, i32, ctypes.c_uint64, p, sz, p],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -465,6 +466,12 @@ def w4_workspace_size(problems, T: int) -> int:
 def w4_matvec(problems, T, ws, ws_bytes, stream):
     """y = x W^T for every projection of w4_problems(...)."""
     _check(lib().lora_w4_matvec(problems.ref, problems.n, T, _ptr(ws), ws_bytes, stream), "lora_w4_matvec")
+
+
+def debug_w4_lost_block(problems, T, block, limit_ns, ws, ws_bytes, stream):
+    """w4_matvec with one block's codes missing: its waits run out after limit_ns."""
+    _check(lib().lora_debug_w4_lost_block(problems.ref, problems.n, T, block, limit_ns, _ptr(ws), ws_bytes, stream),
+           "lora_debug_w4_lost_block")
 
 
 # ----------------------------------------------------------------------------- host runtime

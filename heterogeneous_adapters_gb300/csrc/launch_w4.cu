@@ -114,20 +114,9 @@ lora_status launch_group(WideParams& w, bool narrow, cudaStream_t s) {
     return T <= 64 ? launch_wide<G, 64>(w, s) : launch_wide<G, 128>(w, s);
 }
 
-}  // namespace
-
-extern "C" {
-
-lora_status lora_w4_workspace_size(const lora_w4_problem* probs, int32_t nprob, int32_t T, size_t* bytes) {
-    if (bytes == nullptr) return LORA_EINVAL;
-    lora_status st = check_sizes(probs, nprob, T);
-    if (st != LORA_OK) return st;
-    *bytes = workspace_bytes();
-    return LORA_OK;
-}
-
-lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
-                           void* stream) {
+// All launches of a call.  `lost` and `limit_ns`: see WideParams.
+lora_status run(const lora_w4_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes, void* stream, int32_t lost,
+                uint64_t limit_ns) {
     lora_status st = check_sizes(probs, nprob, T);
     if (st != LORA_OK) return st;
     for (int32_t i = 0; i < nprob; ++i) {
@@ -181,12 +170,38 @@ lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t 
             p.tickets = reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(ws) + sizeof(WsHeader));
             p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + kStepPartAt);
             w.err = &reinterpret_cast<WsHeader*>(ws)->err;
+            w.limit_ns = limit_ns;
+            w.lost = lost;
             cudaStream_t s = (cudaStream_t)stream;
             st = group == 32 ? launch_group<32>(w, narrow, s) : group == 64 ? launch_group<64>(w, narrow, s) : launch_group<128>(w, narrow, s);
             if (st != LORA_OK) return st;
         }
     }
     return LORA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lora_status lora_w4_workspace_size(const lora_w4_problem* probs, int32_t nprob, int32_t T, size_t* bytes) {
+    if (bytes == nullptr) return LORA_EINVAL;
+    lora_status st = check_sizes(probs, nprob, T);
+    if (st != LORA_OK) return st;
+    *bytes = workspace_bytes();
+    return LORA_OK;
+}
+
+lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
+                           void* stream) {
+    return run(probs, nprob, T, ws, ws_bytes, stream, -1, kWaitLimitNs);
+}
+
+lora_status lora_debug_w4_lost_block(const lora_w4_problem* probs, int32_t nprob, int32_t T, int32_t block, uint64_t limit_ns,
+                                     void* ws, size_t ws_bytes, void* stream) {
+    if (T <= kW4NarrowRows || block < 0 || limit_ns < 1000000ull) return LORA_EINVAL;
+    if (limit_ns > kWaitLimitNs) return LORA_ETOOBIG;
+    return run(probs, nprob, T, ws, ws_bytes, stream, block, limit_ns);
 }
 
 }  // extern "C"

@@ -59,6 +59,8 @@ struct WideParams {
     CUtensorMap y[LORA_W4_MAX_PROBLEMS];       // bf16 {N, T}, box {128, N columns}
     W4Params p;                                // blocks of 128 x 256
     uint32_t* err;
+    uint64_t limit_ns;                         // of every wait
+    int32_t lost;                              // a block whose codes never come (a test of the waits), or -1
 };
 
 // A block: projection, row tile and block of K.
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
     constexpr int kDone = kSpans * kSets, kJoin = N > 64 ? 32 : 64;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t code_full[kCodeStages], code_empty[kCodeStages], a_full[kSpans], d_full[kDone], d_empty[2],
-        join, final_bar;
+        final_bar;
     __shared__ uint32_t tmem_slot, last_in;
     const W4Params& p = prm.p;
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -124,7 +126,6 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         for (int i = 0; i < kSpans; ++i) mbar_init(bar(a_full[i]), 1 + (kSpan == kWideK ? 8 : 4));
         for (int i = 0; i < kDone; ++i) mbar_init(bar(d_full[i]), 1);
         for (int i = 0; i < 2; ++i) mbar_init(bar(d_empty[i]), kDrain);
-        mbar_init(bar(join), kDrain);
         mbar_init(bar(final_bar), 1);
         fence_mbar_init();
     }
@@ -144,14 +145,18 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
     bool ok = true;
 
     const uint32_t spans = kWideK / kSpan * (uint32_t)(end - first);   // of this CTA's range
+    // a wait by a warp together: its lanes go on, or give up, as one
+    auto wait = [&](uint64_t& which, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, mbar_wait(bar(which), parity, prm.limit_ns));
+    };
     if (warp == 0) {
         // ------------------------------------------------------------------ codes, one thread
         if (lane == 0) {
             WideAt a = wide_at(p, first);
             uint32_t ic = 0;
-            for (int u = first; u < end && ok; ++u, wide_next(p, a), ++ic) {
+            for (int u = first; u < end && u != prm.lost; ++u, wide_next(p, a), ++ic) {
                 const uint32_t s = ic % kCodeStages;
-                if (!mbar_wait_quiet(bar(code_empty[s]), ((ic / kCodeStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!mbar_wait_quiet(bar(code_empty[s]), ((ic / kCodeStages) & 1) ^ 1, prm.limit_ns)) { ok = false; break; }
                 mbar_arrive_expect_tx(bar(code_full[s]), kWideCodeBytes);
                 tma_load_2d(codes0 + s * kWideCodeBytes, &prm.codes[a.prob], a.kb * (kWideK / 2), a.tile * kWideRows,
                             bar(code_full[s]));
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             for (int u = first; u < end && ok; ++u, wide_next(p, a)) {
                 for (int c = 0; c < kWideK / kSpan; ++c, ++ix) {
                     const uint32_t b = ix % kSpans;
-                    if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((ix / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                    if (!mbar_wait_quiet(bar(d_full[b * kSets + kSets - 1]), ((ix / kSpans) & 1) ^ 1, prm.limit_ns)) { ok = false; break; }
                     mbar_arrive_expect_tx(bar(a_full[b]), kXBytes);
 #pragma unroll
                     for (int h = 0; h < kSpan / 64; ++h)
@@ -188,17 +193,17 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint64_t x_desc = smem_desc(__shfl_sync(0xffffffffu, x0, 0), 16, 1024, 2);
         const uint32_t n_spans = __shfl_sync(0xffffffffu, spans, 0);
-        auto wait = [&](uint64_t& which, uint32_t parity) {
-            return (bool)__all_sync(0xffffffffu, mbar_wait_quiet(bar(which), parity, kWaitLimitNs));
+        auto wait_quiet = [&](uint64_t& which, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait_quiet(bar(which), parity, prm.limit_ns));
         };
         uint32_t id = 0;                       // D sets
         for (uint32_t i = 0; i < n_spans && ok; ++i) {
             const uint32_t b = i % kSpans;
-            if (!wait(a_full[b], (i / kSpans) & 1)) { ok = false; break; }
+            if (!wait_quiet(a_full[b], (i / kSpans) & 1)) { ok = false; break; }
             const uint64_t db = desc_at(x_desc, b * kXBytes);
 #pragma unroll
             for (int s = 0; s < kSets; ++s, ++id) {
-                if (!wait(d_empty[id & 1], ((id >> 1) & 1) ^ 1)) { ok = false; break; }
+                if (!wait_quiet(d_empty[id & 1], ((id >> 1) & 1) ^ 1)) { ok = false; break; }
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -224,7 +229,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         for (int u = first; u < end && ok; ++u, wide_next(p, a), ++ic) {
             const W4Prob& pr = p.prob[a.prob];
             const uint32_t s = ic % kCodeStages;
-            if (!mbar_wait_quiet(bar(code_empty[s]), ((ic / kCodeStages) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+            if (!mbar_wait_quiet(bar(code_empty[s]), ((ic / kCodeStages) & 1) ^ 1, prm.limit_ns)) { ok = false; break; }
             const int row0 = a.tile * kWideRows, groups = pr.K / G;
             for (int i = lane; i < kBlockGroups * 16; i += 32) {       // 8 rows of a group's scales, and of its zeros
                 const int g = i / 16, j = i % 16, grp = a.kb * kBlockGroups + g;
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             const W4Prob& pr = p.prob[a.prob];
             const bool zeros = pr.zeros != nullptr;
             const uint32_t s = ic % kCodeStages;
-            if (!mbar_wait(bar(code_full[s]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
+            if (!wait(code_full[s], (ic / kCodeStages) & 1)) { ok = false; break; }
             {
                 const int c = turn;
                 const uint32_t i = kSpan == kWideK ? ic : 2 * ic + c, b = i % kSpans;   // span
@@ -278,7 +283,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                         codes_in_order(w.z, m, out[h] + j * 16 + 8);
                         codes_in_order(w.w, m, out[h] + j * 16 + 12);
                     }
-                if (!mbar_wait(bar(d_full[b * kSets + kSets - 1]), ((i / kSpans) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!wait(d_full[b * kSets + kSets - 1], ((i / kSpans) & 1) ^ 1)) { ok = false; break; }
                 tc_fence_after();
                 tmem_st32(acol, out[0]);
                 tmem_st32(acol + 32, out[1]);
@@ -296,14 +301,12 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         WideAt a = wide_at(p, first);
-        uint32_t id = 0, ij = 0, ic = 0;
-        // the draining warps meet (bounded, as every wait); false on a timeout
-        auto meet = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(join));
-            return mbar_wait(bar(join), ij++ & 1, kWaitLimitNs);
-        };
-        for (int at = first; at < end && ok;) {
+        uint32_t id = 0, ic = 0;
+        // The draining warps meet at a named barrier, so none of them leaves early: after a wait
+        // that ran out they take no more part in the hand-overs, but still count their parts of
+        // the range's tiles (with the error set), so that the counters end as they began.
+        auto meet = [&]() { named_bar_sync(1, kDrain * 32); };
+        for (int at = first; at < end;) {
             const W4Prob& pr = p.prob[a.prob];
             const int row0 = a.tile * kWideRows;
             const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = min(tile_end, end);
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             for (int j = 0; j < kMine; ++j) acc[j] = 0.f;
             for (int u = at; u < stop && ok; ++u) {
                 const uint32_t st = ic % kCodeStages;
-                if (!mbar_wait(bar(code_full[st]), (ic / kCodeStages) & 1, kWaitLimitNs)) { ok = false; break; }
+                if (!wait(code_full[st], (ic / kCodeStages) & 1)) { ok = false; break; }
 #pragma unroll
                 for (int c = 0; c < kBlockGroups / kSet; ++c, ++id) {
                     float s[kSet];
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                                      : "r"(params0 + st * kParams + ((c * kSet + i) * kWideRows + r) * 2));
                         s[i] = __half2float(__ushort_as_half(h));
                     }
-                    if (!mbar_wait(bar(d_full[id % kDone]), (id / kDone) & 1, kWaitLimitNs)) { ok = false; break; }
+                    if (!wait(d_full[id % kDone], (id / kDone) & 1)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
                     for (int g = 0; g < kSet; ++g)
@@ -339,34 +342,34 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(d_empty[id & 1]));
                 }
+                if (!ok) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(code_empty[st]));
                 wide_next(p, a);
                 ++ic;
             }
-            if (!ok) break;
+            if (!ok && stop < end) a = wide_at(p, stop);
             // ---- the row tile's sums: y, or a part of them
             const bool whole = at == tile_first && stop == tile_end;
             auto part_of = [&](int64_t slot) { return reinterpret_cast<float4*>(p.part + (slot * N + half * kMine) * kWideRows) + r; };
             // y's tile, [column][row of W], through shared memory and one bulk store (what lies
-            // outside y is not written).  False on a timeout.
+            // outside y is not written)
             auto store = [&]() {
                 if (tid == 12 * 32) bulk_wait_read0();             // the last store has left the buffer
-                if (!meet()) return false;
+                meet();
 #pragma unroll
                 for (int j = 0; j < kMine; ++j)
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(y0 + ((half * kMine + j) * kWideRows + r) * 2),
                                  "h"(__bfloat16_as_ushort(__float2bfloat16_rn(acc[j]))) : "memory");
                 fence_proxy_async_smem();
-                if (!meet()) return false;
+                meet();
                 if (tid == 12 * 32) {
                     tma_store_2d(&prm.y[&pr - p.prob], row0, 0, y0);
                     bulk_commit();
                 }
-                return true;
             };
             if (whole) {
-                if (!(ok = store())) break;
+                store();
             } else {
                 // a part lies [column / 4][row][4]
                 float4* part = part_of((int64_t)blockIdx.x * 2 + (tile_first < first ? 0 : 1));
@@ -376,9 +379,9 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
             if (!whole) {
                 const int c0 = tile_first / p.per, c1 = (tile_end - 1) / p.per;
                 __threadfence();
-                if (!(ok = meet())) break;
+                meet();
                 if (tid == 12 * 32) last_in = atomicAdd(&p.tickets[c0], 1u) == (uint32_t)(c1 - c0);
-                if (!(ok = meet())) break;
+                meet();
                 if (*reinterpret_cast<volatile uint32_t*>(&last_in)) {
                     __threadfence();
                     if (tid == 12 * 32) p.tickets[c0] = 0;
@@ -396,9 +399,9 @@ __global__ void __launch_bounds__(wide_threads(N), 1) w4_wide_kernel(const __gri
                             acc[j + 3] += x.w;
                         }
                     }
-                    if (!(ok = store())) break;
+                    store();
                 }
-                if (!(ok = meet())) break;
+                meet();
             }
             at = stop;
         }

@@ -47,6 +47,14 @@ lora_status lora_w4_workspace_size(const lora_w4_problem* probs, int32_t nprob, 
 lora_status lora_w4_matvec(const lora_w4_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
                            void* stream);
 
+/* Self-test of the bounded waits: lora_w4_matvec (17 rows and more) for which the codes of
+ * `block` of each launch (128 rows of a W by 256 of K, counted K fastest through the
+ * projections of a group size) never come and every wait gives up after limit_ns nanoseconds
+ * (1 ms .. 2 s, else LORA_EINVAL / LORA_ETOOBIG).  LORA_DERR_TIMEOUT is set, y is incomplete,
+ * and the workspace serves later calls as before. */
+lora_status lora_debug_w4_lost_block(const lora_w4_problem* probs, int32_t nprob, int32_t T, int32_t block, uint64_t limit_ns,
+                                     void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -2,6 +2,8 @@
 point, one infinite or one very large x."""
 import pytest
 
+import heterogeneous_adapters_gb300 as lora
+
 from .test_gpu_w4 import call, problem
 
 pytestmark = pytest.mark.gpu
@@ -76,3 +78,38 @@ def test_large_x(cuda, T):
     w, x = weights(cuda, p), p["x"].double()
     want, size = x @ w.t(), x.abs() @ w.abs().t()
     assert bool(((p["y"].double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -14 * size).all())
+
+
+@pytest.mark.parametrize("T,block", [(17, 20), (64, 20), (64, 33), (128, 1000)])
+def test_the_workspace_serves_on_after_a_wait_that_ran_out(cuda, T, block):
+    """Row tiles shared by neighbouring workers, one of which never gets its codes: the timeout bit,
+    and later calls on the same workspace are as on a fresh one."""
+    g = cuda.Generator(device="cuda").manual_seed(T)
+    p = problem(cuda, g, T, 14336, 4096, 128, True)
+    tup = lambda y: (p["x"], y, 4096, 14336, p["codes"], p["scales"], p["zeros"], 14336, 4096, 128)  # noqa: E731
+    y = cuda.empty(T, 14336, dtype=cuda.bfloat16, device="cuda")
+    pr, want = lora.w4_problems([tup(y)]), lora.w4_problems([tup(p["y"])])
+    size, stream = lora.w4_workspace_size(pr, T), cuda.cuda.current_stream().cuda_stream
+    ws, fresh = (cuda.zeros(size, dtype=cuda.uint8, device="cuda") for _ in range(2))
+    lora.debug_w4_lost_block(pr, T, block, 5_000_000, ws, size, stream)
+    assert lora.get_device_error(ws, stream) == 0x20
+    for _ in range(3):
+        p["x"].copy_(cuda.randn(T, 4096, generator=g, device="cuda").bfloat16())
+        lora.w4_matvec(pr, T, ws, size, stream)
+        lora.w4_matvec(want, T, fresh, size, stream)
+        assert lora.get_device_error(ws, stream) == 0
+        assert cuda.equal(y.view(cuda.int16), p["y"].view(cuda.int16))
+
+
+def test_lost_block_refusals(cuda):
+    from heterogeneous_adapters_gb300 import _binding as B
+    g = cuda.Generator(device="cuda").manual_seed(1)
+    p = problem(cuda, g, 20, 64, 256, 64, True)
+    pr = lora.w4_problems([(p["x"], p["y"], 256, 64, p["codes"], p["scales"], p["zeros"], 64, 256, 64)])
+    ws = cuda.zeros(lora.w4_workspace_size(pr, 20), dtype=cuda.uint8, device="cuda")
+    for T, block, limit, want in ((16, 0, 5_000_000, B.LORA_EINVAL), (20, -1, 5_000_000, B.LORA_EINVAL),
+                                  (20, 0, 1000, B.LORA_EINVAL), (20, 0, 3_000_000_000, B.LORA_ETOOBIG)):
+        with pytest.raises(lora.LoraError) as e:
+            lora.debug_w4_lost_block(pr, T, block, limit, ws, ws.numel(), 0)
+        assert e.value.status == want
+    assert bool((p["y"] == 7).all())
