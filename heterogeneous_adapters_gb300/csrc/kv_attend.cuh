@@ -195,6 +195,9 @@ __device__ __forceinline__ void att_store(const AttendParams& p, int row, int hq
     uint2 w = make_uint2(pack2(x.x * f, x.y * f), pack2(x.z * f, x.w * f));
     *reinterpret_cast<uint2*>(p.out + row * p.ldo + (int64_t)hq * D + d) = w;
 }
+// A factor of scores, kept in the normal range.
+__device__ __forceinline__ float att_normal(float x) { return fminf(fmaxf(x, 1.1754944e-38f), 3.4028235e38f); }
+
 // (scale, offset) of tokens g and g + 8 of a tile and group, at shared address `at` of the first.
 __device__ __forceinline__ void att_params(float2 (&k)[2], uint32_t at) {
     uint32_t a, b;
@@ -323,7 +326,8 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, G, NT)) kv_attend_
             // 2^(13 - e) and its inverse, the exponent e kept where both are normal
             const int e = max(16, min((int)(big >> 23), 254)) - 127;
             const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-            const float back = p.scale * 1.44269504f * __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+            // (kept normal: -inf of a masked score times 0, or 0 times inf, would not be a number)
+            const float back = att_normal(p.scale * 1.44269504f * __uint_as_float((uint32_t)(e - 13 + 127) << 23));
             sl[n][0] = __shfl_sync(0xffffffffu, back, t * 8);
             sl[n][1] = __shfl_sync(0xffffffffu, back, t * 8 + 4);
 #pragma unroll

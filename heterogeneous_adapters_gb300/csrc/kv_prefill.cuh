@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         // ------------------------------------------------------------------ unpacking: a token, half of its values
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int tok = tid & 127, half = (tid - 256) >> 7;
-        const float sl = p.scale * 1.44269504f;
+        const float sl = att_normal(p.scale * 1.44269504f);
         while (ok && walk.next(v, p.rep, c)) {
             for (int st = c.st0; st < c.st1; ++st, ++n) {
                 const uint32_t b = n & 1, ph = (n >> 1) & 1;
@@ -464,8 +464,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw) : "r"(src + kv_params_at(D, D, 0) + tok % kKvTile * 4));
                     const float2 ks = __half22float2(*reinterpret_cast<__half2*>(&kw));
                     float* table = reinterpret_cast<float*>(base + L.table + (n & 3) * kPreTable);
-                    table[tok] = here ? ks.x * sl : 0.f;
-                    table[kPreStep + tok] = here ? ks.y * sl : 0.f;
+                    // (kept finite, if a number: times a score of 0 it has to give 0)
+                    auto finite = [](float x) { return fabsf(x) > 3.4028235e38f ? copysignf(3.4028235e38f, x) : x; };
+                    table[tok] = here ? finite(ks.x * sl) : 0.f;
+                    table[kPreStep + tok] = here ? finite(ks.y * sl) : 0.f;
                     table[2 * kPreStep + tok] = !here ? 0.f : number ? __uint_as_float(ub) : NAN;
                     if (tok == 0) reinterpret_cast<uint32_t*>(table)[3 * kPreStep] = present;
                 }

@@ -1,5 +1,6 @@
 """Attention over the 4-bit cache where the weights of tokens differ by many powers of two, where a
-visible token is not a number; against 64 bits with the bounds of tests/kv_exact.py."""
+visible token is not a number, and at the ends of the arguments' ranges; against 64 bits with the
+bounds of tests/kv_exact.py."""
 import numpy as np
 import pytest
 
@@ -133,3 +134,19 @@ def test_ordinary_values(cuda, dim, group, rows, lens):
     out, lse = case.attend(q)
     assert case.error() == 0
     check(case, q, out, lse)
+
+
+# ---------------------------------------------------------------------------- the ends of the arguments
+
+@pytest.mark.parametrize("dim,group", FORMS)
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 3e38])
+@pytest.mark.parametrize("rows", [1, 20])
+def test_zero_queries_at_any_scale(cuda, dim, group, scale, rows):
+    """q = 0: the mean of the visible values, whatever the scale."""
+    case = Case([rows, 2], [77, 40], heads=4, kv_heads=1, dim=dim, group=group, block=16, seed=4)
+    total = sum(case.lens)
+    fill(case, case.normal(total, dim), case.normal(total, dim))
+    q = cuda.zeros(case.T, 4 * dim, dtype=cuda.bfloat16, device="cuda")
+    out, lse = case.attend(q, scale=scale)
+    assert case.error() == 0
+    check(case, q, out, lse, scale=scale)
