@@ -103,7 +103,7 @@ struct AttSeq {
 
 __device__ __forceinline__ AttSeq att_seq(const KvView& v, int s, bool report) {
     const int a = v.q_start[s], b = v.q_start[s + 1];
-    int len = v.kv_len[s];
+    const int len = kv_length(v, s);
     AttSeq q = {a, b - a, 0};
     uint32_t err = 0;
     if (b < a || a < 0 || b > v.T) err = LORA_DERR_SEGMENT;

@@ -42,6 +42,10 @@ struct KvRow {
     int32_t token;
 };
 
+// Cached tokens of a request; any negative number is none of them (and stays far from the
+// type's end, so that rows can be counted from it).
+__device__ __forceinline__ int kv_length(const KvView& v, int s) { return max(v.kv_len[s], -(1 << 25)); }
+
 // The request that owns `row` and the row's token, by all 32 lanes of a warp together: most
 // decode batches have one row a request, so request `row` is looked at first; else 32
 // places of q_start are read at a time (log32 n_seq dependent reads).
@@ -71,7 +75,7 @@ __device__ __forceinline__ KvRow kv_find_row(const KvView& v, int row) {
     r.token = -1;
     if (a <= row && row < b) {
         const bool bad = a < 0 || b > v.T, big = b - a > v.max_q;
-        if (!bad && !big) r.token = v.kv_len[s] - (b - row);
+        if (!bad && !big) r.token = kv_length(v, s) - (b - row);
         else {
             r.seq = -1;
             if (lane == 0) set_error(v.err, bad ? LORA_DERR_SEGMENT : LORA_DERR_KV);

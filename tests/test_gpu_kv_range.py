@@ -150,3 +150,23 @@ def test_zero_queries_at_any_scale(cuda, dim, group, scale, rows):
     out, lse = case.attend(q, scale=scale)
     assert case.error() == 0
     check(case, q, out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("length", [-5, -(1 << 31)])
+def test_negative_lengths_hold_no_token(cuda, length):
+    """As any length below the request's rows: nothing appended, zeros read back and attended, no error."""
+    case = Case([1, 2, 60], [20, 30, 80], heads=4, kv_heads=2, dim=128, group=128, block=16)
+    case.fill()
+    q, k, v = case.normal(63, 512), case.normal(63, 256), case.normal(63, 256)
+    case.kv_len.copy_(cuda.tensor([20, length, length], dtype=cuda.int32))
+    before = case.cache.clone()
+    out = case.append(q, k, v, case.rope())
+    rk, rv = case.read()
+    o, lse = case.attend(q)
+    assert case.error() == 0
+    assert not bool(out[1:].any()) and not bool(rk[1:].any()) and not bool(rv[1:].any()) and not bool(o[1:].any())
+    assert bool((lse[1:] == -float("inf")).all()) and bool(o[0].any())
+    case.kv_len[0] = length
+    case.cache.copy_(before)
+    case.append(q, k, v, case.rope())
+    assert case.error() == 0 and cuda.equal(before, case.cache)
