@@ -86,10 +86,12 @@ __device__ __forceinline__ KvRow kv_find_row(const KvView& v, int row) {
     return r;
 }
 
-// Looks for requests whose rows decrease, 32 places of q_start a warp of the launch.
+// Looks for requests whose rows decrease or leave [0, T], 32 places of q_start a warp of the launch.
 __device__ __forceinline__ void kv_check_starts(const KvView& v, int64_t warp, int64_t warps) {
-    for (int64_t i = warp * 32 + (threadIdx.x & 31); i < v.n_seq; i += warps * 32)
-        if (v.q_start[i] > v.q_start[i + 1]) set_error(v.err, LORA_DERR_SEGMENT);
+    for (int64_t i = warp * 32 + (threadIdx.x & 31); i < v.n_seq; i += warps * 32) {
+        const int a = v.q_start[i], b = v.q_start[i + 1];
+        if (a > b || a < 0 || b > v.T) set_error(v.err, LORA_DERR_SEGMENT);
+    }
 }
 
 // Address of the tile that holds `token` (>= 0) of request `seq` and head; nullptr (and the

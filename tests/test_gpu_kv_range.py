@@ -7,7 +7,7 @@ import pytest
 import heterogeneous_adapters_gb300 as lora
 
 from .kv_exact import check
-from .test_gpu_kv import Case
+from .test_gpu_kv import SEG, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,17 @@ def test_negative_lengths_hold_no_token(cuda, length):
     case.cache.copy_(before)
     case.append(q, k, v, case.rope())
     assert case.error() == 0 and cuda.equal(before, case.cache)
+
+
+@pytest.mark.parametrize("start", [[0, 2, 4, 9], [-3, -1, 2, 4], [0, 1, 5, 5]])
+def test_every_call_reports_rows_outside_the_batch(cuda, start):
+    """Requests whose rows leave [0, T] set the segment bit, also where none of their rows is a row of the batch."""
+    case = Case([2, 1, 1], [40, 20, 5], heads=4, kv_heads=2, block=16)
+    case.fill()
+    assert case.error() == 0
+    case.q_start.copy_(cuda.tensor(start, dtype=cuda.int32))
+    case.batch = lora.KvBatch(case.q_start, case.kv_len, case.table, 3, 4, case.max_blocks, 16)
+    q, k, v = case.normal(4, 512), case.normal(4, 256), case.normal(4, 256)
+    for call in (lambda: case.append(q, k, v, case.rope()), case.read, lambda: case.attend(q)):
+        call()
+        assert case.error() == SEG
