@@ -38,6 +38,9 @@ lora_status check_sizes(const lora_kv_cache_desc* c, const lora_kv_batch* b) {
 
 size_t workspace_bytes() { return align256(std::max(attend_workspace(2, 128), pre_workspace(128))); }
 
+// Arrays of 32-bit values (an odd address would fault the kernels).
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
 lora_status check_call(const lora_kv_cache_desc* c, const lora_kv_batch* b, const void* ws, size_t ws_bytes, size_t need) {
     lora_status st = check_sizes(c, b);
     if (st != LORA_OK) return st;
@@ -47,6 +50,7 @@ lora_status check_call(const lora_kv_cache_desc* c, const lora_kv_batch* b, cons
         return LORA_EINVAL;
     if (b->n_seq > 0 && (b->q_start == nullptr || b->kv_len == nullptr || (b->max_blocks > 0 && b->block_table == nullptr)))
         return LORA_EINVAL;
+    if (!aligned4(b->q_start) || !aligned4(b->kv_len) || !aligned4(b->block_table)) return LORA_EALIGN;
     if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < need) return LORA_EWORKSPACE;
     return LORA_OK;
 }
@@ -194,6 +198,7 @@ lora_status lora_kv_append(const lora_kv_cache_desc* cache, const lora_kv_batch*
         if (rope->cos == nullptr || rope->sin == nullptr || rope->max_pos <= 0) return LORA_EINVAL;
         if (!aligned16(rope->cos) || !aligned16(rope->sin)) return LORA_EALIGN;
     }
+    if (!aligned4(rope->positions)) return LORA_EALIGN;
     if (batch->T == 0 || batch->n_seq == 0) return LORA_OK;
     if (num_q_heads > 0) {
         if ((st = check_rows(q, ldq, num_q_heads * dim)) != LORA_OK) return st;
@@ -264,6 +269,7 @@ lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch*
     const int64_t cols = (int64_t)num_q_heads * cache->head_dim;
     if ((st = check_rows(q, ldq, cols)) != LORA_OK) return st;
     if ((st = check_rows(out, ldo, cols)) != LORA_OK) return st;
+    if (!aligned4(lse)) return LORA_EALIGN;
     AttendParams p;
     p.v = view_of(cache, batch, ws);
     p.q = reinterpret_cast<const __nv_bfloat16*>(q);

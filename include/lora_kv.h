@@ -50,8 +50,9 @@ typedef struct {
  * (q_start[0] >= 0, non-decreasing, q_start[n_seq] <= T; a request may have no rows) and
  * the tokens 0 .. kv_len[s] - 1 of the cache, of which its rows are the last ones: the
  * request's row i (of m) is token kv_len[s] - m + i.  Token t lies in block
- * block_table[s][t / block_tokens].  All arrays are device memory.  Entries of the table
- * beyond a request's tokens are not read. */
+ * block_table[s][t / block_tokens].  All arrays are device memory, 4-byte aligned (as are
+ * positions and lse below, else LORA_EALIGN).  Entries of the table beyond a request's
+ * tokens are not read. */
 typedef struct {
     const int32_t* q_start;      /* [n_seq + 1]                                        */
     const int32_t* kv_len;       /* [n_seq]                                            */
