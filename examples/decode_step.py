@@ -6,7 +6,7 @@ over it (kv_attend), and the output projection with its delta.
 The cache's blocks and the adapters' rows live in one pool of pages, as the unified pool is
 meant: block b is a run of pool pages.
 
-    python examples/decode_step.py            # a Llama-3-8B layer, 64 requests, timed
+    python examples/decode_step.py            # a Llama-3-8B layer, 64 requests, in one CUDA graph, timed
 """
 from __future__ import annotations
 
@@ -89,11 +89,34 @@ class Layer:
         lora.kv_workspace_init(self.step_ws, self.step_bytes, stream)
         torch.cuda.current_stream().synchronize()
 
+        self.graph = None
+
     def step(self, x):
         """x bf16 [requests][h] -> the layer's attention output, the cache one token longer."""
+        self.x.copy_(x)
+        if self.graph is not None:
+            self.graph.replay()
+        else:
+            self.calls()
+        return self.out
+
+    def capture(self):
+        """Later steps replay one CUDA graph of the calls: their buffers stay where they are, and the
+        lengths advance on the device."""
+        side, lens = torch.cuda.Stream(), self.kv_len.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            self.calls()                        # loads the kernels; the next step writes the same token again
+            self.kv_len.copy_(lens)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                self.calls()
+        torch.cuda.current_stream().wait_stream(side)
+        self.graph = graph
+
+    def calls(self):
         stream = torch.cuda.current_stream().cuda_stream
         ws, step = (self.ws, self.ws_bytes, stream), (self.step_ws, self.step_bytes, stream)
-        self.x.copy_(x)
         self.kv_len += 1
         lora.w4_matvec(self.w_qkv, self.T, *step)
         lora.bgmv(self.pool, self.d_qkv, self.adapter, self.T, *ws)
@@ -102,7 +125,6 @@ class Layer:
         lora.kv_attend(self.kv, self.batch, self.q, nq, self.heads, self.dim ** -0.5, self.att, nq, None, *step)
         lora.w4_matvec(self.w_out, self.T, *step)
         lora.bgmv(self.pool, self.d_out, self.adapter, self.T, *ws)
-        return self.out
 
     def errors(self):
         stream = torch.cuda.current_stream().cuda_stream
@@ -112,6 +134,7 @@ class Layer:
 def main():
     layer = Layer()
     x = torch.randn(layer.T, layer.h, device="cuda").bfloat16()
+    layer.capture()
     for _ in range(200):
         layer.step(x)
     torch.cuda.synchronize()
