@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(kAttThreads, attend_ctas(D, G, NT)) kv_attend_
 
         for (int i = 0; i < mine_n; ++i, ++it) {
             const uint32_t stage = it % kAttStages;
-            if (!mbar_wait(wbar + stage * 8, (it / kAttStages) & 1, kWaitLimitNs)) {
-                // let the copies in flight land; the rest of the range does no work
+            if (!__all_sync(0xffffffffu, mbar_wait(wbar + stage * 8, (it / kAttStages) & 1, kWaitLimitNs))) {
+                // (the warp as one) let the copies in flight land; the rest of the range does no work
                 ok = false;
                 for (int k = 1; k < kAttStages; ++k)
                     mbar_wait(wbar + ((it + k) % kAttStages) * 8, ((it + k) / kAttStages) & 1, 100000000ull);

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         // These warps meet at named barriers, so none of them leaves early: after a wait that ran
         // out, `wait` returns at once and the rest of the range goes by (with the error set).
         auto wait = [&](uint64_t& which, uint32_t parity) {
-            if (ok && !mbar_wait(bar(which), parity, kWaitLimitNs)) {
+            if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(which), parity, kWaitLimitNs))) {
                 ok = false;
                 if (lane == 0) set_error(v.err, LORA_DERR_TIMEOUT);
             }
@@ -424,15 +424,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
         // ------------------------------------------------------------------ unpacking: a token, half of its values
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int tok = tid & 127, half = (tid - 256) >> 7;
+        auto wait = [&](uint64_t& which, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait(bar(which), parity, kWaitLimitNs));
+        };
         const float sl = att_normal(p.scale * 1.44269504f);
         while (ok && walk.next(v, p.rep, c)) {
             for (int st = c.st0; st < c.st1; ++st, ++n) {
                 const uint32_t b = n & 1, ph = (n >> 1) & 1;
-                if (!mbar_wait(bar(code_full[b]), ph, kWaitLimitNs)) { ok = false; break; }
+                if (!wait(code_full[b], ph)) { ok = false; break; }
                 const uint32_t src = sm + L.codes + b * pre_code_bytes(D) + (tok / kKvTile) * kTile;
                 const uint32_t at = src + (tok % kKvTile) * 16;
                 // the buffer's last S is done (and with it the rows' use of the table four blocks ago)
-                if (!mbar_wait(bar(s_full[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!wait(s_full[b], ph ^ 1)) { ok = false; break; }
                 // K: 16-byte pieces of 32 values; a row of 64 values is 128 bytes, swizzled
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(k_full[b]));
-                if (!mbar_wait(bar(v_empty[b]), ph ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!wait(v_empty[b], ph ^ 1)) { ok = false; break; }
                 // W: rows of tokens, [token / 8][64 values][token % 8]
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
@@ -566,7 +569,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const __grid
                 const int t = st * kPreStep + lane * kKvTile;
                 const unsigned char* tile = lane < 8 && t < tokens ? kv_tile_of(v, c.seq, t, c.head, kTile) : nullptr;
                 const uint32_t present = __ballot_sync(0xffffffffu, tile != nullptr);
-                if (!mbar_wait_quiet(bar(code_empty[b]), ((n >> 1) & 1) ^ 1, kWaitLimitNs)) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, mbar_wait_quiet(bar(code_empty[b]), ((n >> 1) & 1) ^ 1, kWaitLimitNs))) { ok = false; break; }
                 if (lane == 0) {
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(sm + L.mask + b * 4), "r"(present) : "memory");
                     mbar_arrive_expect_tx(bar(code_full[b]), __popc(present) * kTile);
