@@ -37,10 +37,13 @@ constexpr int kPreRows = 128, kPreStep = 128, kPreThreads = 18 * 32;
 constexpr int kPreItemCost = 6;
 constexpr int kPreMinUnits = 8;
 constexpr int kPreMaxCtas = 192;
-// A request's packed rows per KV head from which this kernel serves it.  16 requests over 4000
-// tokens: 32 rows 56 us in kv_attend.cuh, 48 rows 77, 64 rows 95, and here 61 for 48 (heads of
-// 64: 48 rows 32 and 64 rows 41 there, 36 here for 64).
-constexpr int kPreMinPacked = 48;
+// A request's packed rows per KV head from which this kernel serves it: where the few-row kernel
+// takes a third tile of 16 of them (heads of 128) or a fourth (64).  16 requests over 4000
+// tokens, 8 KV heads, us there and here: heads of 128, 32 rows 57 and 61, 40 rows 77 and 61, 64
+// rows 97 and 61; heads of 64, 48 rows 52 and 56, 64 rows 65 and 56.  Few requests reach the
+// same point later (heads of 128, 4 requests: 32 rows 26 and 31, 40 rows 31 and 31; one: 40 rows
+// 22 and 30, 128 rows 27 and 32, 192 rows 33 and 32), hence not before a fourth tile there.
+__host__ __device__ constexpr int pre_min_packed(int dim, int64_t seq_heads) { return dim == 128 && seq_heads >= 32 ? 33 : 49; }
 
 constexpr int kPreTable = 3 * kPreStep * 4 + 16;
 __host__ __device__ constexpr int pre_code_bytes(int dim) { return kPreStep / kKvTile * kv_tile_bytes(dim, dim); }

@@ -285,7 +285,7 @@ lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch*
     cudaStream_t cs = (cudaStream_t)stream;
     // requests with many packed rows take the tensor-core tiles, the others the decode kernel:
     // a launch each (how many rows a request has only the device knows)
-    const int32_t many = (kPreMinPacked + p.rep - 1) / p.rep;
+    const int32_t many = (pre_min_packed(cache->head_dim, (int64_t)batch->n_seq * cache->num_kv_heads) + p.rep - 1) / p.rep;
     if (cache->group == cache->head_dim && batch->max_q >= many) {
         p.v.rows_lo = many;
         if ((st = cache->head_dim == 128 ? prefill<128>(p, cs) : prefill<64>(p, cs)) != LORA_OK) return st;

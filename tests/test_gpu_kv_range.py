@@ -184,3 +184,17 @@ def test_every_call_reports_rows_outside_the_batch(cuda, start):
     for call in (lambda: case.append(q, k, v, case.rope()), case.read, lambda: case.attend(q)):
         call()
         assert case.error() == SEG
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("requests", [4, 40])
+def test_requests_of_either_kernel_in_one_call(cuda, dim, requests):
+    """Requests of 28 to 56 packed rows, on both sides of where the kernel for many rows takes over."""
+    rows = [7 + i % 8 for i in range(requests)]
+    case = Case(rows, [60 + 17 * i for i in range(requests)], heads=4, kv_heads=1, dim=dim, group=dim, block=32, seed=6)
+    total = sum(case.lens)
+    fill(case, case.normal(total, dim), case.normal(total, dim))
+    q = case.normal(case.T, 4 * dim)
+    out, lse = case.attend(q)
+    assert case.error() == 0
+    check(case, q, out, lse)
