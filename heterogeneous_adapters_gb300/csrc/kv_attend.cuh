@@ -23,10 +23,11 @@
 // because the kernel is bound by the bytes of the cache (136 a token and head) and next by
 // the unpacking, not by the MMAs.
 //
-// Measured (grouped queries, 4 per KV head): 64 requests of 17 to 8191 tokens 63 us and two of
-// 131k tokens 63 us, 64% of the copy rate on their 271 and 277 MB; one query head per KV head
-// with groups of 32 (278 MB) 88 us.  The tensor pipe is 22% busy, the issue slots 60% while
-// warps are resident: about 640 instructions per 32 tokens of a head at 16 warps an SM.
+// Measured (grouped queries, 4 per KV head): 64 requests of 17 to 8191 tokens 64 us and two of
+// 131k tokens 64 us, 62% of the copy rate on their 271 and 277 MB; one query head per KV head
+// with groups of 32 (278 MB) 90 us.  (Weights rounded by the conversion to f16 alone, which loses
+// those far below the largest: 63, 63 and 88.)  The tensor pipe is 22% busy, the issue slots 59%
+// while warps are resident: about 650 instructions per 32 tokens of a head at 16 warps an SM.
 //
 // Work.  An item is (request, KV head, tile of 8 NT packed rows), of ceil(tokens / 32) steps
 // and kAttItemCost more for its fixed part.  The units of all items in a row are dealt to

@@ -8,8 +8,8 @@
 // difference is wrong near the zero point and for an infinite x, and not faster: 13 rows of
 // q, k, v 11.6 us, and 10.5 as it is.)  The weights are the long side: 16 rows of W are an
 // MMA's rows and 8 rows of x its columns.  What bounds it is the stream of W (half a byte a
-// weight), next the unpacking: one row of 4096 x 4096 takes 7.8 us (two of launch, three to the
-// first data), of two 14336 x 4096 21.8 us, 41% of the copy rate, where the copies alone
+// weight), next the unpacking: one row of 4096 x 4096 takes 7.7 us (two of launch, three to the
+// first data), of two 14336 x 4096 21.7 us, 41% of the copy rate, where the copies alone
 // take 12.6.
 //
 // Work.  A block of work is 32 rows of W by 256 of K (4 KB of codes); blocks of all

@@ -8,11 +8,11 @@
 // group: a thread per row of W reads its columns and adds scale * D to sums in registers.
 // Half a byte a weight from memory is the floor; unpacking (13 / 8 instructions a weight, in
 // the order of K) and draining (one FMA per group, row and column) fill most of the issue
-// slots of that time at 64 rows.  Measured on two 14336 x 4096 of groups of 128: 17 rows 24.0 us,
-// 64 rows 26.5 us (36% of the copy rate), 128 rows 39.3 us (40% of the bf16 rate); groups of 64
+// slots of that time at 64 rows.  Measured on two 14336 x 4096 of groups of 128: 17 rows 24.2 us,
+// 64 rows 26.5 us (36% of the copy rate), 128 rows 39.6 us (40% of the bf16 rate); groups of 64
 // and 32 at 64 rows 30 and 41 us.  An MMA of 128 rows with A in tensor memory takes 64 clocks
 // for any N up to 128, so a block is 1024 clocks of MMA at least; it takes about 1500, with some
-// 3,800 instructions.
+// 3,900 instructions.
 //
 // One CTA per SM: warp 0 streams codes (blocks of 128 rows x 256 of K) by TMA and warp 11 x,
 // warp 1 issues the MMAs, warps 2-9 unpack, warp 10 brings scales and zero points, the others

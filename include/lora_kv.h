@@ -131,7 +131,10 @@ lora_status lora_kv_read(const lora_kv_cache_desc* cache, const lora_kv_batch* b
  * meet the weights in f16, whose steps end at 2^-28 of a row's largest p |v|: a token may be
  * off by that much beside.  The result does not depend on how the device schedules the work.
  * A token whose V is not a number makes the outputs of its group so, for the rows that see it.
- * num_q_heads is a multiple of num_kv_heads. */
+ * num_q_heads is a multiple of num_kv_heads.  Requests with many rows (chunks of prompts) are
+ * served fast where group = head_dim; with groups of 32 the cache is read and unpacked once per
+ * 16 rows times query heads of a KV head (three chunks of 300 to 512 rows over 3,111 to 6,000
+ * tokens, 32 query and 8 KV heads of 128: 137 us and 741 us). */
 lora_status lora_kv_attend(const lora_kv_cache_desc* cache, const lora_kv_batch* batch, const void* q, int64_t ldq,
                            int32_t num_q_heads, float softmax_scale, void* out, int64_t ldo, float* lse, void* ws,
                            size_t ws_bytes, void* stream);
