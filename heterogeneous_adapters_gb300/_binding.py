@@ -25,6 +25,13 @@ LORA_KV_MAX_SEQS = 16384
 LORA_ROPE_HALVES, LORA_ROPE_PAIRS = range(2)
 LORA_W4_MAX_ROWS = 256
 LORA_W4_MAX_PROBLEMS = 16
+LORA_Q8_MAX_WIDTH = 32768
+LORA_Q8_MAX_ROWS = 1 << 24
+LORA_W8_MAX_ROWS = 65536
+LORA_W8_MAX_PROBLEMS = 16
+LORA_W8_MAX_K = 65536
+LORA_Q8_X_HELD, LORA_Q8_X_FULL = range(2)
+LORA_ACT_NONE, LORA_ACT_SILU, LORA_ACT_GELU, LORA_ACT_GELU_TANH = range(4)
 
 EXPORTED = ["lora_pool_create", "lora_pool_destroy", "lora_pool_set_tuning", "lora_pool_get_tuning",
             "lora_workspace_size", "lora_workspace_init",
@@ -39,7 +46,9 @@ EXPORTED = ["lora_pool_create", "lora_pool_destroy", "lora_pool_set_tuning", "lo
             "lora_sched_destroy", "lora_sched_enqueue", "lora_sched_pick", "lora_sched_pending",
             # the 4-bit KV cache (include/lora_kv.h) and 4-bit weights (include/lora_w4.h)
             "lora_kv_block_bytes", "lora_kv_workspace_size", "lora_kv_workspace_init", "lora_kv_append",
-            "lora_kv_read", "lora_kv_attend", "lora_w4_workspace_size", "lora_w4_matvec", "lora_debug_w4_lost_block"]
+            "lora_kv_read", "lora_kv_attend", "lora_w4_workspace_size", "lora_w4_matvec", "lora_debug_w4_lost_block",
+            # an 8-bit base model (include/lora_w8.h)
+            "lora_q8_norm", "lora_q8_gate", "lora_w8_workspace_size", "lora_w8_matmul"]
 
 
 class lora_pool_desc(ctypes.Structure):
@@ -97,6 +106,28 @@ class lora_w4_problem(ctypes.Structure):
                 ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p),
                 ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class lora_q8_rows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("x", ctypes.c_void_p), ("ldc", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("x_kind", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class lora_q8_norm_desc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("lds", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("d", ctypes.c_int32), ("out", lora_q8_rows)]
+
+
+class lora_q8_gate_desc(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("ldg", ctypes.c_int64), ("ldu", ctypes.c_int64),
+                ("act", ctypes.c_int32), ("d", ctypes.c_int32), ("out", lora_q8_rows)]
+
+
+class lora_w8_problem(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("x_scales", ctypes.c_void_p), ("y", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("w_scales", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32)]
 
 
 class LoraError(RuntimeError):
@@ -165,6 +196,10 @@ def lib():
             "lora_w4_workspace_size": [p, i32, i32, ctypes.POINTER(sz)],
             "lora_w4_matvec": [p, i32, i32, p, sz, p],
             "lora_debug_w4_lost_block": [p, i32, i32, i32, ctypes.c_uint64, p, sz, p],
+            "lora_q8_norm": [p, i32, p],
+            "lora_q8_gate": [p, i32, p],
+            "lora_w8_workspace_size": [p, i32, i32, ctypes.POINTER(sz)],
+            "lora_w8_matmul": [p, i32, i32, p, sz, p],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -448,10 +483,10 @@ def w4_problems(problems):
     arr = (lora_w4_problem * max(1, len(problems)))()
     for i, (x, y, ldx, ldy, codes, scales, zeros, n, k, group) in enumerate(problems):
         arr[i] = lora_w4_problem(_ptr(x), _ptr(y), ldx, ldy, _ptr(codes), _ptr(scales), _ptr(zeros), n, k, group, 0)
-    return _W4Problems(arr, problems)
+    return _Problems(arr, problems)
 
 
-class _W4Problems(_Desc):
+class _Problems(_Desc):
     def __init__(self, arr, problems):
         super().__init__(arr, problems)
         self.n = len(problems)
@@ -472,6 +507,64 @@ def debug_w4_lost_block(problems, T, block, limit_ns, ws, ws_bytes, stream):
     """w4_matvec with one block's codes missing: its waits run out after limit_ns."""
     _check(lib().lora_debug_w4_lost_block(problems.ref, problems.n, T, block, limit_ns, _ptr(ws), ws_bytes, stream),
            "lora_debug_w4_lost_block")
+
+
+# ----------------------------------------------------------------------------- an 8-bit base model
+
+class Q8Rows(_Desc):
+    """Where rows go in 8 bits (lora_q8_rows): int8 codes [T][ldc], f32 scales [T], and in bf16 x
+    [T][ldx] (or None) what the codes stand for (LORA_Q8_X_HELD) or the rows themselves (LORA_Q8_X_FULL)."""
+
+    def __init__(self, codes, ldc, scales, x=None, ldx=0, x_kind=LORA_Q8_X_HELD):
+        super().__init__(lora_q8_rows(_ptr(codes), _ptr(scales), _ptr(x), ldc, ldx, x_kind, 0), codes, scales, x)
+
+
+class Q8Norm(_Desc):
+    """A norm's buffers (lora_q8_norm_desc), kept by the caller for as long as the tensors stay where
+    they are: bf16 x and residual (or None) in, their sum out (or None), bf16 weight [d], rows a Q8Rows."""
+
+    def __init__(self, x, ldx, residual, ldr, total, lds, weight, eps, d, rows):
+        super().__init__(lora_q8_norm_desc(_ptr(x), _ptr(residual), _ptr(total), _ptr(weight), ldx, ldr, lds, eps, d, rows.struct),
+                         x, residual, total, weight, rows)
+
+
+class Q8Gate(_Desc):
+    """A gated activation's buffers (lora_q8_gate_desc): bf16 gate and up (or None), act one of
+    LORA_ACT_*, rows a Q8Rows."""
+
+    def __init__(self, gate, ldg, up, ldu, act, d, rows):
+        super().__init__(lora_q8_gate_desc(_ptr(gate), _ptr(up), ldg, ldu, act, d, rows.struct), gate, up, rows)
+
+
+def q8_norm(norm, T, stream):
+    """The residual's addition and root-mean-square norm of T rows, left in 8 bits."""
+    _check(lib().lora_q8_norm(norm.ref, T, stream), "lora_q8_norm")
+
+
+def q8_gate(gate, T, stream):
+    """act(gate) * up of T rows, left in 8 bits."""
+    _check(lib().lora_q8_gate(gate.ref, T, stream), "lora_q8_gate")
+
+
+def w8_problems(problems):
+    """The projections of a call, kept by the caller for as long as the tensors stay where
+    they are: (x, x_scales, y, ldx, ldy, w, w_scales, N, K) each."""
+    problems = list(problems)
+    arr = (lora_w8_problem * max(1, len(problems)))()
+    for i, (x, x_scales, y, ldx, ldy, w, w_scales, n, k) in enumerate(problems):
+        arr[i] = lora_w8_problem(_ptr(x), _ptr(x_scales), _ptr(y), _ptr(w), _ptr(w_scales), ldx, ldy, n, k)
+    return _Problems(arr, problems)
+
+
+def w8_workspace_size(problems, T: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().lora_w8_workspace_size(problems.ref, problems.n, T, ctypes.byref(n)), "lora_w8_workspace_size")
+    return n.value
+
+
+def w8_matmul(problems, T, ws, ws_bytes, stream):
+    """y = x W^T of 8-bit integers for every projection of w8_problems(...)."""
+    _check(lib().lora_w8_matmul(problems.ref, problems.n, T, _ptr(ws), ws_bytes, stream), "lora_w8_matmul")
 
 
 # ----------------------------------------------------------------------------- host runtime

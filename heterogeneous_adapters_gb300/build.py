@@ -15,7 +15,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 # scheduler; host-only C++)
 SOURCES = [os.path.join(PKG, "csrc", f) for f in
            ("lora_api.cu", "launch_ring.cu", "launch_tile.cu", "launch_cluster.cu", "launch_kv.cu",
-            "launch_w4.cu", "runtime.cpp")]
+            "launch_w4.cu", "launch_w8.cu", "runtime.cpp")]
 
 
 def nvcc() -> str:

@@ -1,0 +1,111 @@
+/* lora_w8.h - an 8-bit base model's layers beside 16-bit adapters (liblora.so).
+ *
+ * Products y = x W^T of 8-bit integers, for decode batches and whole prompts, and the two
+ * operators that leave rows in the 8 bits that these products read: the residual's addition
+ * with the root-mean-square norm (before q/k/v and before the MLP), and the gated activation
+ * (before the MLP's last projection; without an activation it puts any rows into 8 bits, such
+ * as the attention's output).  The delta of lora.h is added to the products' y, and reads the
+ * same rows in 16 bits ("Multi-LoRA serving: S-LoRA, Punica and adapter batching" (pofe.ai),
+ * the paragraph on quantised bases with 16-bit adapters).  Because the deltas are added to the
+ * two projections of the MLP before their activation, that is not part of the product.
+ * Conventions (streams, status codes, no allocation, no host synchronisation, bounded waits,
+ * threading) are those of lora.h.
+ *
+ * A row y of width d in 8 bits:
+ *     scale = max |y| / 127,   code_i = rint(y_i / scale)  (ties to even; 0 if scale = 0),
+ * and a code c stands for scale * c.  A row that holds a value that is not finite has the
+ * scale NaN and codes 0, and so stands for NaN in every product. */
+#ifndef LORA_W8_GB300_H
+#define LORA_W8_GB300_H
+
+#include "lora.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define LORA_Q8_MAX_WIDTH 32768
+#define LORA_Q8_MAX_ROWS (1 << 24)
+#define LORA_W8_MAX_ROWS 65536
+#define LORA_W8_MAX_PROBLEMS 16
+#define LORA_W8_MAX_K 65536
+
+/* Rows in 8 bits, and the same rows in bf16 for the adapters of the layer. */
+enum { LORA_Q8_X_HELD = 0,       /* x = bf16(scale * code): what the base product sees, so that
+                                    base and delta are the product with W + s B A           */
+       LORA_Q8_X_FULL = 1 };     /* x = bf16(y)                                             */
+typedef struct {
+    void* codes;                 /* int8 [T][ldc], 16-byte aligned, ldc % 16 == 0           */
+    float* scales;               /* [T], 4-byte aligned                                     */
+    void* x;                     /* bf16 [T][ldx], 16-byte aligned, ldx % 8 == 0; or NULL   */
+    int64_t ldc;
+    int64_t ldx;
+    int32_t x_kind;
+    int32_t reserved;            /* 0                                                       */
+} lora_q8_rows;
+
+/* The norm: with h = bf16(x + residual) (x itself without a residual),
+ *     y = h weight / sqrt(mean h^2 + eps),
+ * left in 8 bits.  The sum of squares is fp32.  The codes are those of the exact quotients
+ * (they depend on h weight alone); scales are within a few 2^-24 of theirs. */
+typedef struct {
+    const void* x;               /* bf16 [T][ldx]                                           */
+    const void* residual;        /* bf16 [T][ldr], or NULL                                  */
+    void* sum;                   /* bf16 [T][lds]: h; NULL without a residual, or if unused.
+                                    May be x or residual with its pitch                     */
+    const void* weight;          /* bf16 [d]                                                */
+    int64_t ldx;
+    int64_t ldr;
+    int64_t lds;
+    float eps;                   /* 1e-30 or more                                           */
+    int32_t d;                   /* a multiple of 16, at most LORA_Q8_MAX_WIDTH             */
+    lora_q8_rows out;
+} lora_q8_norm_desc;
+
+/* The gated activation: y = act(gate) up (act(gate) without up), in fp32, left in 8 bits. */
+enum { LORA_ACT_NONE = 0, LORA_ACT_SILU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3 };
+typedef struct {
+    const void* gate;            /* bf16 [T][ldg]                                           */
+    const void* up;              /* bf16 [T][ldu], or NULL                                  */
+    int64_t ldg;
+    int64_t ldu;
+    int32_t act;
+    int32_t d;                   /* a multiple of 16, at most LORA_Q8_MAX_WIDTH             */
+    lora_q8_rows out;            /* out.x may be gate or up with its pitch                  */
+} lora_q8_gate_desc;
+
+/* Rows 0 .. T - 1; T <= LORA_Q8_MAX_ROWS.  Arrays are 16-byte aligned with pitches that are
+ * multiples of 8 and at least d (LORA_EALIGN, LORA_EINVAL); apart from the cases named above,
+ * what is written overlaps nothing else. */
+lora_status lora_q8_norm(const lora_q8_norm_desc* norm, int32_t T, void* stream);
+lora_status lora_q8_gate(const lora_q8_gate_desc* gate, int32_t T, void* stream);
+
+/* One projection, y[t, n] = bf16(x_scales[t] w_scales[n] sum_k x[t, k] w[n, k]). */
+typedef struct {
+    const void* x;               /* int8 [T][ldx], 16-byte aligned, ldx % 16 == 0           */
+    const float* x_scales;       /* [T], 4-byte aligned                                     */
+    void* y;                     /* bf16 [T][ldy], overwritten, 16-byte aligned, ldy % 8 == 0 */
+    const void* w;               /* int8 [N][K], 16-byte aligned                            */
+    const float* w_scales;       /* [N], 4-byte aligned                                     */
+    int64_t ldx;
+    int64_t ldy;
+    int32_t N;                   /* a multiple of 8                                         */
+    int32_t K;                   /* a multiple of 16, at most LORA_W8_MAX_K                 */
+} lora_w8_problem;
+
+/* Bytes of device workspace for the call: the device error word, partial sums and, for many
+ * rows, x in the type that the tensor cores read; problems with the same x, ldx and K share
+ * that.  (Other pointers are not read.)  A workspace serves calls of fewer rows too.  Prepare
+ * it once with lora_kv_workspace_init (lora_kv.h); one workspace, large enough for all, may
+ * serve the calls of lora_kv.h, lora_w4.h and this one. */
+lora_status lora_w8_workspace_size(const lora_w8_problem* probs, int32_t nprob, int32_t T, size_t* bytes);
+
+/* All projections of the call, at most LORA_W8_MAX_PROBLEMS, over the same T <=
+ * LORA_W8_MAX_ROWS rows (their x may differ). */
+lora_status lora_w8_matmul(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
+                           void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* LORA_W8_GB300_H */
