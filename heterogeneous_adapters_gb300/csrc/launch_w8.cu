@@ -6,6 +6,7 @@
 #include "host.h"
 #include "q8_rows.cuh"
 #include "w8_narrow.cuh"
+#include "w8_wide.cuh"
 
 using namespace lora;
 using namespace lora::host;
@@ -69,9 +70,173 @@ lora_status check_sizes(const lora_w8_problem* probs, int32_t nprob, int32_t T) 
     return LORA_OK;
 }
 
+// Rows up to which w8_narrow.cuh serves.
+constexpr int kW8NarrowRows = 32;
+// Steps that joining a tile from several pairs costs.
+constexpr int kW8JoinCost = 8;
+
+// Tiles of a wide call along x.
+struct WideShape {
+    int nmax, cols, ttiles;
+};
+WideShape wide_shape(int32_t T) {
+    if (T <= 256) {
+        const int cols = (T + 31) / 32 * 32;
+        return {cols <= 64 ? 64 : cols <= 128 ? 128 : 256, cols, 1};
+    }
+    const int tiles = (T + 255) / 256;
+    return {256, ((T + tiles - 1) / tiles + 31) / 32 * 32, tiles};
+}
+
+// The first problem with i's x.
+int32_t x_of(const lora_w8_problem* probs, int32_t i) {
+    int32_t j = 0;
+    while (probs[j].x != probs[i].x || probs[j].ldx != probs[i].ldx || probs[j].K != probs[i].K) ++j;
+    return j;
+}
+
+size_t x_bytes(const lora_w8_problem& p, int32_t T) { return align256((size_t)T * p.K * 2); }
+
 size_t workspace_bytes(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
-    (void)probs; (void)nprob; (void)T;
-    return align256(kStepPartAt);
+    if (T <= kW8NarrowRows) return align256(kStepPartAt);
+    size_t n = align256(kStepPartAt) + w8_part_bytes(wide_shape(T).nmax);
+    for (int32_t i = 0; i < nprob; ++i)
+        if (x_of(probs, i) == i) n += x_bytes(probs[i], T);
+    return n;
+}
+
+lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, cudaStream_t s) {
+    static thread_local W8Params p;
+    memset(&p, 0, sizeof p);
+    p.T = T;
+    p.nprob = nprob;
+    int64_t total = 0;
+    for (int32_t i = 0; i < nprob; ++i) {
+        const lora_w8_problem& pr = probs[i];
+        p.prob[i] = {reinterpret_cast<const unsigned char*>(pr.x), pr.x_scales, reinterpret_cast<__nv_bfloat16*>(pr.y),
+                     reinterpret_cast<const unsigned char*>(pr.w), pr.w_scales, pr.ldx, pr.ldy, pr.N, pr.K, (int32_t)total};
+        total += (pr.N + kW8Rows - 1) / kW8Rows;
+    }
+    p.total = (int32_t)total;
+    const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
+    if (nt == 1) w8_narrow_kernel<1><<<(unsigned)total, kW8Threads, 0, s>>>(p);
+    else if (nt == 2) w8_narrow_kernel<2><<<(unsigned)total, kW8Threads, 0, s>>>(p);
+    else w8_narrow_kernel<4><<<(unsigned)total, kW8Threads, 0, s>>>(p);
+    return cuda_status(cudaGetLastError());
+}
+
+// 2-D map of `rows` rows of `inner` elements, box {box0, box1}, zeros outside.
+lora_status map2d(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                  uint64_t inner, uint64_t rows, uint64_t pitch, uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {pitch};
+    const cuuint32_t box[2] = {box0, box1}, one[2] = {1, 1};
+    const CUresult r = enc(map, type, 2, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return LORA_OK;
+    g_last_cuda_error = 10000 + (int)r;
+    return LORA_ECUDA;
+}
+
+template <int NMAX>
+lora_status launch_wide(W8WideParams& w, cudaStream_t s) {
+    DeviceInfo* di = nullptr;
+    lora_status st = device_info(&di);
+    if (st != LORA_OK) return st;
+    auto kern = w8_wide_kernel<NMAX>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kW8WideThreads);
+    cfg.dynamicSmemBytes = w8_wide_smem(NMAX);
+    static thread_local const DeviceInfo* ready = nullptr;
+    static thread_local int pairs = 0;
+    if (ready != di) {
+        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes));
+        if (st != LORA_OK) return st;
+        cudaLaunchAttribute pair;
+        pair.id = cudaLaunchAttributeClusterDimension;
+        pair.val.clusterDim.x = 2;
+        pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(di->sm_count / 2 * 2);
+        cfg.attrs = &pair;
+        cfg.numAttrs = 1;
+        st = cuda_status(cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg));
+        if (st != LORA_OK) return st;
+        pairs = std::max(1, std::min(pairs, kW8MaxPairs));
+        ready = di;
+    }
+    // equal shares of all steps, or whole tiles where the largest share of them is not much more
+    // (which needs one K for all projections)
+    int32_t per = (w.total + pairs - 1) / pairs;
+    const int32_t kb = w.prob[0].kblocks;
+    bool one_k = true;
+    for (int32_t i = 1; i < w.nprob; ++i) one_k = one_k && w.prob[i].kblocks == kb;
+    const int32_t whole = (w.total / kb + pairs - 1) / pairs * kb;
+    if (one_k && whole <= per + kW8JoinCost) per = whole;
+    w.per = per;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    cfg.stream = s;
+    cfg.gridDim = dim3(2 * std::min(pairs, (w.total + per - 1) / per));
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, w));
+}
+
+lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, cudaStream_t s) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    lora_status st = encode_fn(&enc);
+    if (st != LORA_OK) return st;
+    static thread_local W8WideParams w;
+    static thread_local W8Widen v;
+    memset(&w, 0, sizeof w);
+    memset(&v, 0, sizeof v);
+    const WideShape sh = wide_shape(T);
+    char* base = reinterpret_cast<char*>(ws);
+    w.nprob = nprob;
+    w.T = v.T = T;
+    w.cols = sh.cols;
+    w.ttiles = sh.ttiles;
+    w.tickets = reinterpret_cast<uint32_t*>(base + sizeof(WsHeader));
+    w.part = reinterpret_cast<float*>(base + align256(kStepPartAt));
+    w.err = &reinterpret_cast<WsHeader*>(ws)->err;
+    w.limit_ns = kWaitLimitNs;
+    char* at = base + align256(kStepPartAt) + w8_part_bytes(sh.nmax);
+    int32_t copies = 0, slot[LORA_W8_MAX_PROBLEMS];
+    int64_t total = 0, most = 0;
+    for (int32_t i = 0; i < nprob; ++i) {
+        const lora_w8_problem& pr = probs[i];
+        const int32_t j = x_of(probs, i);
+        if (j == i) {
+            v.x[copies] = reinterpret_cast<const unsigned char*>(pr.x);
+            v.out[copies] = reinterpret_cast<uint32_t*>(at);
+            v.ldx[copies] = pr.ldx;
+            v.K[copies] = pr.K;
+            most = std::max(most, (int64_t)T * (pr.K / 16));
+            st = map2d(enc, &w.x[copies], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, at, pr.K, T, (uint64_t)pr.K * 2, 64, sh.cols / 2,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+            if (st != LORA_OK) return st;
+            at += x_bytes(pr, T);
+            slot[i] = copies++;
+        } else {
+            slot[i] = slot[j];
+        }
+        st = map2d(enc, &w.w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.w, pr.K, pr.N, pr.K, kW8WideK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st != LORA_OK) return st;
+        st = map2d(enc, &w.y[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.y, pr.N, T, (uint64_t)pr.ldy * 2, 128, kW8StageCols,
+                   CU_TENSOR_MAP_SWIZZLE_NONE);
+        if (st != LORA_OK) return st;
+        w.prob[i] = {pr.x_scales, pr.w_scales, pr.N, (pr.K + kW8WideK - 1) / kW8WideK, (int32_t)total, slot[i]};
+        total += (int64_t)((pr.N + kW8WideRows - 1) / kW8WideRows) * sh.ttiles * w.prob[i].kblocks;
+        if (total > INT32_MAX) return LORA_ETOOBIG;
+    }
+    w.total = (int32_t)total;
+    const int64_t blocks = std::min<int64_t>((most + kWidenThreads - 1) / kWidenThreads, 2048);
+    w8_widen_kernel<<<dim3((unsigned)blocks, (unsigned)copies), kWidenThreads, 0, s>>>(v);
+    st = cuda_status(cudaGetLastError());
+    if (st != LORA_OK) return st;
+    if (sh.nmax == 64) return launch_wide<64>(w, s);
+    return sh.nmax == 128 ? launch_wide<128>(w, s) : launch_wide<256>(w, s);
 }
 
 }  // namespace
@@ -146,25 +311,8 @@ lora_status lora_w8_matmul(const lora_w8_problem* probs, int32_t nprob, int32_t 
     }
     if (nprob == 0 || T == 0) return LORA_OK;
     if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes(probs, nprob, T)) return LORA_EWORKSPACE;
-    static thread_local W8Params p;
-    memset(&p, 0, sizeof p);
-    p.T = T;
-    p.nprob = nprob;
-    int64_t total = 0;
-    for (int32_t i = 0; i < nprob; ++i) {
-        const lora_w8_problem& pr = probs[i];
-        p.prob[i] = {reinterpret_cast<const unsigned char*>(pr.x), pr.x_scales, reinterpret_cast<__nv_bfloat16*>(pr.y),
-                     reinterpret_cast<const unsigned char*>(pr.w), pr.w_scales, pr.ldx, pr.ldy, pr.N, pr.K, (int32_t)total};
-        total += (pr.N + kW8Rows - 1) / kW8Rows;
-    }
-    p.total = (int32_t)total;
     cudaStream_t s = (cudaStream_t)stream;
-    const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
-    const dim3 grid((unsigned)total, (unsigned)((T + 8 * nt - 1) / (8 * nt)));
-    if (nt == 1) w8_narrow_kernel<1><<<grid, kW8Threads, 0, s>>>(p);
-    else if (nt == 2) w8_narrow_kernel<2><<<grid, kW8Threads, 0, s>>>(p);
-    else w8_narrow_kernel<4><<<grid, kW8Threads, 0, s>>>(p);
-    return cuda_status(cudaGetLastError());
+    return T <= kW8NarrowRows ? run_narrow(probs, nprob, T, s) : run_wide(probs, nprob, T, ws, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,432 @@
+// y = x W^T of 8-bit integers with a scale per row of x and per row of W, for many rows of x.
+//
+// The sums of w8_narrow.cuh on the fifth-generation tensor cores: codes as f16, where they are
+// exact, and their products summed in fp32, which holds whole numbers up to 2^24 exactly (sums
+// past that are rounded as fp32 sums are).
+//
+// Two CTAs of a cluster make one tile of 256 rows of W by up to 256 rows of x: each holds its
+// 128 rows of W, widened into its tensor memory as the A operand, and half of the rows of x in
+// shared memory, where one TMA load serves both SMs' products.  x comes in f16 from the
+// workspace, where w8_widen_kernel puts it once a call; W, the long side, is widened on the
+// way, so that memory sees one byte a weight.
+//
+// Warp 0 streams W (128 rows x 128 of K a CTA and step) and warp 2 x by TMA, warps 4 to 11
+// widen W into tensor memory, warp 1 of the even CTA issues the MMAs of both, warps 12 to 19
+// take the sums out.  The pairs take equal contiguous ranges of the steps of all tiles, or
+// whole tiles; a tile shared by several pairs is joined over partial sums in the workspace by
+// the one that arrives last, in the order of K.
+#pragma once
+#include <cuda.h>
+
+#include "w8_narrow.cuh"
+
+namespace lora {
+
+constexpr int kW8WideRows = 256;               // rows of W of a tile: 128 a CTA
+constexpr int kW8WideK = 128;                  // K of a step
+constexpr int kW8WideThreads = 640;
+constexpr int kW8MaxPairs = 96;
+constexpr int kW8Bufs = 4;                     // A buffers in tensor memory and stages of x
+constexpr int kW8WBytes = 128 * kW8WideK;
+constexpr int kW8StageCols = 16;               // columns of y that leave together
+constexpr int kW8StageBytes = kW8StageCols * 128 * 2;
+
+// By the most columns (rows of x) of a tile: stages of W, as many as fit beside x.
+__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 4 : n > 64 ? 8 : 10; }
+__host__ __device__ constexpr size_t w8_wide_smem(int n) {
+    return 1024 + (size_t)w8_w_stages(n) * kW8WBytes + (size_t)kW8Bufs * n * 128 + 4 * kW8StageBytes;
+}
+// Partial sums of a CTA: two tiles' of 128 rows.
+__host__ __device__ constexpr size_t w8_part_floats(int n) { return (size_t)128 * n; }
+__host__ __device__ constexpr size_t w8_part_bytes(int n) { return (size_t)kW8MaxPairs * 2 * 2 * w8_part_floats(n) * 4; }
+
+struct W8WideProb {
+    const float* x_scales;
+    const float* w_scales;
+    int32_t N;
+    int32_t kblocks;
+    int32_t first;                             // steps before the projection
+    int32_t xi;                                // its map of x
+};
+
+struct W8WideParams {
+    CUtensorMap w[LORA_W8_MAX_PROBLEMS];       // bytes {K, N}, box {128, 128}, 128-byte swizzle
+    CUtensorMap x[LORA_W8_MAX_PROBLEMS];       // f16 {K, T}, box {64, cols / 2}, 128-byte swizzle
+    CUtensorMap y[LORA_W8_MAX_PROBLEMS];       // bf16 {N, T}, box {128, 16}
+    W8WideProb prob[LORA_W8_MAX_PROBLEMS];
+    int32_t nprob;
+    int32_t T;
+    int32_t cols;                              // rows of x of a tile, a multiple of 32
+    int32_t ttiles;                            // tiles along x
+    int32_t total;                             // steps
+    int32_t per;                               // steps of a pair
+    uint32_t* tickets;                         // [kStepTickets], zero between calls
+    float* part;
+    uint32_t* err;
+    uint64_t limit_ns;
+};
+
+// ---------------------------------------------------------------------------- x in f16
+struct W8Widen {
+    const unsigned char* x[LORA_W8_MAX_PROBLEMS];
+    uint32_t* out[LORA_W8_MAX_PROBLEMS];       // f16 [T][K]
+    int64_t ldx[LORA_W8_MAX_PROBLEMS];
+    int32_t K[LORA_W8_MAX_PROBLEMS];
+    int32_t T;
+};
+constexpr int kWidenThreads = 256;
+
+// Sixteen codes a thread; blockIdx.y: the matrix.
+__global__ void __launch_bounds__(kWidenThreads) w8_widen_kernel(const __grid_constant__ W8Widen p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int i = blockIdx.y, K = p.K[i];
+    const int64_t n = (int64_t)p.T * (K / 16);
+    for (int64_t e = (int64_t)blockIdx.x * kWidenThreads + threadIdx.x; e < n; e += (int64_t)gridDim.x * kWidenThreads) {
+        const int64_t row = e / (K / 16), c = e - row * (K / 16);
+        const uint4 v = ld16(p.x[i] + row * p.ldx[i] + c * 16);
+        uint4 a, b;
+        codes8_f16(v.x, a.x, a.y);
+        codes8_f16(v.y, a.z, a.w);
+        codes8_f16(v.z, b.x, b.y);
+        codes8_f16(v.w, b.z, b.w);
+        uint32_t* to = p.out[i] + (row * K + c * 16) / 2;
+        st16(to, a);
+        st16(to + 4, b);
+    }
+}
+
+// ---------------------------------------------------------------------------- pairs of CTAs
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The address of `addr` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// mbar_wait_quiet for a barrier that the other CTA arrives at too.
+__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t t = global_timer_ns();
+        if (t0 == 0) t0 = t;
+        else if (t - t0 > limit_ns) return false;
+    }
+}
+// A 2-D TMA load into this CTA whose bytes count on the even CTA's barrier.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// D[tmem of both] (+)= A[tmem of both] x B[half in each CTA's shared memory], f16.
+__device__ __forceinline__ void tc_mma_pair(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive once on the barrier at `bar` of both CTAs when this thread's MMAs so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// A step: projection, tiles along W and along x, block of K.
+struct W8At {
+    int prob, rt, tt, kb;
+};
+__device__ __forceinline__ W8At w8_at(const W8WideParams& p, int u) {
+    W8At a;
+    a.prob = 0;
+    while (a.prob + 1 < p.nprob && u >= p.prob[a.prob + 1].first) ++a.prob;
+    const int b = u - p.prob[a.prob].first, tile = b / p.prob[a.prob].kblocks;
+    a.kb = b - tile * p.prob[a.prob].kblocks;
+    a.rt = tile / p.ttiles;
+    a.tt = tile - a.rt * p.ttiles;
+    return a;
+}
+__device__ __forceinline__ void w8_next(const W8WideParams& p, W8At& a) {
+    if (++a.kb < p.prob[a.prob].kblocks) return;
+    a.kb = 0;
+    if (++a.tt < p.ttiles) return;
+    a.tt = 0;
+    if (++a.rt * kW8WideRows < p.prob[a.prob].N) return;
+    a.rt = 0;
+    ++a.prob;
+}
+
+// NMAX: the most columns of a tile.
+template <int NMAX>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w8_wide_kernel(const __grid_constant__ W8WideParams p) {
+    constexpr int kWStages = w8_w_stages(NMAX), kXStage = NMAX * 128;
+    constexpr uint32_t kACol = 256;            // D in columns 0 .. 255, four A buffers of 64 columns after it
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full, d_empty, final_bar;
+    __shared__ float sx[2][128];
+    __shared__ uint32_t tmem_slot, last_in[2], lost[2];
+    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t w0 = smem_addr(base), x0 = w0 + kWStages * kW8WBytes, y0 = x0 + kW8Bufs * kXStage;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cta_rank();
+    const int pair = blockIdx.x >> 1;
+    const int first = min(pair * p.per, p.total), end = min(first + p.per, p.total);
+    const int half_cols = p.cols / 2;
+    auto bar = [](uint64_t& b) { return smem_addr(&b); };
+    if (tid == 0) {
+        for (int i = 0; i < kWStages; ++i) {
+            mbar_init(bar(w_full[i]), 1);
+            mbar_init(bar(w_empty[i]), 8);
+        }
+        for (int i = 0; i < kW8Bufs; ++i) {
+            mbar_init(bar(ready[i]), 1 + 16);          // of the even CTA: x's bytes in both, and both CTAs' widening warps
+            mbar_init(bar(freed[i]), 1);
+        }
+        mbar_init(bar(d_full), 1);
+        mbar_init(bar(d_empty), 16);
+        mbar_init(bar(final_bar), 1);
+        lost[0] = lost[1] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
+    bool ok = true;
+    auto wait = [&](uint64_t& which, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, mbar_wait_pair(bar(which), parity, p.limit_ns));
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ W, one thread
+        if (lane == 0) {
+            W8At a = w8_at(p, first);
+            uint32_t i = 0;
+            for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
+                const uint32_t s = i % kWStages;
+                if (!mbar_wait_quiet(bar(w_empty[s]), ((i / kWStages) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
+                mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);
+                tma_load_2d(w0 + s * kW8WBytes, &p.w[a.prob], a.kb * kW8WideK, a.rt * kW8WideRows + (int)rank * 128, bar(w_full[s]));
+            }
+            if (!ok) set_error(p.err, LORA_DERR_TIMEOUT);
+            // every copy has landed before the CTA can end
+            for (uint32_t k = i > kWStages ? i - kWStages : 0; k < i; ++k)
+                mbar_wait_quiet(bar(w_full[k % kWStages]), (k / kWStages) & 1, 100000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------------------------ x, one thread
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            W8At a = w8_at(p, first);
+            uint32_t i = 0;
+            const uint32_t box = half_cols * 128;
+            for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
+                const uint32_t b = i % kW8Bufs;
+                if (!mbar_wait_pair(bar(freed[b]), ((i / kW8Bufs) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
+                const uint32_t at = mapa(bar(ready[b]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(bar(ready[b]), 4 * box);
+                const CUtensorMap* map = &p.x[p.prob[a.prob].xi];
+                const int row = a.tt * p.cols + (int)rank * half_cols;
+                tma_load_2d_pair(x0 + b * kXStage, map, a.kb * kW8WideK, row, at);
+                tma_load_2d_pair(x0 + b * kXStage + box, map, a.kb * kW8WideK + 64, row, at);
+            }
+            if (!ok) {
+                // the copies count on the even CTA's barriers: those in flight land long before this
+                set_error(p.err, LORA_DERR_TIMEOUT);
+                for (const uint64_t t = global_timer_ns(); global_timer_ns() - t < 10000000ull;) {}
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issue, the even CTA's
+        if (rank == 0) {
+            const uint32_t idesc = (1u << 4) | ((uint32_t)(p.cols >> 3) << 17) | ((256u >> 4) << 24);   // f16, fp32 sums
+            const uint64_t x_desc = smem_desc(x0, 16, 1024, 2);
+            const uint32_t box = half_cols * 128;
+            W8At a = w8_at(p, first);
+            uint32_t i = 0, tiles = 0;
+            bool fresh = true;
+            for (int u = first; u < end && ok; ++u, ++i) {
+                const uint32_t b = i % kW8Bufs;
+                const bool last = a.kb + 1 == p.prob[a.prob].kblocks || u + 1 == end;
+                w8_next(p, a);
+                if (fresh && !wait(d_empty, (tiles & 1) ^ 1)) { ok = false; break; }
+                if (!wait(ready[b], (i / kW8Bufs) & 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint64_t db = desc_at(x_desc, b * kXStage);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kW8WideK / 16; ++k)
+                        tc_mma_pair(tmem, tmem + kACol + b * 64 + k * 8, desc_at(db, (k / 4) * box + (k % 4) * 32), idesc,
+                                    !(fresh && k == 0));
+                    tc_commit_pair(bar(freed[b]));
+                    if (last) tc_commit_pair(bar(d_full));
+                }
+                __syncwarp();
+                fresh = last;
+                tiles += last;
+            }
+            if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
+            if (elect_one()) tc_commit_pair(bar(final_bar));
+            __syncwarp();
+        }
+        mbar_wait_pair(bar(final_bar), 0, 4 * p.limit_ns);   // the MMAs are done before tensor memory is given back
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        // ------------------------------------------------------------------ widening: a row of W, half of a step's K
+        const int quad = warp & 3, turn = (warp - 4) >> 2, r = quad * 32 + lane;
+        const uint32_t acol = tmem + ((uint32_t)(quad * 32) << 16) + kACol + turn * 32;
+        uint32_t i = 0;
+        for (int u = first; u < end; ++u, ++i) {
+            const uint32_t s = i % kWStages, b = i % kW8Bufs;
+            if (!wait(w_full[s], (i / kWStages) & 1)) { ok = false; break; }
+            uint32_t out[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 v = lds128(w0 + s * kW8WBytes + r * 128 + (((turn * 4 + c) ^ (r & 7)) << 4));
+                codes8_f16(v.x, out[c * 8], out[c * 8 + 1]);
+                codes8_f16(v.y, out[c * 8 + 2], out[c * 8 + 3]);
+                codes8_f16(v.z, out[c * 8 + 4], out[c * 8 + 5]);
+                codes8_f16(v.w, out[c * 8 + 6], out[c * 8 + 7]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(w_empty[s]));
+            if (!wait(freed[b], ((i / kW8Bufs) & 1) ^ 1)) { ok = false; break; }
+            tc_fence_after();
+            tmem_st32(acol + b * 64, out);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(mapa(bar(ready[b]), 0));
+        }
+        if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
+    } else if (warp >= 12) {
+        // ------------------------------------------------------------------ sums out: a row of W, half of the columns
+        const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
+        const uint32_t dcol = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
+        const uint32_t stage = y0 + half * 2 * kW8StageBytes;
+        const int chunks = half_cols / kW8StageCols;
+        auto meet = [&]() { named_bar_sync(1 + half, 128); };
+        W8At a = w8_at(p, first);
+        uint32_t tiles = 0, stores = 0;
+        for (int at = first; at < end; ++tiles) {
+            const W8WideProb& pr = p.prob[a.prob];
+            const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = min(tile_end, end);
+            const int row0 = a.rt * kW8WideRows + (int)rank * 128, col0 = a.tt * p.cols + half * half_cols;
+            const bool whole = at == tile_first && stop == tile_end;
+            const float sw = row0 + r < pr.N ? pr.w_scales[row0 + r] : 0.f;
+            meet();                                            // the last tile's scales have been read
+            sx[half][g] = col0 + g < p.T && g < half_cols ? pr.x_scales[col0 + g] : 0.f;
+            // after a wait that ran out the four warps take no more sums, as one, but still count
+            // their parts of the range's tiles (with the error set), so that the tickets end as they began
+            if (ok && !wait(d_full, tiles & 1)) lost[half] = 1;
+            meet();
+            ok = *reinterpret_cast<volatile uint32_t*>(&lost[half]) == 0;
+            // 16 columns of y, [column][row of W], through shared memory and one bulk store (what
+            // lies outside y is not written)
+            auto store = [&](int c, const float (&v)[16]) {
+                const uint32_t buf = stage + (stores & 1) * kW8StageBytes;
+                if (g == 0) bulk_wait_read1();                 // the last store but one has left its buffer
+                meet();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + (j * 128 + r) * 2),
+                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v[j] * sx[half][c * 16 + j] * sw))) : "memory");
+                fence_proxy_async_smem();
+                meet();
+                if (g == 0) {
+                    if (row0 < pr.N && col0 + c * 16 < p.T) tma_store_2d(&p.y[a.prob], row0, col0 + c * 16, buf);
+                    bulk_commit();
+                }
+                ++stores;
+            };
+            // a part lies [column / 4][row][4]
+            auto part_of = [&](int64_t cta, int slot) {
+                return reinterpret_cast<float4*>(p.part + (cta * 2 + slot) * (int64_t)w8_part_floats(NMAX) + (int64_t)half * half_cols * 128) + r;
+            };
+            float4* part = part_of(blockIdx.x, tile_first < first ? 0 : 1);
+            tc_fence_after();
+            for (int c = 0; c < chunks && ok; ++c) {
+                float v[16];
+                tmem_ld16(dcol + c * 16, v);
+                tmem_ld_wait();
+                if (whole) {
+                    store(c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
+            if (!whole) {
+                const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per;
+                uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
+                __threadfence();
+                meet();
+                if (g == 0) last_in[half] = atomicAdd(ticket, 1u) == (uint32_t)(p1 - p0);
+                meet();
+                if (*reinterpret_cast<volatile uint32_t*>(&last_in[half])) {
+                    __threadfence();
+                    if (g == 0) *ticket = 0;
+                    for (int c = 0; c < chunks; ++c) {
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                        for (int q = p0; q <= p1; ++q) {
+                            const float4* from = part_of((int64_t)q * 2 + rank, tile_first < q * p.per ? 0 : 1);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float4 x = __ldcg(from + (c * 4 + j) * 128);
+                                v[4 * j] += x.x;
+                                v[4 * j + 1] += x.y;
+                                v[4 * j + 2] += x.z;
+                                v[4 * j + 3] += x.w;
+                            }
+                        }
+                        store(c, v);
+                    }
+                }
+                meet();
+            }
+            at = stop;
+            if (at < end) a = w8_at(p, at);
+        }
+        if (g == 0) bulk_wait0();
+        if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 3) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+}  // namespace lora
