@@ -107,29 +107,14 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+// Arrives on a barrier of either CTA.  What it announces is tensor memory, which tcgen05.wait and
+// tcgen05.fence order, so the release is that of a CTA: one of cluster scope drains every memory
+// access of the thread first (about 800 clocks a step, two thirds of the kernel's time).
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// mbar_wait_quiet for a barrier that the other CTA arrives at too.
-__device__ __forceinline__ bool mbar_wait_pair(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity), "r"(1000000u)
-            : "memory");
-        if (ok) return true;
-        const uint64_t t = global_timer_ns();
-        if (t0 == 0) t0 = t;
-        else if (t - t0 > limit_ns) return false;
-    }
 }
 // A 2-D TMA load into this CTA whose bytes count on the even CTA's barrier.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, uint32_t bar) {
@@ -153,6 +138,19 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
                  "h"((uint16_t)3)
                  : "memory");
 }
+
+// Waits for the loads of tensor memory into v.
+__device__ __forceinline__ void tmem_ld_wait16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                   "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
 // A step: projection, tiles along W and along x, block of K.
 struct W8At {
@@ -185,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     constexpr uint32_t kACol = 256;            // D in columns 0 .. 255, four A buffers of 64 columns after it
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full, d_empty, final_bar;
-    __shared__ float sx[2][128];
+    __shared__ __align__(16) float sx[2][128];
     __shared__ uint32_t tmem_slot, last_in[2], lost[2];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const uint32_t w0 = smem_addr(base), x0 = w0 + kWStages * kW8WBytes, y0 = x0 + kW8Bufs * kXStage;
@@ -220,11 +218,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
     bool ok = true;
     auto wait = [&](uint64_t& which, uint32_t parity) {
-        return (bool)__all_sync(0xffffffffu, mbar_wait_pair(bar(which), parity, p.limit_ns));
+        return (bool)__all_sync(0xffffffffu, mbar_wait_quiet(bar(which), parity, p.limit_ns));
     };
 
+    // Registers from the warps that issue and widen to those that hold a row's sums: 56, twice 72
+    // and twice 136 a thread of the five groups of four warps, 472 of the 480 of the launch.
     if (warp == 0) {
         // ------------------------------------------------------------------ W, one thread
+        regs_dec<56>();
         if (lane == 0) {
             W8At a = w8_at(p, first);
             uint32_t i = 0;
@@ -242,6 +243,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------------ x, one thread
+        regs_dec<56>();
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             W8At a = w8_at(p, first);
@@ -249,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             const uint32_t box = half_cols * 128;
             for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
                 const uint32_t b = i % kW8Bufs;
-                if (!mbar_wait_pair(bar(freed[b]), ((i / kW8Bufs) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
+                if (!mbar_wait_quiet(bar(freed[b]), ((i / kW8Bufs) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
                 const uint32_t at = mapa(bar(ready[b]), 0);
                 if (rank == 0) mbar_arrive_expect_tx(bar(ready[b]), 4 * box);
                 const CUtensorMap* map = &p.x[p.prob[a.prob].xi];
@@ -266,6 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issue, the even CTA's
+        regs_dec<56>();
         if (rank == 0) {
             const uint32_t idesc = (1u << 4) | ((uint32_t)(p.cols >> 3) << 17) | ((256u >> 4) << 24);   // f16, fp32 sums
             const uint64_t x_desc = smem_desc(x0, 16, 1024, 2);
@@ -297,10 +300,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             if (elect_one()) tc_commit_pair(bar(final_bar));
             __syncwarp();
         }
-        mbar_wait_pair(bar(final_bar), 0, 4 * p.limit_ns);   // the MMAs are done before tensor memory is given back
+        mbar_wait_quiet(bar(final_bar), 0, 4 * p.limit_ns);   // the MMAs are done before tensor memory is given back
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------------ widening: a row of W, half of a step's K
+        regs_dec<72>();
         const int quad = warp & 3, turn = (warp - 4) >> 2, r = quad * 32 + lane;
         const uint32_t acol = tmem + ((uint32_t)(quad * 32) << 16) + kACol + turn * 32;
         uint32_t i = 0;
@@ -329,6 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
     } else if (warp >= 12) {
         // ------------------------------------------------------------------ sums out: a row of W, half of the columns
+        regs_inc<136>();
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
         const uint32_t dcol = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
         const uint32_t stage = y0 + half * 2 * kW8StageBytes;
@@ -349,16 +354,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             if (ok && !wait(d_full, tiles & 1)) lost[half] = 1;
             meet();
             ok = *reinterpret_cast<volatile uint32_t*>(&lost[half]) == 0;
+            // 16 columns' sums as bf16 pairs of y
+            auto scale = [&](int c, const float (&v)[16], uint32_t* to) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sx[half][c * 16 + 4 * j]);
+                    to[2 * j] = pack2(v[4 * j] * f.x * sw, v[4 * j + 1] * f.y * sw);
+                    to[2 * j + 1] = pack2(v[4 * j + 2] * f.z * sw, v[4 * j + 3] * f.w * sw);
+                }
+            };
             // 16 columns of y, [column][row of W], through shared memory and one bulk store (what
             // lies outside y is not written)
-            auto store = [&](int c, const float (&v)[16]) {
+            auto store = [&](int c, const uint32_t* from) {
                 const uint32_t buf = stage + (stores & 1) * kW8StageBytes;
                 if (g == 0) bulk_wait_read1();                 // the last store but one has left its buffer
                 meet();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + (j * 128 + r) * 2),
-                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v[j] * sx[half][c * 16 + j] * sw))) : "memory");
+                                 "h"((uint16_t)(j & 1 ? from[j / 2] >> 16 : from[j / 2])) : "memory");
                 fence_proxy_async_smem();
                 meet();
                 if (g == 0) {
@@ -373,20 +387,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             };
             float4* part = part_of(blockIdx.x, tile_first < first ? 0 : 1);
             tc_fence_after();
-            for (int c = 0; c < chunks && ok; ++c) {
-                float v[16];
-                tmem_ld16(dcol + c * 16, v);
-                tmem_ld_wait();
-                if (whole) {
-                    store(c, v);
-                } else {
+            // a whole tile's sums become y in registers, a part goes out as it is: either way the
+            // MMAs of the next tile wait for no store
+            uint32_t out[NMAX / 4];
+            float v[2][16];
+            if (ok) {
+                tmem_ld16(dcol, v[0]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                for (int c = 0; c < NMAX / 32; ++c) {
+                    if (c < chunks) {
+                        tmem_ld_wait16(v[c & 1]);
+                        if (c + 1 < chunks) tmem_ld16(dcol + (c + 1) * 16, v[(c + 1) & 1]);
+                        const float(&f)[16] = v[c & 1];
+                        if (whole) {
+                            scale(c, f, out + c * 8);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        }
+                    }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
+            if (whole && ok) {
+#pragma unroll
+                for (int c = 0; c < NMAX / 32; ++c)
+                    if (c < chunks) store(c, out + c * 8);
+            }
             if (!whole) {
                 const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per;
                 uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
@@ -398,21 +427,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                     __threadfence();
                     if (g == 0) *ticket = 0;
                     for (int c = 0; c < chunks; ++c) {
-                        float v[16];
+                        float sum[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+                        for (int j = 0; j < 16; ++j) sum[j] = 0.f;
                         for (int q = p0; q <= p1; ++q) {
                             const float4* from = part_of((int64_t)q * 2 + rank, tile_first < q * p.per ? 0 : 1);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const float4 x = __ldcg(from + (c * 4 + j) * 128);
-                                v[4 * j] += x.x;
-                                v[4 * j + 1] += x.y;
-                                v[4 * j + 2] += x.z;
-                                v[4 * j + 3] += x.w;
+                                sum[4 * j] += x.x;
+                                sum[4 * j + 1] += x.y;
+                                sum[4 * j + 2] += x.z;
+                                sum[4 * j + 3] += x.w;
                             }
                         }
-                        store(c, v);
+                        scale(c, sum, out);
+                        store(c, out);
                     }
                 }
                 meet();
@@ -422,6 +452,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         }
         if (g == 0) bulk_wait0();
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
+    } else {
+        regs_dec<56>();
     }
     tc_fence_before();
     cluster_sync();
