@@ -223,10 +223,7 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
         }
         st = map2d(enc, &w.w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, pr.w, pr.K, pr.N, pr.K, kW8WideK, 128, CU_TENSOR_MAP_SWIZZLE_128B);
         if (st != LORA_OK) return st;
-        st = map2d(enc, &w.y[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, pr.y, pr.N, T, (uint64_t)pr.ldy * 2, 128, kW8StageCols,
-                   CU_TENSOR_MAP_SWIZZLE_NONE);
-        if (st != LORA_OK) return st;
-        w.prob[i] = {pr.x_scales, pr.w_scales, pr.N, (pr.K + kW8WideK - 1) / kW8WideK, (int32_t)total, slot[i]};
+        w.prob[i] = {pr.x_scales, pr.w_scales, reinterpret_cast<__nv_bfloat16*>(pr.y), pr.ldy, pr.N, (pr.K + kW8WideK - 1) / kW8WideK, (int32_t)total, slot[i]};
         total += (int64_t)((pr.N + kW8WideRows - 1) / kW8WideRows) * sh.ttiles * w.prob[i].kblocks;
         if (total > INT32_MAX) return LORA_ETOOBIG;
     }

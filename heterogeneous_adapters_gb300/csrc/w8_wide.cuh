@@ -28,13 +28,11 @@ constexpr int kW8WideThreads = 640;
 constexpr int kW8MaxPairs = 96;
 constexpr int kW8Bufs = 4;                     // A buffers in tensor memory and stages of x
 constexpr int kW8WBytes = 128 * kW8WideK;
-constexpr int kW8StageCols = 16;               // columns of y that leave together
-constexpr int kW8StageBytes = kW8StageCols * 128 * 2;
 
 // By the most columns (rows of x) of a tile: stages of W, as many as fit beside x.
-__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 4 : n > 64 ? 8 : 10; }
+__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 5 : n > 64 ? 9 : 11; }
 __host__ __device__ constexpr size_t w8_wide_smem(int n) {
-    return 1024 + (size_t)w8_w_stages(n) * kW8WBytes + (size_t)kW8Bufs * n * 128 + 4 * kW8StageBytes;
+    return 1024 + (size_t)w8_w_stages(n) * kW8WBytes + (size_t)kW8Bufs * n * 128;
 }
 // Partial sums of a CTA: two tiles' of 128 rows.
 __host__ __device__ constexpr size_t w8_part_floats(int n) { return (size_t)128 * n; }
@@ -43,6 +41,8 @@ __host__ __device__ constexpr size_t w8_part_bytes(int n) { return (size_t)kW8Ma
 struct W8WideProb {
     const float* x_scales;
     const float* w_scales;
+    __nv_bfloat16* y;
+    int64_t ldy;
     int32_t N;
     int32_t kblocks;
     int32_t first;                             // steps before the projection
@@ -52,7 +52,6 @@ struct W8WideProb {
 struct W8WideParams {
     CUtensorMap w[LORA_W8_MAX_PROBLEMS];       // bytes {K, N}, box {128, 128}, 128-byte swizzle
     CUtensorMap x[LORA_W8_MAX_PROBLEMS];       // f16 {K, T}, box {64, cols / 2}, 128-byte swizzle
-    CUtensorMap y[LORA_W8_MAX_PROBLEMS];       // bf16 {N, T}, box {128, 16}
     W8WideProb prob[LORA_W8_MAX_PROBLEMS];
     int32_t nprob;
     int32_t T;
@@ -186,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     __shared__ __align__(16) float sx[2][128];
     __shared__ uint32_t tmem_slot, last_in[2], lost[2];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t w0 = smem_addr(base), x0 = w0 + kWStages * kW8WBytes, y0 = x0 + kW8Bufs * kXStage;
+    const uint32_t w0 = smem_addr(base), x0 = w0 + kWStages * kW8WBytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     const int pair = blockIdx.x >> 1;
@@ -196,10 +195,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     if (tid == 0) {
         for (int i = 0; i < kWStages; ++i) {
             mbar_init(bar(w_full[i]), 1);
-            mbar_init(bar(w_empty[i]), 8);
+            mbar_init(bar(w_empty[i]), 4);
         }
         for (int i = 0; i < kW8Bufs; ++i) {
-            mbar_init(bar(ready[i]), 1 + 16);          // of the even CTA: x's bytes in both, and both CTAs' widening warps
+            mbar_init(bar(ready[i]), 1 + 8);           // of the even CTA: x's bytes in both, and both CTAs' four widening warps
             mbar_init(bar(freed[i]), 1);
         }
         mbar_init(bar(d_full), 1);
@@ -225,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     // and twice 136 a thread of the five groups of four warps, 472 of the 480 of the launch.
     if (warp == 0) {
         // ------------------------------------------------------------------ W, one thread
-        regs_dec<56>();
+        regs_dec<48>();
         if (lane == 0) {
             W8At a = w8_at(p, first);
             uint32_t i = 0;
@@ -243,7 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------------ x, one thread
-        regs_dec<56>();
+        regs_dec<48>();
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             W8At a = w8_at(p, first);
@@ -268,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issue, the even CTA's
-        regs_dec<56>();
+        regs_dec<48>();
         if (rank == 0) {
             const uint32_t idesc = (1u << 4) | ((uint32_t)(p.cols >> 3) << 17) | ((256u >> 4) << 24);   // f16, fp32 sums
             const uint64_t x_desc = smem_desc(x0, 16, 1024, 2);
@@ -303,44 +302,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         mbar_wait_quiet(bar(final_bar), 0, 4 * p.limit_ns);   // the MMAs are done before tensor memory is given back
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
-        // ------------------------------------------------------------------ widening: a row of W, half of a step's K
+        // ------------------------------------------------------------------ widening: a row of W, every other step
         regs_dec<72>();
-        const int quad = warp & 3, turn = (warp - 4) >> 2, r = quad * 32 + lane;
-        const uint32_t acol = tmem + ((uint32_t)(quad * 32) << 16) + kACol + turn * 32;
-        uint32_t i = 0;
-        for (int u = first; u < end; ++u, ++i) {
+        const int quad = warp & 3, r = quad * 32 + lane;
+        const uint32_t acol = tmem + ((uint32_t)(quad * 32) << 16) + kACol;
+        uint32_t i = (warp - 4) >> 2;
+        for (int u = first + (int)i; u < end; u += 2, i += 2) {
             const uint32_t s = i % kWStages, b = i % kW8Bufs;
             if (!wait(w_full[s], (i / kWStages) & 1)) { ok = false; break; }
-            uint32_t out[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 v = lds128(w0 + s * kW8WBytes + r * 128 + (((turn * 4 + c) ^ (r & 7)) << 4));
-                codes8_f16(v.x, out[c * 8], out[c * 8 + 1]);
-                codes8_f16(v.y, out[c * 8 + 2], out[c * 8 + 3]);
-                codes8_f16(v.z, out[c * 8 + 4], out[c * 8 + 5]);
-                codes8_f16(v.w, out[c * 8 + 6], out[c * 8 + 7]);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t out[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = lds128(w0 + s * kW8WBytes + r * 128 + (((h * 4 + c) ^ (r & 7)) << 4));
+                    codes8_f16(v.x, out[c * 8], out[c * 8 + 1]);
+                    codes8_f16(v.y, out[c * 8 + 2], out[c * 8 + 3]);
+                    codes8_f16(v.z, out[c * 8 + 4], out[c * 8 + 5]);
+                    codes8_f16(v.w, out[c * 8 + 6], out[c * 8 + 7]);
+                }
+                if (h == 0) {
+                    if (!wait(freed[b], ((i / kW8Bufs) & 1) ^ 1)) { ok = false; break; }
+                    tc_fence_after();
+                }
+                tmem_st32(acol + b * 64 + h * 32, out);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(w_empty[s]));
-            if (!wait(freed[b], ((i / kW8Bufs) & 1) ^ 1)) { ok = false; break; }
-            tc_fence_after();
-            tmem_st32(acol + b * 64, out);
+            if (!ok) break;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(mapa(bar(ready[b]), 0));
+            if (lane == 0) {
+                mbar_arrive(bar(w_empty[s]));
+                mbar_arrive_at(mapa(bar(ready[b]), 0));
+            }
         }
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
     } else if (warp >= 12) {
         // ------------------------------------------------------------------ sums out: a row of W, half of the columns
-        regs_inc<136>();
+        regs_inc<144>();
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
         const uint32_t dcol = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
-        const uint32_t stage = y0 + half * 2 * kW8StageBytes;
-        const int chunks = half_cols / kW8StageCols;
+        const int chunks = half_cols / 16;
         auto meet = [&]() { named_bar_sync(1 + half, 128); };
         W8At a = w8_at(p, first);
-        uint32_t tiles = 0, stores = 0;
+        uint32_t tiles = 0;
         for (int at = first; at < end; ++tiles) {
             const W8WideProb& pr = p.prob[a.prob];
             const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = min(tile_end, end);
@@ -363,23 +368,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                     to[2 * j + 1] = pack2(v[4 * j + 2] * f.z * sw, v[4 * j + 3] * f.w * sw);
                 }
             };
-            // 16 columns of y, [column][row of W], through shared memory and one bulk store (what
-            // lies outside y is not written)
-            auto store = [&](int c, const uint32_t* from) {
-                const uint32_t buf = stage + (stores & 1) * kW8StageBytes;
-                if (g == 0) bulk_wait_read1();                 // the last store but one has left its buffer
-                meet();
+            // 16 columns of y.  Neighbouring lanes swap halves, so that a lane stores two rows of W of
+            // one column: 64 bytes a column and warp
+            const int odd = lane & 1;
+            int left = 0;                                      // columns of y from the lane's next one
+            int64_t two = 0;
+            __nv_bfloat16* to = nullptr;
+            auto store_from = [&]() {
+                left = row0 + r < pr.N ? p.T - col0 - odd : 0;
+                two = 2 * pr.ldy;
+                to = pr.y + (int64_t)(col0 + odd) * pr.ldy + row0 + (r & ~1);
+                asm volatile("" : "+l"(two), "+l"(to), "+r"(left));   // not before the sums are out: registers
+            };
+            auto store = [&](const uint32_t* from) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + (j * 128 + r) * 2),
-                                 "h"((uint16_t)(j & 1 ? from[j / 2] >> 16 : from[j / 2])) : "memory");
-                fence_proxy_async_smem();
-                meet();
-                if (g == 0) {
-                    if (row0 < pr.N && col0 + c * 16 < p.T) tma_store_2d(&p.y[a.prob], row0, col0 + c * 16, buf);
-                    bulk_commit();
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t mine = from[j], other = __shfl_xor_sync(0xffffffffu, mine, 1);
+                    const uint32_t v = __byte_perm(mine, other, odd ? 0x3276 : 0x5410);
+                    if (left > 0) *reinterpret_cast<uint32_t*>(to) = v;
+                    left -= 2;
+                    to += two;
                 }
-                ++stores;
             };
             // a part lies [column / 4][row][4]
             auto part_of = [&](int64_t cta, int slot) {
@@ -389,34 +398,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             tc_fence_after();
             // a whole tile's sums become y in registers, a part goes out as it is: either way the
             // MMAs of the next tile wait for no store
-            uint32_t out[NMAX / 4];
-            float v[2][16];
-            if (ok) {
-                tmem_ld16(dcol, v[0]);
+            auto drain = [&](auto&& take) {
+                float v[2][16];
+                if (ok) {
+                    tmem_ld16(dcol, v[0]);
 #pragma unroll
-                for (int c = 0; c < NMAX / 32; ++c) {
-                    if (c < chunks) {
+                    for (int c = 0; c < NMAX / 32; ++c) {      // columns past the tile's are read for nothing
                         tmem_ld_wait16(v[c & 1]);
-                        if (c + 1 < chunks) tmem_ld16(dcol + (c + 1) * 16, v[(c + 1) & 1]);
-                        const float(&f)[16] = v[c & 1];
-                        if (whole) {
-                            scale(c, f, out + c * 8);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
-                        }
+                        if (c + 1 < NMAX / 32) tmem_ld16(dcol + (c + 1) * 16, v[(c + 1) & 1]);
+                        take(c, v[c & 1]);
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
-            if (whole && ok) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
+            };
+            if (whole) {
+                uint32_t out[NMAX / 4];
+                drain([&](int c, const float (&v)[16]) { scale(c, v, out + c * 8); });
+                if (ok) {
+                    store_from();
 #pragma unroll
-                for (int c = 0; c < NMAX / 32; ++c)
-                    if (c < chunks) store(c, out + c * 8);
-            }
-            if (!whole) {
+                    for (int c = 0; c < NMAX / 32; ++c)
+                        if (c < chunks) store(out + c * 8);
+                }
+            } else {
+                drain([&](int c, const float (&v)[16]) {
+                    if (c >= chunks) return;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                });
                 const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per;
                 uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
                 __threadfence();
@@ -426,23 +437,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 if (*reinterpret_cast<volatile uint32_t*>(&last_in[half])) {
                     __threadfence();
                     if (g == 0) *ticket = 0;
+                    store_from();
                     for (int c = 0; c < chunks; ++c) {
                         float sum[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) sum[j] = 0.f;
+#pragma unroll 4
                         for (int q = p0; q <= p1; ++q) {
-                            const float4* from = part_of((int64_t)q * 2 + rank, tile_first < q * p.per ? 0 : 1);
+                            const float4* from = part_of((int64_t)q * 2 + rank, tile_first < q * p.per ? 0 : 1) + c * 512;
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float4 x = __ldcg(from + (c * 4 + j) * 128);
+                                const float4 x = __ldcg(from + j * 128);
                                 sum[4 * j] += x.x;
                                 sum[4 * j + 1] += x.y;
                                 sum[4 * j + 2] += x.z;
                                 sum[4 * j + 3] += x.w;
                             }
                         }
+                        uint32_t out[8];
                         scale(c, sum, out);
-                        store(c, out);
+                        store(out);
                     }
                 }
                 meet();
@@ -450,10 +464,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             at = stop;
             if (at < end) a = w8_at(p, at);
         }
-        if (g == 0) bulk_wait0();
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
     } else {
-        regs_dec<56>();
+        regs_dec<48>();
     }
     tc_fence_before();
     cluster_sync();
