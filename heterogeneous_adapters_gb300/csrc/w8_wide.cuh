@@ -175,10 +175,91 @@ __device__ __forceinline__ void w8_next(const W8WideParams& p, W8At& a) {
     ++a.prob;
 }
 
+// What joining a tile's parts needs of it.
+struct W8Join {
+    const float4* part;        // the thread's row of the first pair's part in slot 0; a pair's two slots are
+    int64_t slot;              // `slot` float4 apart, pairs 4 `slot`
+    int32_t p0, p1;            // its pairs: the first one's part is in slot 1, the others' in slot 0
+    int32_t own;               // the pair whose part is in tensor memory, or -1
+    uint32_t dcol;
+    int32_t chunks;            // of 16 columns
+    const float* sx;           // shared memory
+    float sw;
+    __nv_bfloat16* to;         // y at the lane's first column and pair of rows
+    int64_t two;               // two columns of y
+    int32_t left;              // columns from the lane's first
+};
+
+// Sixteen columns' sums as bf16 pairs of y.
+__device__ __forceinline__ void w8_scale(const float (&v)[16], const float* sx, float sw, uint32_t* to) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 f = reinterpret_cast<const float4*>(sx)[j];
+        to[2 * j] = pack2(v[4 * j] * f.x * sw, v[4 * j + 1] * f.y * sw);
+        to[2 * j + 1] = pack2(v[4 * j + 2] * f.z * sw, v[4 * j + 3] * f.w * sw);
+    }
+}
+// Sixteen columns of y.  Neighbouring lanes swap halves, so that a lane stores two rows of W of one
+// column: 64 bytes a column and warp.
+__device__ __forceinline__ void w8_store(const uint32_t* from, __nv_bfloat16*& to, int64_t two, int& left) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t mine = from[j], other = __shfl_xor_sync(0xffffffffu, mine, 1);
+        const uint32_t v = __byte_perm(mine, other, threadIdx.x & 1 ? 0x3276 : 0x5410);
+        if (left > 0) *reinterpret_cast<uint32_t*>(to) = v;
+        left -= 2;
+        to += two;
+    }
+}
+
+// A tile's sums over all parts, in the order of K, 32 columns at a time.  Out of line: inlined, it
+// takes registers from the path of whole tiles, whose spills cost as much as the path itself.
+__device__ __forceinline__ void w8_join(W8Join j) {
+    for (int c = 0; c < j.chunks; c += 2) {
+        const bool both = c + 1 < j.chunks;
+        float sum[2][16];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i / 16][i % 16] = 0.f;
+        for (int q = j.p0; q <= j.p1; ++q) {
+            float x[2][16];
+            if (q == j.own) {
+                tmem_ld16(j.dcol + c * 16, x[0]);
+                tmem_ld16(j.dcol + (both ? c + 1 : c) * 16, x[1]);
+                tmem_ld_wait16(x[0]);
+                tmem_ld_wait16(x[1]);
+            } else {
+                const float4* from = j.part + (4 * (int64_t)(q - j.p0) + (q == j.p0)) * j.slot + c * 512;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 f = __ldcg(from + (i < 4 || both ? i : i - 4) * 128);
+                    x[i / 4][i % 4 * 4] = f.x;
+                    x[i / 4][i % 4 * 4 + 1] = f.y;
+                    x[i / 4][i % 4 * 4 + 2] = f.z;
+                    x[i / 4][i % 4 * 4 + 3] = f.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[i / 16][i % 16] += x[i / 16][i % 16];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (i == 0 || both) {
+                uint32_t out[8];
+                w8_scale(sum[i], j.sx + (c + i) * 16, j.sw, out);
+                w8_store(out, j.to, j.two, j.left);
+            }
+    }
+}
+
 // NMAX: the most columns of a tile.
 template <int NMAX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w8_wide_kernel(const __grid_constant__ W8WideParams p) {
     constexpr int kWStages = w8_w_stages(NMAX), kXStage = NMAX * 128;
+    // Registers move from the warps that issue and widen to those that hold a row's sums: the shares of
+    // the five groups of four warps add up to the 480 of the launch.  (A few spilled registers in the
+    // path of whole tiles cost as much as the path itself.)
+    constexpr int kRegsOut = NMAX > 128 ? 160 : 136, kRegsWiden = NMAX > 128 ? 56 : 80, kRegsMisc = 48;
+    static_assert(kRegsMisc + 2 * kRegsWiden + 2 * kRegsOut <= 480, "registers of the launch");
     constexpr uint32_t kACol = 256;            // D in columns 0 .. 255, four A buffers of 64 columns after it
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full, d_empty, final_bar;
@@ -220,11 +301,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         return (bool)__all_sync(0xffffffffu, mbar_wait_quiet(bar(which), parity, p.limit_ns));
     };
 
-    // Registers from the warps that issue and widen to those that hold a row's sums: 56, twice 72
-    // and twice 136 a thread of the five groups of four warps, 472 of the 480 of the launch.
     if (warp == 0) {
         // ------------------------------------------------------------------ W, one thread
-        regs_dec<48>();
+        regs_dec<kRegsMisc>();
         if (lane == 0) {
             W8At a = w8_at(p, first);
             uint32_t i = 0;
@@ -242,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------------ x, one thread
-        regs_dec<48>();
+        regs_dec<kRegsMisc>();
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
             W8At a = w8_at(p, first);
@@ -267,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issue, the even CTA's
-        regs_dec<48>();
+        regs_dec<kRegsMisc>();
         if (rank == 0) {
             const uint32_t idesc = (1u << 4) | ((uint32_t)(p.cols >> 3) << 17) | ((256u >> 4) << 24);   // f16, fp32 sums
             const uint64_t x_desc = smem_desc(x0, 16, 1024, 2);
@@ -303,14 +382,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------------ widening: a row of W, every other step
-        regs_dec<72>();
+        regs_dec<kRegsWiden>();
         const int quad = warp & 3, r = quad * 32 + lane;
         const uint32_t acol = tmem + ((uint32_t)(quad * 32) << 16) + kACol;
         uint32_t i = (warp - 4) >> 2;
         for (int u = first + (int)i; u < end; u += 2, i += 2) {
             const uint32_t s = i % kWStages, b = i % kW8Bufs;
             if (!wait(w_full[s], (i / kWStages) & 1)) { ok = false; break; }
-#pragma unroll
+#pragma unroll (NMAX > 128 ? 1 : 2)
             for (int h = 0; h < 2; ++h) {
                 uint32_t out[32];
 #pragma unroll
@@ -339,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
     } else if (warp >= 12) {
         // ------------------------------------------------------------------ sums out: a row of W, half of the columns
-        regs_inc<144>();
+        regs_inc<kRegsOut>();
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
         const uint32_t dcol = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
         const int chunks = half_cols / 16;
@@ -359,37 +438,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             if (ok && !wait(d_full, tiles & 1)) lost[half] = 1;
             meet();
             ok = *reinterpret_cast<volatile uint32_t*>(&lost[half]) == 0;
-            // 16 columns' sums as bf16 pairs of y
-            auto scale = [&](int c, const float (&v)[16], uint32_t* to) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sx[half][c * 16 + 4 * j]);
-                    to[2 * j] = pack2(v[4 * j] * f.x * sw, v[4 * j + 1] * f.y * sw);
-                    to[2 * j + 1] = pack2(v[4 * j + 2] * f.z * sw, v[4 * j + 3] * f.w * sw);
-                }
-            };
-            // 16 columns of y.  Neighbouring lanes swap halves, so that a lane stores two rows of W of
-            // one column: 64 bytes a column and warp
-            const int odd = lane & 1;
-            int left = 0;                                      // columns of y from the lane's next one
-            int64_t two = 0;
-            __nv_bfloat16* to = nullptr;
-            auto store_from = [&]() {
-                left = row0 + r < pr.N ? p.T - col0 - odd : 0;
-                two = 2 * pr.ldy;
-                to = pr.y + (int64_t)(col0 + odd) * pr.ldy + row0 + (r & ~1);
-                asm volatile("" : "+l"(two), "+l"(to), "+r"(left));   // not before the sums are out: registers
-            };
-            auto store = [&](const uint32_t* from) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t mine = from[j], other = __shfl_xor_sync(0xffffffffu, mine, 1);
-                    const uint32_t v = __byte_perm(mine, other, odd ? 0x3276 : 0x5410);
-                    if (left > 0) *reinterpret_cast<uint32_t*>(to) = v;
-                    left -= 2;
-                    to += two;
-                }
-            };
             // a part lies [column / 4][row][4]
             auto part_of = [&](int64_t cta, int slot) {
                 return reinterpret_cast<float4*>(p.part + (cta * 2 + slot) * (int64_t)w8_part_floats(NMAX) + (int64_t)half * half_cols * 128) + r;
@@ -415,48 +463,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             };
             if (whole) {
                 uint32_t out[NMAX / 4];
-                drain([&](int c, const float (&v)[16]) { scale(c, v, out + c * 8); });
+                drain([&](int c, const float (&v)[16]) { w8_scale(v, &sx[half][c * 16], sw, out + c * 8); });
                 if (ok) {
-                    store_from();
+                    int left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
+                    int64_t two = 2 * pr.ldy;
+                    __nv_bfloat16* to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
+                    asm volatile("" : "+l"(two), "+l"(to), "+r"(left));   // not before the sums are out: registers
 #pragma unroll
                     for (int c = 0; c < NMAX / 32; ++c)
-                        if (c < chunks) store(out + c * 8);
+                        if (c < chunks) w8_store(out + c * 8, to, two, left);
                 }
             } else {
-                drain([&](int c, const float (&v)[16]) {
-                    if (c >= chunks) return;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                });
                 const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per;
                 uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
-                __threadfence();
+                auto join = [&](int own) {
+                    W8Join j;
+                    j.part = part_of((int64_t)p0 * 2 + rank, 0);
+                    j.slot = w8_part_floats(NMAX) / 4;
+                    j.p0 = p0;
+                    j.p1 = p1;
+                    j.own = own;
+                    j.dcol = dcol;
+                    j.chunks = chunks;
+                    j.sx = sx[half];
+                    j.sw = sw;
+                    j.to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
+                    j.two = 2 * pr.ldy;
+                    j.left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
+                    w8_join(j);
+                };
+                // Where all other parts are there already (a pair comes to the tile that it begins last, when
+                // the next pair has long done its rest), this one stays where it is.
+                if (g == 0) {
+                    uint32_t there;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
+                    last_in[half] = there == (uint32_t)(p1 - p0);
+                }
                 meet();
-                if (g == 0) last_in[half] = atomicAdd(ticket, 1u) == (uint32_t)(p1 - p0);
-                meet();
-                if (*reinterpret_cast<volatile uint32_t*>(&last_in[half])) {
+                const bool early = *reinterpret_cast<volatile uint32_t*>(&last_in[half]) && ok;
+                if (early) {
                     __threadfence();
+                    join(pair);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
                     if (g == 0) *ticket = 0;
-                    store_from();
-                    for (int c = 0; c < chunks; ++c) {
-                        float sum[16];
+                } else {
+                    drain([&](int c, const float (&v)[16]) {
+                        if (c >= chunks) return;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[j] = 0.f;
-#pragma unroll 4
-                        for (int q = p0; q <= p1; ++q) {
-                            const float4* from = part_of((int64_t)q * 2 + rank, tile_first < q * p.per ? 0 : 1) + c * 512;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float4 x = __ldcg(from + j * 128);
-                                sum[4 * j] += x.x;
-                                sum[4 * j + 1] += x.y;
-                                sum[4 * j + 2] += x.z;
-                                sum[4 * j + 3] += x.w;
-                            }
-                        }
-                        uint32_t out[8];
-                        scale(c, sum, out);
-                        store(out);
+                        for (int j = 0; j < 4; ++j) part[(c * 4 + j) * 128] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    });
+                    __threadfence();
+                    meet();
+                    if (g == 0) last_in[half] = atomicAdd(ticket, 1u) == (uint32_t)(p1 - p0);
+                    meet();
+                    if (*reinterpret_cast<volatile uint32_t*>(&last_in[half])) {
+                        __threadfence();
+                        if (g == 0) *ticket = 0;
+                        join(-1);
                     }
                 }
                 meet();
@@ -466,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         }
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
     } else {
-        regs_dec<48>();
+        regs_dec<kRegsMisc>();
     }
     tc_fence_before();
     cluster_sync();
