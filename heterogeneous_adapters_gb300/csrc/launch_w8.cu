@@ -138,49 +138,67 @@ lora_status map2d(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, CUten
     return LORA_ECUDA;
 }
 
-template <int NMAX>
-lora_status launch_wide(W8WideParams& w, cudaStream_t s) {
+// Readies a kernel on the current device, once; pairs of CTAs that the device holds at a time.
+template <int NMAX, bool SPLIT>
+lora_status ready_wide(int* out) {
     DeviceInfo* di = nullptr;
     lora_status st = device_info(&di);
     if (st != LORA_OK) return st;
-    auto kern = w8_wide_kernel<NMAX>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kW8WideThreads);
-    cfg.dynamicSmemBytes = w8_wide_smem(NMAX);
+    auto kern = w8_wide_kernel<NMAX, SPLIT>;
     static thread_local const DeviceInfo* ready = nullptr;
     static thread_local int pairs = 0;
     if (ready != di) {
-        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes));
-        if (st != LORA_OK) return st;
         cudaLaunchAttribute pair;
         pair.id = cudaLaunchAttributeClusterDimension;
         pair.val.clusterDim.x = 2;
         pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(di->sm_count / 2 * 2);
+        cfg.blockDim = dim3(kW8WideThreads);
+        cfg.dynamicSmemBytes = w8_wide_smem(NMAX);
         cfg.attrs = &pair;
         cfg.numAttrs = 1;
+        st = cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes));
+        if (st != LORA_OK) return st;
         st = cuda_status(cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg));
         if (st != LORA_OK) return st;
         pairs = std::max(1, std::min(pairs, kW8MaxPairs));
         ready = di;
     }
+    *out = pairs;
+    return LORA_OK;
+}
+
+template <int NMAX, bool SPLIT>
+lora_status launch_wide(const W8WideParams& w, int pairs, cudaStream_t s) {
+    cudaLaunchAttribute early;                         // it waits for w8_widen_kernel itself
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * std::min(pairs, (w.total + w.per - 1) / w.per));
+    cfg.blockDim = dim3(kW8WideThreads);
+    cfg.dynamicSmemBytes = w8_wide_smem(NMAX);
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    cfg.stream = s;
+    return cuda_status(cudaLaunchKernelEx(&cfg, w8_wide_kernel<NMAX, SPLIT>, w));
+}
+
+template <int NMAX>
+lora_status share_wide(W8WideParams& w, cudaStream_t s) {
+    int pairs = 0, same = 0;
+    lora_status st = ready_wide<NMAX, false>(&pairs);
+    if (st == LORA_OK) st = ready_wide<NMAX, true>(&same);
+    if (st != LORA_OK) return st;
     // equal shares of all steps, or whole tiles where the largest share of them is not much more
     // (which needs one K for all projections)
-    int32_t per = (w.total + pairs - 1) / pairs;
+    w.per = (w.total + pairs - 1) / pairs;
     const int32_t kb = w.prob[0].kblocks;
     bool one_k = true;
     for (int32_t i = 1; i < w.nprob; ++i) one_k = one_k && w.prob[i].kblocks == kb;
     const int32_t whole = (w.total / kb + pairs - 1) / pairs * kb;
-    if (one_k && whole <= per + kW8JoinCost) per = whole;
-    w.per = per;
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    cfg.stream = s;
-    cfg.gridDim = dim3(2 * std::min(pairs, (w.total + per - 1) / per));
-    return cuda_status(cudaLaunchKernelEx(&cfg, kern, w));
+    if (one_k && whole <= w.per + kW8JoinCost) w.per = whole;
+    return one_k && w.per % kb == 0 ? launch_wide<NMAX, false>(w, pairs, s) : launch_wide<NMAX, true>(w, pairs, s);
 }
 
 lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, cudaStream_t s) {
@@ -232,8 +250,8 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
     w8_widen_kernel<<<dim3((unsigned)blocks, (unsigned)copies), kWidenThreads, 0, s>>>(v);
     st = cuda_status(cudaGetLastError());
     if (st != LORA_OK) return st;
-    if (sh.nmax == 64) return launch_wide<64>(w, s);
-    return sh.nmax == 128 ? launch_wide<128>(w, s) : launch_wide<256>(w, s);
+    if (sh.nmax == 64) return share_wide<64>(w, s);
+    return sh.nmax == 128 ? share_wide<128>(w, s) : share_wide<256>(w, s);
 }
 
 }  // namespace

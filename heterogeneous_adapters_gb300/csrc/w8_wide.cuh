@@ -212,8 +212,7 @@ __device__ __forceinline__ void w8_store(const uint32_t* from, __nv_bfloat16*& t
     }
 }
 
-// A tile's sums over all parts, in the order of K, 32 columns at a time.  Out of line: inlined, it
-// takes registers from the path of whole tiles, whose spills cost as much as the path itself.
+// A tile's sums over all parts, in the order of K, 32 columns at a time.
 __device__ __forceinline__ void w8_join(W8Join j) {
     for (int c = 0; c < j.chunks; c += 2) {
         const bool both = c + 1 < j.chunks;
@@ -251,8 +250,9 @@ __device__ __forceinline__ void w8_join(W8Join j) {
     }
 }
 
-// NMAX: the most columns of a tile.
-template <int NMAX>
+// NMAX: the most columns of a tile.  SPLIT: whether a pair's range may begin or end inside a tile
+// (the code for that takes registers from the path of whole tiles).
+template <int NMAX, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w8_wide_kernel(const __grid_constant__ W8WideParams p) {
     constexpr int kWStages = w8_w_stages(NMAX), kXStage = NMAX * 128;
     // Registers move from the warps that issue and widen to those that hold a row's sums: the shares of
@@ -429,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             const W8WideProb& pr = p.prob[a.prob];
             const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = min(tile_end, end);
             const int row0 = a.rt * kW8WideRows + (int)rank * 128, col0 = a.tt * p.cols + half * half_cols;
-            const bool whole = at == tile_first && stop == tile_end;
+            const bool whole = !SPLIT || (at == tile_first && stop == tile_end);
             const float sw = row0 + r < pr.N ? pr.w_scales[row0 + r] : 0.f;
             meet();                                            // the last tile's scales have been read
             sx[half][g] = col0 + g < p.T && g < half_cols ? pr.x_scales[col0 + g] : 0.f;
