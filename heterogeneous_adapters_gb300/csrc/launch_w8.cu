@@ -42,20 +42,26 @@ Q8Out out_of(const lora_q8_rows& o) {
             o.x_kind == LORA_Q8_X_FULL};
 }
 
-// Eights of a row a thread, and threads of a row.
-struct RowShape {
-    int v, threads;
-};
-RowShape row_shape(int32_t d) {
-    const int eights = d / 8, v = eights <= 512 ? 1 : eights <= 1024 ? 2 : 4;
-    return {v, ((eights + v - 1) / v + 31) / 32 * 32};
+// Threads of a row, and CTAs: every row its own while the SMs hold them all, else as many as the
+// SMs hold (1,024 threads, at the kernels' 64 registers), each with rows in turn.
+template <typename K, typename P>
+lora_status launch_rows(K kern, const P& q, int v, cudaStream_t s) {
+    DeviceInfo* di = nullptr;
+    lora_status st = device_info(&di);
+    if (st != LORA_OK) return st;
+    const int threads = ((q.d / 8 + v - 1) / v + 31) / 32 * 32;
+    kern<<<std::min(q.T, di->sm_count * std::max(1024 / threads, 1)), threads, 0, s>>>(q);
+    return cuda_status(cudaGetLastError());
 }
 
+// Eights of a row that a thread holds.
+int row_eights(int32_t d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
+
 template <int ACT>
-void launch_gate(const Q8GateParams& q, RowShape sh, int32_t T, cudaStream_t s) {
-    if (sh.v == 1) q8_gate_kernel<1, ACT><<<T, sh.threads, 0, s>>>(q);
-    else if (sh.v == 2) q8_gate_kernel<2, ACT><<<T, sh.threads, 0, s>>>(q);
-    else q8_gate_kernel<4, ACT><<<T, sh.threads, 0, s>>>(q);
+lora_status launch_gate(const Q8GateParams& q, cudaStream_t s) {
+    const int v = row_eights(q.d);
+    if (v == 1) return launch_rows(q8_gate_kernel<1, ACT, true>, q, v, s);
+    return v == 2 ? launch_rows(q8_gate_kernel<2, ACT, true>, q, v, s) : launch_rows(q8_gate_kernel<4, ACT, false>, q, v, s);
 }
 
 // ---------------------------------------------------------------------------- products
@@ -273,13 +279,11 @@ lora_status lora_q8_norm(const lora_q8_norm_desc* n, int32_t T, void* stream) {
     if (T == 0) return LORA_OK;
     const Q8NormParams q = {reinterpret_cast<const __nv_bfloat16*>(n->x), reinterpret_cast<const __nv_bfloat16*>(n->residual),
                             reinterpret_cast<__nv_bfloat16*>(n->sum), reinterpret_cast<const __nv_bfloat16*>(n->weight),
-                            n->ldx, n->ldr, n->lds, n->eps, n->d, out_of(n->out)};
-    const RowShape sh = row_shape(n->d);
+                            n->ldx, n->ldr, n->lds, n->eps, n->d, T, out_of(n->out)};
+    const int v = row_eights(n->d);
     cudaStream_t s = (cudaStream_t)stream;
-    if (sh.v == 1) q8_norm_kernel<1><<<T, sh.threads, 0, s>>>(q);
-    else if (sh.v == 2) q8_norm_kernel<2><<<T, sh.threads, 0, s>>>(q);
-    else q8_norm_kernel<4><<<T, sh.threads, 0, s>>>(q);
-    return cuda_status(cudaGetLastError());
+    if (v == 1) return launch_rows(q8_norm_kernel<1, true>, q, v, s);
+    return v == 2 ? launch_rows(q8_norm_kernel<2, true>, q, v, s) : launch_rows(q8_norm_kernel<4, false>, q, v, s);
 }
 
 lora_status lora_q8_gate(const lora_q8_gate_desc* n, int32_t T, void* stream) {
@@ -293,16 +297,14 @@ lora_status lora_q8_gate(const lora_q8_gate_desc* n, int32_t T, void* stream) {
     if (pitch_differs(n->out.x, n->out.ldx, n->gate, n->ldg) || pitch_differs(n->out.x, n->out.ldx, n->up, n->ldu)) return LORA_EINVAL;
     if (T == 0) return LORA_OK;
     const Q8GateParams q = {reinterpret_cast<const __nv_bfloat16*>(n->gate), reinterpret_cast<const __nv_bfloat16*>(n->up),
-                            n->ldg, n->ldu, n->d, out_of(n->out)};
-    const RowShape sh = row_shape(n->d);
+                            n->ldg, n->ldu, n->d, T, out_of(n->out)};
     cudaStream_t s = (cudaStream_t)stream;
     switch (n->act) {
-        case LORA_ACT_NONE: launch_gate<LORA_ACT_NONE>(q, sh, T, s); break;
-        case LORA_ACT_SILU: launch_gate<LORA_ACT_SILU>(q, sh, T, s); break;
-        case LORA_ACT_GELU: launch_gate<LORA_ACT_GELU>(q, sh, T, s); break;
-        default: launch_gate<LORA_ACT_GELU_TANH>(q, sh, T, s);
+        case LORA_ACT_NONE: return launch_gate<LORA_ACT_NONE>(q, s);
+        case LORA_ACT_SILU: return launch_gate<LORA_ACT_SILU>(q, s);
+        case LORA_ACT_GELU: return launch_gate<LORA_ACT_GELU>(q, s);
+        default: return launch_gate<LORA_ACT_GELU_TANH>(q, s);
     }
-    return cuda_status(cudaGetLastError());
 }
 
 lora_status lora_w8_workspace_size(const lora_w8_problem* probs, int32_t nprob, int32_t T, size_t* bytes) {

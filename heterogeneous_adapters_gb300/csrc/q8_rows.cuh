@@ -2,7 +2,8 @@
 // activation (include/lora_w8.h).
 //
 // A row's codes need its largest magnitude, so a CTA holds one row in registers between its
-// only read and its only write, with one exchange between the warps.
+// only read and its only write, with one exchange between the warps.  A CTA takes row after row,
+// with the next row's loads on their way while it works on one.
 #pragma once
 #include "lora_w8.h"
 #include "mma_legacy.cuh"
@@ -25,7 +26,7 @@ struct Q8NormParams {
     const __nv_bfloat16* weight;
     int64_t ldx, ldr, lds;
     float eps;
-    int32_t d;
+    int32_t d, T;
     Q8Out out;
 };
 
@@ -33,7 +34,7 @@ struct Q8GateParams {
     const __nv_bfloat16* gate;
     const __nv_bfloat16* up;
     int64_t ldg, ldu;
-    int32_t d;
+    int32_t d, T;
     Q8Out out;
 };
 
@@ -67,16 +68,23 @@ __device__ __forceinline__ void q8_reduce(uint32_t& top, float& ss, uint32_t* re
 __device__ __forceinline__ void q8_codes(const float (&p)[8], float top, float inv, float (&c)[8], uint2& packed) {
     constexpr float kMagic = 12582912.0f;
     uint32_t b[8];
+    float far = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float v = p[i] * inv, t = v + kMagic;
+        const float t = fmaf(p[i], inv, kMagic);
         c[i] = t - kMagic;
-        if (fabsf(v - c[i]) > 0.4999f) {
+        far = fmaxf(far, fabsf(fmaf(p[i], inv, -c[i])));
+        b[i] = __float_as_uint(t);
+    }
+    if (far > 0.4999f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
             const float e = fmaf(-c[i], top, 127.0f * p[i]), half = 0.5f * top;
-            const bool odd = __float_as_uint(t) & 1u;
-            if (fabsf(e) > half || (fabsf(e) == half && odd)) c[i] += copysignf(1.0f, e);
+            if (fabsf(e) > half || (fabsf(e) == half && (b[i] & 1u))) {
+                c[i] += copysignf(1.0f, e);
+                b[i] = __float_as_uint(c[i] + kMagic);
+            }
         }
-        b[i] = __float_as_uint(c[i] + kMagic);
     }
     packed.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
     packed.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
@@ -100,147 +108,191 @@ __device__ __forceinline__ void q8_store(const Q8Out& o, int64_t row, int at, co
     st16(o.x + row * o.ldx + at, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// A row per CTA; thread i holds the eight values from columns 8 (i + j blockDim), j < V.
-template <int V>
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; thread i holds the eight values from columns
+// 8 (i + j blockDim), j < V.  PRE: the next row is fetched ahead.
+template <int V, bool PRE>
 __global__ void __launch_bounds__(1024) q8_norm_kernel(const __grid_constant__ Q8NormParams q) {
-    __shared__ uint32_t red_top[2][32];
-    __shared__ float red_ss[2][32];
-    const int64_t row = blockIdx.x;
+    __shared__ uint32_t red_top[3][32];
+    __shared__ float red_ss[3][32];
     const int tid = threadIdx.x;
-    float h[V][8], p[V][8];
-    uint32_t top = 0;
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int at = 8 * (tid + j * blockDim.x);
-        if (at >= q.d) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[j][i] = p[j][i] = 0.f;
-            continue;
-        }
-        unpack8(ld16(q.x + row * q.ldx + at), h[j]);
-        if (q.residual) {
-            float r[8];
-            unpack8(ld16(q.residual + row * q.ldr + at), r);
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // the sum is held in bf16, and the norm is that of what is held
-                w[i] = pack2(h[j][2 * i] + r[2 * i], h[j][2 * i + 1] + r[2 * i + 1]);
-                h[j][2 * i] = bf16lo(w[i]);
-                h[j][2 * i + 1] = bf16hi(w[i]);
-            }
-            if (q.sum) st16(q.sum + row * q.lds + at, make_uint4(w[0], w[1], w[2], w[3]));
-        }
-        float g[8];
-        unpack8(ld16(q.weight + at), g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            p[j][i] = h[j][i] * g[i];
-            ss = fmaf(h[j][i], h[j][i], ss);
-            top = max(top, __float_as_uint(fabsf(p[j][i])));
-        }
-    }
-    q8_reduce(top, ss, red_top[0], red_ss[0]);
-    float over = 1.f / sqrtf(ss / (float)q.d + q.eps), back = 1.f;
-    const bool large = __float_as_uint(ss) == kInfBits;
-    if (large || (top != 0 && __uint_as_float(top) < kQ8Small)) {
-        // squares past fp32's range, or products near its other end: once more by a power of two
-        const float by_h = large ? 0x1p-80f : 0x1p32f, by_w = large ? 1.f : 0x1p32f;
-        ss = 0.f;
-        top = 0;
+    const bool add = q.residual != nullptr;
+    uint4 xn[V], rn[V];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int at = 8 * (tid + j * blockDim.x);
-            if (at >= q.d) continue;
-            float g[8];
-            unpack8(ld16(q.weight + at), g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                h[j][i] *= by_h;
-                p[j][i] = h[j][i] * (g[i] * by_w);
-                ss = fmaf(h[j][i], h[j][i], ss);
-                top = max(top, __float_as_uint(fabsf(p[j][i])));
+            xn[j] = rn[j] = make_uint4(0, 0, 0, 0);
+            if (at < q.d && row < q.T) {
+                xn[j] = ld16(q.x + row * q.ldx + at);
+                if (add) rn[j] = ld16(q.residual + row * q.ldr + at);
             }
         }
-        q8_reduce(top, ss, red_top[1], red_ss[1]);
-        if (large) over = 1.f / sqrtf(ss / (float)q.d);         // of values so large that eps is nothing
-        else back = kQ8Small;
-    }
-    float inv = 0.f, scale = 0.f;
-    const float m = __uint_as_float(top);
-    if (top >= kInfBits) scale = over = __uint_as_float(0x7FC00000u);
-    else if (top != 0) {
-        inv = 127.f / m;
-        scale = m * over / 127.f * back;
-        over *= back;
-    }
-    if (tid == 0) q.out.scales[row] = scale;
+    };
+    uint4 gw[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int at = 8 * (tid + j * blockDim.x);
-        if (at < q.d) q8_store(q.out, row, at, p[j], m, inv, scale, over);
+        gw[j] = at < q.d ? ld16(q.weight + at) : make_uint4(0, 0, 0, 0);
+    }
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < q.T; row += gridDim.x, turn ^= 1) {
+        float p[V][8];
+        uint32_t top = 0;
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int at = 8 * (tid + j * blockDim.x);
+            float h[8], g[8];
+            unpack8(xn[j], h);
+            if (add) {
+                float r[8];
+                unpack8(rn[j], r);
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // the sum is held in bf16, and the norm is that of what is held
+                    w[i] = pack2(h[2 * i] + r[2 * i], h[2 * i + 1] + r[2 * i + 1]);
+                    h[2 * i] = bf16lo(w[i]);
+                    h[2 * i + 1] = bf16hi(w[i]);
+                }
+                if (q.sum && at < q.d) st16(q.sum + row * q.lds + at, make_uint4(w[0], w[1], w[2], w[3]));
+            }
+            unpack8(gw[j], g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[j][i] = h[i] * g[i];
+                ss = fmaf(h[i], h[i], ss);
+                top = max(top, __float_as_uint(fabsf(p[j][i])));
+            }
+        }
+        if (PRE) fetch(row + gridDim.x);
+        q8_reduce(top, ss, red_top[turn], red_ss[turn]);
+        float over = 1.f / sqrtf(ss / (float)q.d + q.eps), back = 1.f;
+        const bool large = __float_as_uint(ss) == kInfBits;
+        if (large || (top != 0 && __uint_as_float(top) < kQ8Small)) {
+            // squares past fp32's range, or products near its other end: once more by a power of two
+            const float by_h = large ? 0x1p-80f : 0x1p32f, by_w = large ? 1.f : 0x1p32f;
+            ss = 0.f;
+            top = 0;
+            // from h where that is held: x or the residual may have given it their place
+            const __nv_bfloat16* from = q.sum ? q.sum + row * q.lds : q.x + row * q.ldx;
+#pragma unroll 1
+            for (int j = 0; j < V; ++j) {
+                const int at = 8 * (tid + j * blockDim.x);
+                if (at >= q.d) continue;
+                float h[8], g[8];
+                unpack8(ld16(from + at), h);
+                if (add && !q.sum) {
+                    float r[8];
+                    unpack8(ld16(q.residual + row * q.ldr + at), r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = __bfloat162float(__float2bfloat16_rn(h[i] + r[i]));
+                }
+                unpack8(ld16(q.weight + at), g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float v = h[i] * by_h, w = v * (g[i] * by_w);
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (k == j) p[k][i] = w;
+                    ss = fmaf(v, v, ss);
+                    top = max(top, __float_as_uint(fabsf(w)));
+                }
+            }
+            q8_reduce(top, ss, red_top[2], red_ss[2]);
+            if (large) over = 1.f / sqrtf(ss / (float)q.d);     // of values so large that eps is nothing
+            else back = kQ8Small;
+        }
+        float inv = 0.f, scale = 0.f;
+        const float m = __uint_as_float(top);
+        if (top >= kInfBits) scale = over = __uint_as_float(0x7FC00000u);
+        else if (top != 0) {
+            inv = 127.f / m;
+            scale = m * over / 127.f * back;
+            over *= back;
+        }
+        if (tid == 0) q.out.scales[row] = scale;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int at = 8 * (tid + j * blockDim.x);
+            if (at < q.d) q8_store(q.out, row, at, p[j], m, inv, scale, over);
+        }
+        if (!PRE) fetch(row + gridDim.x);
     }
 }
 
 template <int ACT>
 __device__ __forceinline__ float q8_act(float a) {
-    if (ACT == LORA_ACT_SILU) return a / (1.f + expf(-a));
+    // e^-a to 2^-24 (4 + |a|) of itself; where it passes fp32's range, a e^a is nothing
+    if (ACT == LORA_ACT_SILU) return a * rcp_approx(1.f + exp2_approx(-1.44269504f * a));
     if (ACT == LORA_ACT_GELU) return 0.5f * a * (1.f + erff(a * 0.70710678f));
     if (ACT == LORA_ACT_GELU_TANH) return 0.5f * a * (1.f + tanhf(0.79788456f * (a + 0.044715f * a * a * a)));
     return a;
 }
 
-template <int V, int ACT>
+template <int V, int ACT, bool PRE>
 __global__ void __launch_bounds__(1024) q8_gate_kernel(const __grid_constant__ Q8GateParams q) {
     __shared__ uint32_t red_top[2][32];
     __shared__ float red_ss[2][32];
-    const int64_t row = blockIdx.x;
     const int tid = threadIdx.x;
-    float p[V][8];
-    uint32_t top = 0;
-    float none = 0.f;
+    const bool gated = q.up != nullptr;
+    uint4 an[V], un[V];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int at = 8 * (tid + j * blockDim.x);
-        if (at >= q.d) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[j][i] = 0.f;
-            continue;
+        for (int j = 0; j < V; ++j) {
+            const int at = 8 * (tid + j * blockDim.x);
+            an[j] = un[j] = make_uint4(0, 0, 0, 0);
+            if (at < q.d && row < q.T) {
+                an[j] = ld16(q.gate + row * q.ldg + at);
+                if (gated) un[j] = ld16(q.up + row * q.ldu + at);
+            }
         }
-        unpack8(ld16(q.gate + row * q.ldg + at), p[j]);
-        float u[8];
-        if (q.up) unpack8(ld16(q.up + row * q.ldu + at), u);
+    };
+    fetch(blockIdx.x);
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < q.T; row += gridDim.x, turn ^= 1) {
+        float p[V][8];
+        uint32_t top = 0;
+        float none = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool bad = __float_as_uint(fabsf(p[j][i])) >= kInfBits || (q.up && __float_as_uint(fabsf(u[i])) >= kInfBits);
-            p[j][i] = q8_act<ACT>(p[j][i]);
-            if (q.up) p[j][i] *= u[i];
-            top = max(top, bad ? 0x7FC00000u : __float_as_uint(fabsf(p[j][i])));
+        for (int j = 0; j < V; ++j) {
+            unpack8(an[j], p[j]);
+            float u[8];
+            unpack8(un[j], u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool bad = max(__float_as_uint(fabsf(p[j][i])), __float_as_uint(fabsf(u[i]))) >= kInfBits;
+                p[j][i] = q8_act<ACT>(p[j][i]);
+                if (gated) p[j][i] *= u[i];
+                top = max(top, bad ? 0x7FC00000u : __float_as_uint(fabsf(p[j][i])));
+            }
         }
-    }
-    q8_reduce(top, none, red_top[0], red_ss[0]);
-    float back = 1.f;
-    if (top != 0 && __uint_as_float(top) < kQ8Small) {       // near fp32's smallest values: by a power of two
-        back = kQ8Small;
-        top = __float_as_uint(__uint_as_float(top) * kQ8Up);
+        if (PRE) fetch(row + gridDim.x);
+        q8_reduce(top, none, red_top[turn], red_ss[turn]);
+        float back = 1.f;
+        if (top != 0 && __uint_as_float(top) < kQ8Small) {  // near fp32's smallest values: by a power of two
+            back = kQ8Small;
+            top = __float_as_uint(__uint_as_float(top) * kQ8Up);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+            for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[j][i] *= kQ8Up;
-    }
-    float inv = 0.f, scale = 0.f, over = back;
-    const float m = __uint_as_float(top);
-    if (top >= kInfBits) scale = over = __uint_as_float(0x7FC00000u);
-    else if (top != 0) {
-        inv = 127.f / m;
-        scale = m / 127.f * back;
-    }
-    if (tid == 0) q.out.scales[row] = scale;
+                for (int i = 0; i < 8; ++i) p[j][i] *= kQ8Up;
+        }
+        float inv = 0.f, scale = 0.f, over = back;
+        const float m = __uint_as_float(top);
+        if (top >= kInfBits) scale = over = __uint_as_float(0x7FC00000u);
+        else if (top != 0) {
+            inv = 127.f / m;
+            scale = m / 127.f * back;
+        }
+        if (tid == 0) q.out.scales[row] = scale;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int at = 8 * (tid + j * blockDim.x);
-        if (at < q.d) q8_store(q.out, row, at, p[j], m, inv, scale, over);
+        for (int j = 0; j < V; ++j) {
+            const int at = 8 * (tid + j * blockDim.x);
+            if (at < q.d) q8_store(q.out, row, at, p[j], m, inv, scale, over);
+        }
+        if (!PRE) fetch(row + gridDim.x);
     }
 }
 

@@ -42,21 +42,29 @@ __device__ __forceinline__ void codes8_f16(uint32_t w, uint32_t& lo, uint32_t& h
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
 }
 
+// By the column tiles: steps of a group, whose loads are on their way while the group before is
+// multiplied, and CTAs that an SM should hold.
+__host__ __device__ constexpr int w8_group(int nt) { return nt == 1 ? 4 : 2; }
+__host__ __device__ constexpr int w8_ctas(int nt) { return nt == 2 ? 3 : nt == 1 ? 2 : 1; }
+
 // Lane (g, t) = (lane / 4, lane % 4) takes the 16 bytes from k = 16 t of its row's 64: word j of
 // them are the two pairs that an MMA of 16 of K wants of the lane, for W and for x alike, so
 // that the order of K within the 64 is the same for both.
 template <int NT>
-__global__ void __launch_bounds__(kW8Threads) w8_narrow_kernel(const __grid_constant__ W8Params p) {
+__global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(const __grid_constant__ W8Params p) {
+    constexpr int G = w8_group(NT), kStride = kW8Warps * kW8Chunk;
     __shared__ int32_t red[kW8Warps][8 * NT][kW8Rows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     int i = 0;
     while (i + 1 < p.nprob && (int)blockIdx.x >= p.prob[i + 1].first) ++i;
     const W8Prob& pr = p.prob[i];
-    const int row0 = ((int)blockIdx.x - pr.first) * kW8Rows, t0 = blockIdx.y * 8 * NT;
-    const unsigned char* w0 = pr.w + (int64_t)(row0 + g) * pr.K;
+    const int row0 = ((int)blockIdx.x - pr.first) * kW8Rows, K = pr.K;
     const bool in1 = row0 + 8 + g < pr.N;                      // N is a multiple of 8
-    const unsigned char* w1 = w0 + (in1 ? 8 * (int64_t)pr.K : 0);
-    const uint4 none = make_uint4(0, 0, 0, 0);
+    const unsigned char* w0 = pr.w + (int64_t)(row0 + g) * K;
+    const unsigned char* w1 = w0 + (in1 ? 8 * (int64_t)K : 0);
+    const unsigned char* xr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xr[n] = pr.x + min(n * 8 + g, p.T - 1) * pr.ldx;   // rows past the last: the last again
     int32_t sum[NT][4];
     float acc[NT][4];
 #pragma unroll
@@ -75,32 +83,56 @@ __global__ void __launch_bounds__(kW8Threads) w8_narrow_kernel(const __grid_cons
                 acc[n][j] = 0.f;
             }
     };
-    int steps = 0;
-#pragma unroll 2
-    for (int k = warp * kW8Chunk + 16 * t; k - 16 * t < pr.K; k += kW8Warps * kW8Chunk) {
-        const bool in = k < pr.K;
-        const uint4 a0 = in ? ld16(w0 + k) : none, a1 = in && in1 ? ld16(w1 + k) : none;
-        uint4 b[NT];
+    struct Group {
+        uint4 a[G][2], b[G][NT];
+    };
+    // a group's words; what lies past K is zeros in W
+    auto load = [&](Group& q, int k0) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            b[n] = in && t0 + n * 8 + g < p.T ? ld16(pr.x + (int64_t)(t0 + n * 8 + g) * pr.ldx + k) : none;
-        const uint32_t aw0[4] = {a0.x, a0.y, a0.z, a0.w}, aw1[4] = {a1.x, a1.y, a1.z, a1.w};
+        for (int s = 0; s < G; ++s) {
+            const int k = k0 + s * kStride;
+            const bool in = k < K;
+            q.a[s][0] = in ? ld_stream16(w0 + k) : make_uint4(0, 0, 0, 0);
+            q.a[s][1] = in ? ld_stream16(w1 + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t a[4];
-            codes8_f16(aw0[j], a[0], a[2]);
-            codes8_f16(aw1[j], a[1], a[3]);
+            for (int n = 0; n < NT; ++n) q.b[s][n] = ld16(xr[n] + (in ? k : 0));
+        }
+    };
+    auto multiply = [&](const Group& q) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint32_t bw[4] = {b[n].x, b[n].y, b[n].z, b[n].w};
-                uint32_t b0, b1;
-                codes8_f16(bw[j], b0, b1);
-                mma16816_f16(acc[n], a[0], a[1], a[2], a[3], b0, b1);
+        for (int s = 0; s < G; ++s) {
+            const uint32_t aw0[4] = {q.a[s][0].x, q.a[s][0].y, q.a[s][0].z, q.a[s][0].w};
+            const uint32_t aw1[4] = {q.a[s][1].x, q.a[s][1].y, q.a[s][1].z, q.a[s][1].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[4];
+                codes8_f16(aw0[j], a[0], a[2]);
+                codes8_f16(aw1[j], a[1], a[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint32_t bw[4] = {q.b[s][n].x, q.b[s][n].y, q.b[s][n].z, q.b[s][n].w};
+                    uint32_t b0, b1;
+                    codes8_f16(bw[j], b0, b1);
+                    mma16816_f16(acc[n], a[0], a[1], a[2], a[3], b0, b1);
+                }
             }
         }
-        if (++steps == 1024 / kW8Chunk) {
-            flush();
-            steps = 0;
+    };
+    Group q[2];
+    const int k0 = warp * kW8Chunk + 16 * t, end = K + 16 * t;  // a warp's lanes end together
+    load(q[0], k0);
+    int steps = 0;
+    for (int k = k0; k < end;) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h == 1 && k >= end) break;
+            if (k + G * kStride < end) load(q[1 - h], k + G * kStride);
+            multiply(q[h]);
+            k += G * kStride;
+            if ((steps += G) == 1024 / kW8Chunk) {
+                flush();
+                steps = 0;
+            }
         }
     }
     flush();
@@ -114,9 +146,8 @@ __global__ void __launch_bounds__(kW8Threads) w8_narrow_kernel(const __grid_cons
         int32_t s = 0;
 #pragma unroll
         for (int w = 0; w < kW8Warps; ++w) s += red[w][col][r];
-        if (t0 + col < p.T && row0 + r < pr.N)
-            pr.y[(int64_t)(t0 + col) * pr.ldy + row0 + r] =
-                __float2bfloat16_rn((float)s * pr.x_scales[t0 + col] * pr.w_scales[row0 + r]);
+        if (col < p.T && row0 + r < pr.N)
+            pr.y[col * pr.ldy + row0 + r] = __float2bfloat16_rn((float)s * pr.x_scales[col] * pr.w_scales[row0 + r]);
     }
 }
 
