@@ -268,7 +268,7 @@ lora_status lora_q8_norm(const lora_q8_norm_desc* n, int32_t T, void* stream) {
     if (n == nullptr) return LORA_EINVAL;
     lora_status st = check_shape(T, n->d);
     if (st != LORA_OK) return st;
-    if (!(n->eps >= 1e-30f) || !(n->eps <= 3.4e38f)) return LORA_EINVAL;
+    if (!(n->eps >= 1e-30f) || !(n->eps <= 1.f)) return LORA_EINVAL;
     if ((st = check_rows(n->x, n->ldx, n->d)) != LORA_OK) return st;
     if (n->residual != nullptr && (st = check_rows(n->residual, n->ldr, n->d)) != LORA_OK) return st;
     if (n->sum != nullptr && n->residual == nullptr) return LORA_EINVAL;
@@ -279,7 +279,7 @@ lora_status lora_q8_norm(const lora_q8_norm_desc* n, int32_t T, void* stream) {
     if (T == 0) return LORA_OK;
     const Q8NormParams q = {reinterpret_cast<const __nv_bfloat16*>(n->x), reinterpret_cast<const __nv_bfloat16*>(n->residual),
                             reinterpret_cast<__nv_bfloat16*>(n->sum), reinterpret_cast<const __nv_bfloat16*>(n->weight),
-                            n->ldx, n->ldr, n->lds, n->eps, n->d, T, out_of(n->out)};
+                            n->ldx, n->ldr, n->lds, n->eps, 1.f / (float)n->d, n->d, T, out_of(n->out)};
     const int v = row_eights(n->d);
     cudaStream_t s = (cudaStream_t)stream;
     if (v == 1) return launch_rows(q8_norm_kernel<1, true>, q, v, s);

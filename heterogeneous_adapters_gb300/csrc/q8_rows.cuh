@@ -25,7 +25,7 @@ struct Q8NormParams {
     __nv_bfloat16* sum;
     const __nv_bfloat16* weight;
     int64_t ldx, ldr, lds;
-    float eps;
+    float eps, by_d;               // by_d = 1 / d
     int32_t d, T;
     Q8Out out;
 };
@@ -38,74 +38,109 @@ struct Q8GateParams {
     Q8Out out;
 };
 
-constexpr uint32_t kInfBits = 0x7F800000u;
-constexpr float kQ8Up = 18446744073709551616.0f, kQ8Small = 1.0f / kQ8Up;  // 2^64 and 2^-64
+// Between these magnitudes of a row's largest value the quotients below are right; a row outside
+// is multiplied by a power of two first.
+constexpr float kQ8Small = 0x1p-64f, kQ8Large = 0x1p100f, kQ8Up = 0x1p64f, kQ8Down = 0x1p-80f;
 
-// The block's largest `top` (fp32 bits of magnitudes, in their order as integers, a NaN above
-// all) and sum of `ss`, for every thread.  A second call needs a barrier in between.
-__device__ __forceinline__ void q8_reduce(uint32_t& top, float& ss, uint32_t* red_top, float* red_ss) {
+// A word of two bf16 as a pair of fp32.
+__device__ __forceinline__ uint64_t pair_of(uint32_t w) { return pack2f(bf16lo(w), bf16hi(w)); }
+// The sum of two pairs, held in bf16: the norm is that of what is held.
+__device__ __forceinline__ uint32_t add_pairs(uint32_t a, uint32_t b) {
+    float lo, hi;
+    unpack2f(add2(pair_of(a), pair_of(b)), lo, hi);
+    return pack2(lo, hi);
+}
+// The larger of m and a pair's magnitudes (a NaN is passed over: the sums that go with the maxima show it).
+__device__ __forceinline__ float max_pair(uint64_t v, float m) {
+    float a, b;
+    unpack2f(v, a, b);
+    return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+}
+
+// The block's largest `top` (not negative) and its sum of `ss`, for every thread.
+__device__ __forceinline__ void q8_reduce(float& top, float& ss, uint32_t* red_top, float* red_ss) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    top = __reduce_max_sync(0xffffffffu, top);
+    uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if (lane == 0) {
-        red_top[warp] = top;
+        red_top[warp] = bits;
         red_ss[warp] = ss;
     }
     __syncthreads();
-    top = lane < warps ? red_top[lane] : 0u;
+    bits = lane < warps ? red_top[lane] : 0u;
     ss = lane < warps ? red_ss[lane] : 0.f;
-    top = __reduce_max_sync(0xffffffffu, top);
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
 }
 
-// Codes of eight values p of a row whose largest magnitude is `top` (> 0, and large enough for
-// inv = 127 / top to be finite): rint(127 p / top), ties to even.  1.5 * 2^23 + v rounds v to a
-// whole number and shows it in the low byte.  v is within 2^-15 of the quotient, so where it
-// lies further from a half the rounding is right; next to one, 127 p - c top (exact where p has
-// 16 bits, as a product of two bf16 does) decides.
-__device__ __forceinline__ void q8_codes(const float (&p)[8], float top, float inv, float (&c)[8], uint2& packed) {
+// What a row's values p become: codes rint(127 p / top), and for the adapters bf16(scale code) or
+// bf16(p over).
+struct Q8Row {
+    float top, inv, scale, over;
+};
+
+// Writes eight values from column `at` of a row.  1.5 * 2^23 + v rounds v to a whole number, ties to
+// even, and shows it in the low byte.  v = p inv is within 2^-15 of the quotient, so where it lies
+// further from a half the rounding is right; next to one, 127 p - c top (exact where p has 16
+// bits, as a product of two bf16 does) decides.
+__device__ __forceinline__ void q8_store(const Q8Out& o, int64_t row, int at, const uint64_t (&p)[4], const Q8Row& r) {
     constexpr float kMagic = 12582912.0f;
-    uint32_t b[8];
+    const uint64_t inv = pack2f(r.inv, r.inv), magic = pack2f(kMagic, kMagic);
+    const float by = o.full ? r.over : r.scale;
+    uint32_t two[4], w[4];                                  // two codes' low bytes, two values of x
+    auto put = [&](int i, uint64_t t) {                     // t: two codes + kMagic
+        float lo, hi;
+        unpack2f(t, lo, hi);
+        two[i] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
+        unpack2f(mul2(o.full ? p[i] : add2(t, pack2f(-kMagic, -kMagic)), pack2f(by, by)), lo, hi);
+        w[i] = pack2(lo, hi);
+    };
     float far = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = fmaf(p[i], inv, kMagic);
-        c[i] = t - kMagic;
-        far = fmaxf(far, fabsf(fmaf(p[i], inv, -c[i])));
-        b[i] = __float_as_uint(t);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t t = fma2(p[i], inv, magic);
+        far = max_pair(fma2(p[i], inv, add2(magic, mul2(t, pack2f(-1.f, -1.f)))), far);
+        put(i, t);
     }
     if (far > 0.4999f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float e = fmaf(-c[i], top, 127.0f * p[i]), half = 0.5f * top;
-            if (fabsf(e) > half || (fabsf(e) == half && (b[i] & 1u))) {
-                c[i] += copysignf(1.0f, e);
-                b[i] = __float_as_uint(c[i] + kMagic);
+        for (int i = 0; i < 4; ++i) {
+            float v[2], t[2];
+            unpack2f(p[i], v[0], v[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                t[j] = fmaf(v[j], r.inv, kMagic);
+                const float e = fmaf(kMagic - t[j], r.top, 127.0f * v[j]), half = 0.5f * r.top;
+                if (fabsf(e) > half || (fabsf(e) == half && (__float_as_uint(t[j]) & 1u))) t[j] += copysignf(1.0f, e);
             }
+            put(i, pack2f(t[0], t[1]));
         }
     }
-    packed.x = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    packed.y = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+    *reinterpret_cast<uint2*>(o.codes + row * o.ldc + at) = make_uint2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[2], two[3], 0x5410));
+    if (o.x != nullptr) st16(o.x + row * o.ldx + at, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// Writes eight values from column `at` of a row: y = p * over.
-__device__ __forceinline__ void q8_store(const Q8Out& o, int64_t row, int at, const float (&p)[8], float top, float inv, float scale,
-                                         float over) {
-    float c[8];
-    uint2 packed = make_uint2(0u, 0u);
-    if (inv != 0.f) q8_codes(p, top, inv, c, packed);
-    else
+// The row's constants from its largest magnitude `top`, where y = p over back.  A row that is not
+// finite stands for NaN: codes of zero, which p of zero gives.
+template <int V>
+__device__ __forceinline__ Q8Row q8_row(uint64_t (&p)[V][4], float top, float over, float back, bool finite) {
+    Q8Row r;
+    r.top = top;
+    r.inv = top != 0.f ? 127.f * rcp_approx(top) : 0.f;
+    r.scale = top * over * (1.f / 127.f) * back;
+    r.over = over * back;
+    if (!finite) {
+        r.top = 1.f;
+        r.inv = 0.f;
+        r.scale = r.over = __uint_as_float(0x7FC00000u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = 0.f;
-    *reinterpret_cast<uint2*>(o.codes + row * o.ldc + at) = packed;
-    if (o.x == nullptr) return;
-    uint32_t w[4];
+        for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = o.full ? pack2(p[2 * i] * over, p[2 * i + 1] * over) : pack2(c[2 * i] * scale, c[2 * i + 1] * scale);
-    st16(o.x + row * o.ldx + at, make_uint4(w[0], w[1], w[2], w[3]));
+            for (int i = 0; i < 4; ++i) p[j][i] = 0;
+    }
+    return r;
 }
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ...; thread i holds the eight values from columns
@@ -116,119 +151,130 @@ __global__ void __launch_bounds__(1024) q8_norm_kernel(const __grid_constant__ Q
     __shared__ float red_ss[3][32];
     const int tid = threadIdx.x;
     const bool add = q.residual != nullptr;
-    uint4 xn[V], rn[V];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int at = 8 * (tid + j * blockDim.x);
-            xn[j] = rn[j] = make_uint4(0, 0, 0, 0);
-            if (at < q.d && row < q.T) {
-                xn[j] = ld16(q.x + row * q.ldx + at);
-                if (add) rn[j] = ld16(q.residual + row * q.ldr + at);
-            }
+    uint4 xn[V], rn[V], gw = make_uint4(0, 0, 0, 0);
+    auto fetch = [&](int64_t row, int j) {
+        const int at = 8 * (tid + j * blockDim.x);
+        xn[j] = rn[j] = make_uint4(0, 0, 0, 0);
+        if (at < q.d && row < q.T) {
+            xn[j] = ld16(q.x + row * q.ldx + at);
+            if (add) rn[j] = ld16(q.residual + row * q.ldr + at);
         }
     };
-    uint4 gw[V];
+    auto fetch_row = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) fetch(row, j);
+    };
+    if (PRE) fetch_row(blockIdx.x);
+    float bad = 0.f;                                        // NaN where a weight is not finite
+    // eight weights: kept where there are no more, else from the first-level cache
+    auto weights = [&](int j) {
+        const int at = 8 * (tid + j * blockDim.x);
+        return V == 1 ? gw : at < q.d ? ld16(q.weight + at) : make_uint4(0, 0, 0, 0);
+    };
+    if (V == 1 && 8 * tid < q.d) gw = ld16(q.weight + 8 * tid);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int at = 8 * (tid + j * blockDim.x);
-        gw[j] = at < q.d ? ld16(q.weight + at) : make_uint4(0, 0, 0, 0);
+        float g[8];
+        unpack8(weights(j), g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) bad = fmaf(g[i], 0.f, bad);
     }
-    fetch(blockIdx.x);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < q.T; row += gridDim.x, turn ^= 1) {
-        float p[V][8];
-        uint32_t top = 0;
-        float ss = 0.f;
+        uint64_t p[V][4], squares = pack2f(bad, 0.f);
+        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int at = 8 * (tid + j * blockDim.x);
-            float h[8], g[8];
-            unpack8(xn[j], h);
+            if (!PRE) fetch(row, j);
+            const uint4 gj = weights(j);
+            uint32_t w[4] = {xn[j].x, xn[j].y, xn[j].z, xn[j].w};
+            const uint32_t r[4] = {rn[j].x, rn[j].y, rn[j].z, rn[j].w}, g[4] = {gj.x, gj.y, gj.z, gj.w};
             if (add) {
-                float r[8];
-                unpack8(rn[j], r);
-                uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // the sum is held in bf16, and the norm is that of what is held
-                    w[i] = pack2(h[2 * i] + r[2 * i], h[2 * i + 1] + r[2 * i + 1]);
-                    h[2 * i] = bf16lo(w[i]);
-                    h[2 * i + 1] = bf16hi(w[i]);
-                }
+                for (int i = 0; i < 4; ++i) w[i] = add_pairs(w[i], r[i]);
                 if (q.sum && at < q.d) st16(q.sum + row * q.lds + at, make_uint4(w[0], w[1], w[2], w[3]));
             }
-            unpack8(gw[j], g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[j][i] = h[i] * g[i];
-                ss = fmaf(h[i], h[i], ss);
-                top = max(top, __float_as_uint(fabsf(p[j][i])));
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t h = pair_of(w[i]);
+                p[j][i] = mul2(h, pair_of(g[i]));
+                squares = fma2(h, h, squares);
+                top = max_pair(p[j][i], top);
             }
         }
-        if (PRE) fetch(row + gridDim.x);
+        if (PRE) fetch_row(row + gridDim.x);
+        float ss, odd;
+        unpack2f(squares, ss, odd);
+        ss += odd;
         q8_reduce(top, ss, red_top[turn], red_ss[turn]);
-        float over = 1.f / sqrtf(ss / (float)q.d + q.eps), back = 1.f;
-        const bool large = __float_as_uint(ss) == kInfBits;
-        if (large || (top != 0 && __uint_as_float(top) < kQ8Small)) {
-            // squares past fp32's range, or products near its other end: once more by a power of two
-            const float by_h = large ? 0x1p-80f : 0x1p32f, by_w = large ? 1.f : 0x1p32f;
-            ss = 0.f;
-            top = 0;
+        float over = rsqrtf(fmaf(ss, q.by_d, q.eps)), back = 1.f;
+        const bool large = !(ss < 0x1p125f);
+        if (large || top > kQ8Large || (top != 0.f && top < kQ8Small)) {
+            // squares or products near an end of fp32's range: once more by powers of two
+            const float by_h = large ? kQ8Down : top < 1.f ? 0x1p32f : 1.f;
+            const float by_w = large ? 1.f : top < 1.f ? 0x1p32f : kQ8Down;
+            back = large ? 1.f : top < 1.f ? 1.f / kQ8Up : 1.f / kQ8Down;
+            ss = bad;
+            top = 0.f;
             // from h where that is held: x or the residual may have given it their place
             const __nv_bfloat16* from = q.sum ? q.sum + row * q.lds : q.x + row * q.ldx;
-#pragma unroll 1
+#pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int at = 8 * (tid + j * blockDim.x);
                 if (at >= q.d) continue;
-                float h[8], g[8];
-                unpack8(ld16(from + at), h);
+                const uint4 x = ld16(from + at), gj = weights(j);
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t g[4] = {gj.x, gj.y, gj.z, gj.w};
                 if (add && !q.sum) {
-                    float r[8];
-                    unpack8(ld16(q.residual + row * q.ldr + at), r);
+                    const uint4 y = ld16(q.residual + row * q.ldr + at);
+                    const uint32_t r[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = __bfloat162float(__float2bfloat16_rn(h[i] + r[i]));
+                    for (int i = 0; i < 4; ++i) w[i] = add_pairs(w[i], r[i]);
                 }
-                unpack8(ld16(q.weight + at), g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float v = h[i] * by_h, w = v * (g[i] * by_w);
-#pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        if (k == j) p[k][i] = w;
-                    ss = fmaf(v, v, ss);
-                    top = max(top, __float_as_uint(fabsf(w)));
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t h = mul2(pair_of(w[i]), pack2f(by_h, by_h));
+                    p[j][i] = mul2(h, mul2(pair_of(g[i]), pack2f(by_w, by_w)));
+                    float lo, hi;
+                    unpack2f(h, lo, hi);
+                    ss = fmaf(hi, hi, fmaf(lo, lo, ss));
+                    top = max_pair(p[j][i], top);
                 }
             }
             q8_reduce(top, ss, red_top[2], red_ss[2]);
-            if (large) over = 1.f / sqrtf(ss / (float)q.d);     // of values so large that eps is nothing
-            else back = kQ8Small;
+            if (large) over = rsqrtf(ss * q.by_d);          // of values so large that eps is nothing
         }
-        float inv = 0.f, scale = 0.f;
-        const float m = __uint_as_float(top);
-        if (top >= kInfBits) scale = over = __uint_as_float(0x7FC00000u);
-        else if (top != 0) {
-            inv = 127.f / m;
-            scale = m * over / 127.f * back;
-            over *= back;
-        }
-        if (tid == 0) q.out.scales[row] = scale;
+        const Q8Row r = q8_row(p, top, over, back, ss < 0x1p125f && top <= kQ8Large);
+        if (tid == 0) q.out.scales[row] = r.scale;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int at = 8 * (tid + j * blockDim.x);
-            if (at < q.d) q8_store(q.out, row, at, p[j], m, inv, scale, over);
+            if (at < q.d) q8_store(q.out, row, at, p[j], r);
         }
-        if (!PRE) fetch(row + gridDim.x);
     }
 }
 
+// act of a pair.  Every value that is not finite gives one that is not.
 template <int ACT>
-__device__ __forceinline__ float q8_act(float a) {
-    // e^-a to 2^-24 (4 + |a|) of itself; where it passes fp32's range, a e^a is nothing
-    if (ACT == LORA_ACT_SILU) return a * rcp_approx(1.f + exp2_approx(-1.44269504f * a));
-    if (ACT == LORA_ACT_GELU) return 0.5f * a * (1.f + erff(a * 0.70710678f));
-    if (ACT == LORA_ACT_GELU_TANH) return 0.5f * a * (1.f + tanhf(0.79788456f * (a + 0.044715f * a * a * a)));
-    return a;
+__device__ __forceinline__ uint64_t q8_act(uint64_t v) {
+    float a[2];
+    unpack2f(v, a[0], a[1]);
+    if (ACT == LORA_ACT_NONE) {
+        return v;
+    } else if (ACT == LORA_ACT_SILU) {
+        // e^-a to 2^-24 (4 + |a|) of itself; where it passes fp32's range, a e^a is nothing
+        float e[2];
+        unpack2f(mul2(v, pack2f(-1.44269504f, -1.44269504f)), e[0], e[1]);
+        unpack2f(add2(pack2f(exp2_approx(e[0]), exp2_approx(e[1])), pack2f(1.f, 1.f)), e[0], e[1]);
+        return mul2(v, pack2f(rcp_approx(e[0]), rcp_approx(e[1])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            a[i] = 0.5f * a[i] * (1.f + (ACT == LORA_ACT_GELU ? erff(a[i] * 0.70710678f)
+                                                              : tanhf(0.79788456f * (a[i] + 0.044715f * a[i] * a[i] * a[i]))));
+        return pack2f(a[0], a[1]);
+    }
 }
 
 template <int V, int ACT, bool PRE>
@@ -238,61 +284,58 @@ __global__ void __launch_bounds__(1024) q8_gate_kernel(const __grid_constant__ Q
     const int tid = threadIdx.x;
     const bool gated = q.up != nullptr;
     uint4 an[V], un[V];
-    auto fetch = [&](int64_t row) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int at = 8 * (tid + j * blockDim.x);
-            an[j] = un[j] = make_uint4(0, 0, 0, 0);
-            if (at < q.d && row < q.T) {
-                an[j] = ld16(q.gate + row * q.ldg + at);
-                if (gated) un[j] = ld16(q.up + row * q.ldu + at);
-            }
+    auto fetch = [&](int64_t row, int j) {
+        const int at = 8 * (tid + j * blockDim.x);
+        an[j] = un[j] = make_uint4(0, 0, 0, 0);
+        if (at < q.d && row < q.T) {
+            an[j] = ld16(q.gate + row * q.ldg + at);
+            if (gated) un[j] = ld16(q.up + row * q.ldu + at);
         }
     };
-    fetch(blockIdx.x);
+    auto fetch_row = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) fetch(row, j);
+    };
+    if (PRE) fetch_row(blockIdx.x);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < q.T; row += gridDim.x, turn ^= 1) {
-        float p[V][8];
-        uint32_t top = 0;
-        float none = 0.f;
+        uint64_t p[V][4], zeros = 0;                        // zeros: 0 y summed, NaN where a y is not finite
+        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            unpack8(an[j], p[j]);
-            float u[8];
-            unpack8(un[j], u);
+            if (!PRE) fetch(row, j);
+            const uint32_t a[4] = {an[j].x, an[j].y, an[j].z, an[j].w}, u[4] = {un[j].x, un[j].y, un[j].z, un[j].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const bool bad = max(__float_as_uint(fabsf(p[j][i])), __float_as_uint(fabsf(u[i]))) >= kInfBits;
-                p[j][i] = q8_act<ACT>(p[j][i]);
-                if (gated) p[j][i] *= u[i];
-                top = max(top, bad ? 0x7FC00000u : __float_as_uint(fabsf(p[j][i])));
+            for (int i = 0; i < 4; ++i) {
+                p[j][i] = q8_act<ACT>(pair_of(a[i]));
+                if (gated) p[j][i] = mul2(p[j][i], pair_of(u[i]));
+                zeros = fma2(p[j][i], 0, zeros);
+                top = max_pair(p[j][i], top);
             }
         }
-        if (PRE) fetch(row + gridDim.x);
+        if (PRE) fetch_row(row + gridDim.x);
+        float none, odd;
+        unpack2f(zeros, none, odd);
+        none += odd;
         q8_reduce(top, none, red_top[turn], red_ss[turn]);
+        const bool finite = none == 0.f;
         float back = 1.f;
-        if (top != 0 && __uint_as_float(top) < kQ8Small) {  // near fp32's smallest values: by a power of two
-            back = kQ8Small;
-            top = __float_as_uint(__uint_as_float(top) * kQ8Up);
+        if (finite && top != 0.f && (top < kQ8Small || top > kQ8Large)) {   // near an end of fp32's range: by a power of two
+            const float by = top < 1.f ? kQ8Up : kQ8Down;
+            back = 1.f / by;
+            top *= by;
 #pragma unroll
             for (int j = 0; j < V; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[j][i] *= kQ8Up;
+                for (int i = 0; i < 4; ++i) p[j][i] = mul2(p[j][i], pack2f(by, by));
         }
-        float inv = 0.f, scale = 0.f, over = back;
-        const float m = __uint_as_float(top);
-        if (top >= kInfBits) scale = over = __uint_as_float(0x7FC00000u);
-        else if (top != 0) {
-            inv = 127.f / m;
-            scale = m / 127.f * back;
-        }
-        if (tid == 0) q.out.scales[row] = scale;
+        const Q8Row r = q8_row(p, top, 1.f, back, finite);
+        if (tid == 0) q.out.scales[row] = r.scale;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const int at = 8 * (tid + j * blockDim.x);
-            if (at < q.d) q8_store(q.out, row, at, p[j], m, inv, scale, over);
+            if (at < q.d) q8_store(q.out, row, at, p[j], r);
         }
-        if (!PRE) fetch(row + gridDim.x);
     }
 }
 

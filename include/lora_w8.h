@@ -13,8 +13,9 @@
  *
  * A row y of width d in 8 bits:
  *     scale = max |y| / 127,   code_i = rint(y_i / scale)  (ties to even; 0 if scale = 0),
- * and a code c stands for scale * c.  A row that holds a value that is not finite has the
- * scale NaN and codes 0, and so stands for NaN in every product. */
+ * and a code c stands for scale * c.  y and scale are fp32.  A row that holds a value that is
+ * not finite (or whose values leave fp32's range on the way) has the scale NaN and codes 0, and
+ * so stands for NaN in every product. */
 #ifndef LORA_W8_GB300_H
 #define LORA_W8_GB300_H
 
@@ -57,7 +58,7 @@ typedef struct {
     int64_t ldx;
     int64_t ldr;
     int64_t lds;
-    float eps;                   /* 1e-30 or more                                           */
+    float eps;                   /* 1e-30 .. 1                                              */
     int32_t d;                   /* a multiple of 16, at most LORA_Q8_MAX_WIDTH             */
     lora_q8_rows out;
 } lora_q8_norm_desc;
