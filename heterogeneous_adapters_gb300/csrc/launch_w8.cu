@@ -54,14 +54,20 @@ lora_status launch_rows(K kern, const P& q, int v, cudaStream_t s) {
     return cuda_status(cudaGetLastError());
 }
 
-// Eights of a row that a thread holds.
-int row_eights(int32_t d) { return d <= 8192 ? 1 : d <= 16384 ? 2 : 4; }
-
+// Eights of a row that a thread holds, by measured times: a norm's weights fit beside one of them and
+// the next row (8,191 rows of 4096: 49 us, 59 with two), above that several CTAs an SM with four each
+// and nothing ahead are better (8,000 of 5120: 70 with one, 76 with two, 65; 2,000 of 14336: 67 with
+// two, 50).  An activation has no weights: two and the next row (2,339 gated of 14336 39, 50 with
+// four; 8,000 of 4096 without a gate 29, 36 with one), for narrow rows one.
 template <int ACT>
 lora_status launch_gate(const Q8GateParams& q, cudaStream_t s) {
-    const int v = row_eights(q.d);
-    if (v == 1) return launch_rows(q8_gate_kernel<1, ACT, true>, q, v, s);
-    return v == 2 ? launch_rows(q8_gate_kernel<2, ACT, true>, q, v, s) : launch_rows(q8_gate_kernel<4, ACT, false>, q, v, s);
+    if (q.d <= 2048) return launch_rows(q8_gate_kernel<1, ACT, true>, q, 1, s);
+    if (q.d <= 16384) return launch_rows(q8_gate_kernel<2, ACT, true>, q, 2, s);
+    return launch_rows(q8_gate_kernel<4, ACT, false>, q, 4, s);
+}
+lora_status launch_norm(const Q8NormParams& q, cudaStream_t s) {
+    if (q.d <= 4096) return launch_rows(q8_norm_kernel<1, true>, q, 1, s);
+    return launch_rows(q8_norm_kernel<4, false>, q, 4, s);
 }
 
 // ---------------------------------------------------------------------------- products
@@ -280,10 +286,7 @@ lora_status lora_q8_norm(const lora_q8_norm_desc* n, int32_t T, void* stream) {
     const Q8NormParams q = {reinterpret_cast<const __nv_bfloat16*>(n->x), reinterpret_cast<const __nv_bfloat16*>(n->residual),
                             reinterpret_cast<__nv_bfloat16*>(n->sum), reinterpret_cast<const __nv_bfloat16*>(n->weight),
                             n->ldx, n->ldr, n->lds, n->eps, 1.f / (float)n->d, n->d, T, out_of(n->out)};
-    const int v = row_eights(n->d);
-    cudaStream_t s = (cudaStream_t)stream;
-    if (v == 1) return launch_rows(q8_norm_kernel<1, true>, q, v, s);
-    return v == 2 ? launch_rows(q8_norm_kernel<2, true>, q, v, s) : launch_rows(q8_norm_kernel<4, false>, q, v, s);
+    return launch_norm(q, (cudaStream_t)stream);
 }
 
 lora_status lora_q8_gate(const lora_q8_gate_desc* n, int32_t T, void* stream) {
