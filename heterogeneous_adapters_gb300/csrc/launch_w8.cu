@@ -258,7 +258,9 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
         if (total > INT32_MAX) return LORA_ETOOBIG;
     }
     w.total = (int32_t)total;
-    const int64_t blocks = std::min<int64_t>((most + kWidenThreads - 1) / kWidenThreads, 2048);
+    DeviceInfo* di = nullptr;
+    if ((st = device_info(&di)) != LORA_OK) return st;
+    const int64_t blocks = std::min<int64_t>((most + kWidenThreads - 1) / kWidenThreads, std::max(di->sm_count * 8 / copies, 1));
     w8_widen_kernel<<<dim3((unsigned)blocks, (unsigned)copies), kWidenThreads, 0, s>>>(v);
     st = cuda_status(cudaGetLastError());
     if (st != LORA_OK) return st;

@@ -29,8 +29,11 @@ constexpr int kW8MaxPairs = 96;
 constexpr int kW8Bufs = 4;                     // A buffers in tensor memory and stages of x
 constexpr int kW8WBytes = 128 * kW8WideK;
 
-// By the most columns (rows of x) of a tile: stages of W, as many as fit beside x.
-__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 5 : n > 64 ? 9 : 11; }
+// By the most columns (rows of x) of a tile: stages of W, as many as fit beside x, an even number.
+__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 6 : n > 64 ? 8 : 12; }
+// Steps of W that are fetched together.  A step is 128 bytes of each row, and memory answers better to
+// four in a row: 5.8 TB/s, one by one 5.3 (478 MB, in a kernel that does nothing else).
+__host__ __device__ constexpr int w8_w_group(int n) { return n > 128 ? 2 : 4; }
 __host__ __device__ constexpr size_t w8_wide_smem(int n) {
     return 1024 + (size_t)w8_w_stages(n) * kW8WBytes + (size_t)kW8Bufs * n * 128;
 }
@@ -73,24 +76,33 @@ struct W8Widen {
     int32_t K[LORA_W8_MAX_PROBLEMS];
     int32_t T;
 };
-constexpr int kWidenThreads = 256;
+constexpr int kWidenThreads = 256, kWidenAhead = 4;
 
-// Sixteen codes a thread; blockIdx.y: the matrix.
-__global__ void __launch_bounds__(kWidenThreads) w8_widen_kernel(const __grid_constant__ W8Widen p) {
+// Sixteen codes a thread and time, four times in flight; blockIdx.y: the matrix.  At most one CTA of
+// these for each that an SM holds: the next kernel begins when all have begun.
+__global__ void __launch_bounds__(kWidenThreads, 8) w8_widen_kernel(const __grid_constant__ W8Widen p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int i = blockIdx.y, K = p.K[i];
-    const int64_t n = (int64_t)p.T * (K / 16);
-    for (int64_t e = (int64_t)blockIdx.x * kWidenThreads + threadIdx.x; e < n; e += (int64_t)gridDim.x * kWidenThreads) {
-        const int64_t row = e / (K / 16), c = e - row * (K / 16);
-        const uint4 v = ld16(p.x[i] + row * p.ldx[i] + c * 16);
-        uint4 a, b;
-        codes8_f16(v.x, a.x, a.y);
-        codes8_f16(v.y, a.z, a.w);
-        codes8_f16(v.z, b.x, b.y);
-        codes8_f16(v.w, b.z, b.w);
-        uint32_t* to = p.out[i] + (row * K + c * 16) / 2;
-        st16(to, a);
-        st16(to + 4, b);
+    const int i = blockIdx.y;
+    const uint32_t per_row = p.K[i] / 16, n = p.T * per_row, step = gridDim.x * kWidenThreads;   // n < 2^28
+    for (uint32_t e = blockIdx.x * kWidenThreads + threadIdx.x; e < n; e += kWidenAhead * step) {
+        uint4 v[kWidenAhead];
+#pragma unroll
+        for (int k = 0; k < kWidenAhead; ++k) {
+            const uint32_t at = min(e + k * step, n - 1), row = at / per_row;
+            v[k] = ld16(p.x[i] + row * p.ldx[i] + (at - row * per_row) * 16);
+        }
+#pragma unroll
+        for (int k = 0; k < kWidenAhead; ++k) {
+            if (e + k * step >= n) break;
+            uint4 a, b;
+            codes8_f16(v[k].x, a.x, a.y);
+            codes8_f16(v[k].y, a.z, a.w);
+            codes8_f16(v[k].z, b.x, b.y);
+            codes8_f16(v[k].w, b.z, b.w);
+            uint32_t* to = p.out[i] + (int64_t)(e + k * step) * 8;       // rows lie end to end
+            st16(to, a);
+            st16(to + 4, b);
+        }
     }
 }
 
@@ -175,21 +187,6 @@ __device__ __forceinline__ void w8_next(const W8WideParams& p, W8At& a) {
     ++a.prob;
 }
 
-// What joining a tile's parts needs of it.
-struct W8Join {
-    const float4* part;        // the thread's row of the first pair's part in slot 0; a pair's two slots are
-    int64_t slot;              // `slot` float4 apart, pairs 4 `slot`
-    int32_t p0, p1;            // its pairs: the first one's part is in slot 1, the others' in slot 0
-    int32_t own;               // the pair whose part is in tensor memory, or -1
-    uint32_t dcol;
-    int32_t chunks;            // of 16 columns
-    const float* sx;           // shared memory
-    float sw;
-    __nv_bfloat16* to;         // y at the lane's first column and pair of rows
-    int64_t two;               // two columns of y
-    int32_t left;              // columns from the lane's first
-};
-
 // Sixteen columns' sums as bf16 pairs of y.
 __device__ __forceinline__ void w8_scale(const float (&v)[16], const float* sx, float sw, uint32_t* to) {
 #pragma unroll
@@ -212,41 +209,29 @@ __device__ __forceinline__ void w8_store(const uint32_t* from, __nv_bfloat16*& t
     }
 }
 
-// A tile's sums over all parts, in the order of K, 32 columns at a time.
-__device__ __forceinline__ void w8_join(W8Join j) {
-    for (int c = 0; c < j.chunks; c += 2) {
-        const bool both = c + 1 < j.chunks;
-        float sum[2][16];
+// Adds parts 0 .. n - 1 of sixteen columns of a row, `stride` apart, in their order, SOME at a time:
+// what is in flight counts, an answer takes 800 clocks, or 1,500 from the other die.
+template <int SOME>
+__device__ __forceinline__ void w8_add_parts(float (&sum)[16], const float4* from, int64_t stride, int n) {
+    for (int q = 0; q < n; q += SOME) {
+        float4 x[SOME][4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sum[i / 16][i % 16] = 0.f;
-        for (int q = j.p0; q <= j.p1; ++q) {
-            float x[2][16];
-            if (q == j.own) {
-                tmem_ld16(j.dcol + c * 16, x[0]);
-                tmem_ld16(j.dcol + (both ? c + 1 : c) * 16, x[1]);
-                tmem_ld_wait16(x[0]);
-                tmem_ld_wait16(x[1]);
-            } else {
-                const float4* from = j.part + (4 * (int64_t)(q - j.p0) + (q == j.p0)) * j.slot + c * 512;
+        for (int k = 0; k < SOME; ++k) {
+            const float4* at = from + min(q + k, n - 1) * stride;      // past the last: the last again
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 f = __ldcg(from + (i < 4 || both ? i : i - 4) * 128);
-                    x[i / 4][i % 4 * 4] = f.x;
-                    x[i / 4][i % 4 * 4 + 1] = f.y;
-                    x[i / 4][i % 4 * 4 + 2] = f.z;
-                    x[i / 4][i % 4 * 4 + 3] = f.w;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sum[i / 16][i % 16] += x[i / 16][i % 16];
+            for (int i = 0; i < 4; ++i) x[k][i] = __ldcg(at + i * 128);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (i == 0 || both) {
-                uint32_t out[8];
-                w8_scale(sum[i], j.sx + (c + i) * 16, j.sw, out);
-                w8_store(out, j.to, j.two, j.left);
+        for (int k = 0; k < SOME; ++k) {
+            const bool in = q + k < n;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum[4 * i] += in ? x[k][i].x : 0.f;
+                sum[4 * i + 1] += in ? x[k][i].y : 0.f;
+                sum[4 * i + 2] += in ? x[k][i].z : 0.f;
+                sum[4 * i + 3] += in ? x[k][i].w : 0.f;
             }
+        }
     }
 }
 
@@ -254,12 +239,16 @@ __device__ __forceinline__ void w8_join(W8Join j) {
 // (the code for that takes registers from the path of whole tiles).
 template <int NMAX, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w8_wide_kernel(const __grid_constant__ W8WideParams p) {
-    constexpr int kWStages = w8_w_stages(NMAX), kXStage = NMAX * 128;
+    constexpr int kWStages = w8_w_stages(NMAX), kWGroup = w8_w_group(NMAX), kXStage = NMAX * 128;
     // Registers move from the warps that issue and widen to those that hold a row's sums: the shares of
     // the five groups of four warps add up to the 480 of the launch.  (A few spilled registers in the
     // path of whole tiles cost as much as the path itself.)
     constexpr int kRegsOut = NMAX > 128 ? 160 : 136, kRegsWiden = NMAX > 128 ? 56 : 80, kRegsMisc = 48;
     static_assert(kRegsMisc + 2 * kRegsWiden + 2 * kRegsOut <= 480, "registers of the launch");
+    // A wait for a barrier's phase must not fall two phases behind.  The two groups of widening warps take
+    // the steps in turn, so each stage and buffer has to belong to one of them: with an odd number, a
+    // group may come to a stage whose last step the other one has not even seen arrive.
+    static_assert(kWStages % 2 == 0 && kW8Bufs % 2 == 0 && kWStages % kWGroup == 0, "stages of one group each");
     constexpr uint32_t kACol = 256;            // D in columns 0 .. 255, four A buffers of 64 columns after it
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full, d_empty, final_bar;
@@ -293,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    cluster_sync();
+    cluster_sync();                                            // nothing is fetched before: W's loads delay all others
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
     bool ok = true;
@@ -307,11 +296,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         if (lane == 0) {
             W8At a = w8_at(p, first);
             uint32_t i = 0;
-            for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
-                const uint32_t s = i % kWStages;
-                if (!mbar_wait_quiet(bar(w_empty[s]), ((i / kWStages) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
-                mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);
-                tma_load_2d(w0 + s * kW8WBytes, &p.w[a.prob], a.kb * kW8WideK, a.rt * kW8WideRows + (int)rank * 128, bar(w_full[s]));
+            const uint32_t steps = end - first;
+            while (i < steps) {
+                const uint32_t n = min(steps, i + kWGroup);
+                for (uint32_t k = i; k < n && ok; ++k)
+                    ok = mbar_wait_quiet(bar(w_empty[k % kWStages]), ((k / kWStages) & 1) ^ 1, p.limit_ns);
+                if (!ok) break;
+                for (; i < n; ++i, w8_next(p, a)) {
+                    const uint32_t s = i % kWStages;
+                    mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);
+                    tma_load_2d(w0 + s * kW8WBytes, &p.w[a.prob], a.kb * kW8WideK, a.rt * kW8WideRows + (int)rank * 128, bar(w_full[s]));
+                }
             }
             if (!ok) set_error(p.err, LORA_DERR_TIMEOUT);
             // every copy has landed before the CTA can end
@@ -420,6 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         // ------------------------------------------------------------------ sums out: a row of W, half of the columns
         regs_inc<kRegsOut>();
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
+        constexpr int kChunks = NMAX / 32;
         const uint32_t dcol = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
         const int chunks = half_cols / 16;
         auto meet = [&]() { named_bar_sync(1 + half, 128); };
@@ -451,9 +447,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 if (ok) {
                     tmem_ld16(dcol, v[0]);
 #pragma unroll
-                    for (int c = 0; c < NMAX / 32; ++c) {      // columns past the tile's are read for nothing
+                    for (int c = 0; c < kChunks; ++c) {         // columns past the tile's are read for nothing
                         tmem_ld_wait16(v[c & 1]);
-                        if (c + 1 < NMAX / 32) tmem_ld16(dcol + (c + 1) * 16, v[(c + 1) & 1]);
+                        if (c + 1 < kChunks) tmem_ld16(dcol + (c + 1) * 16, v[(c + 1) & 1]);
                         take(c, v[c & 1]);
                     }
                 }
@@ -462,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
             };
             if (whole) {
-                uint32_t out[NMAX / 4];
+                uint32_t out[8 * kChunks];
                 drain([&](int c, const float (&v)[16]) { w8_scale(v, &sx[half][c * 16], sw, out + c * 8); });
                 if (ok) {
                     int left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
@@ -470,40 +466,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                     __nv_bfloat16* to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
                     asm volatile("" : "+l"(two), "+l"(to), "+r"(left));   // not before the sums are out: registers
 #pragma unroll
-                    for (int c = 0; c < NMAX / 32; ++c)
+                    for (int c = 0; c < kChunks; ++c)
                         if (c < chunks) w8_store(out + c * 8, to, two, left);
                 }
             } else {
                 const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per;
                 uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
-                auto join = [&](int own) {
-                    W8Join j;
-                    j.part = part_of((int64_t)p0 * 2 + rank, 0);
-                    j.slot = w8_part_floats(NMAX) / 4;
-                    j.p0 = p0;
-                    j.p1 = p1;
-                    j.own = own;
-                    j.dcol = dcol;
-                    j.chunks = chunks;
-                    j.sx = sx[half];
-                    j.sw = sw;
-                    j.to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
-                    j.two = 2 * pr.ldy;
-                    j.left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
-                    w8_join(j);
+                // the sum over all parts, in the order of K; `mine`: the first one is in tensor memory
+                auto join = [&](bool mine) {
+                    constexpr int64_t kSlot = w8_part_floats(NMAX) / 4;    // the first pair's part is in the second of
+                    const float4* from = part_of((int64_t)p0 * 2 + rank, 0);   // its two slots, the others' in their first
+                    int left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
+                    const int64_t two = 2 * pr.ldy;
+                    __nv_bfloat16* to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
+                    for (int c = 0; c < chunks; ++c, from += 512) {
+                        float sum[16];
+                        if (mine) {
+                            tmem_ld16(dcol + c * 16, sum);
+                            tmem_ld_wait16(sum);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+                            w8_add_parts<1>(sum, from + kSlot, 0, 1);
+                        }
+                        w8_add_parts<(NMAX > 128 ? 2 : 4)>(sum, from + 4 * kSlot, 4 * kSlot, p1 - p0);
+                        uint32_t out[8];
+                        w8_scale(sum, &sx[half][c * 16], sw, out);
+                        w8_store(out, to, two, left);
+                    }
                 };
                 // Where all other parts are there already (a pair comes to the tile that it begins last, when
                 // the next pair has long done its rest), this one stays where it is.
                 if (g == 0) {
-                    uint32_t there;
-                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
+                    uint32_t there = 0;
+                    if (pair == p0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
                     last_in[half] = there == (uint32_t)(p1 - p0);
                 }
                 meet();
                 const bool early = *reinterpret_cast<volatile uint32_t*>(&last_in[half]) && ok;
                 if (early) {
                     __threadfence();
-                    join(pair);
+                    join(true);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
@@ -521,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                     if (*reinterpret_cast<volatile uint32_t*>(&last_in[half])) {
                         __threadfence();
                         if (g == 0) *ticket = 0;
-                        join(-1);
+                        join(false);
                     }
                 }
                 meet();

@@ -273,3 +273,19 @@ def test_no_rows(cuda):
     lora.q8_norm(lora.Q8Norm(x, 64, None, 0, None, 0, x, 1e-5, 64, out.rows), 0, stream(cuda))
     lora.q8_gate(lora.Q8Gate(x, 64, None, 0, lora.LORA_ACT_NONE, 64, out.rows), 0, stream(cuda))
     assert out.untouched()
+
+
+def test_in_place_with_more_rows_than_the_device_holds(cuda):
+    """A CTA's next row is fetched before the one before it is written."""
+    g = cuda.Generator(device="cuda").manual_seed(6)
+    for T, d in ((3001, 64), (1203, 4096), (701, 4112)):
+        x, r = matrix(cuda, g, T, d), matrix(cuda, g, T, d)
+        w = (1 + 0.2 * cuda.randn(d, generator=g, device="cuda")).bfloat16()
+        codes, scales, xo, total = run_norm(cuda, x, r, w)
+        out = Out(cuda, T, d)
+        lora.q8_norm(lora.Q8Norm(x, d, r, d, x, d, w, 1e-5, d, out.rows), T, stream(cuda))
+        assert cuda.equal(x, total) and all(cuda.equal(p, q) for p, q in zip(out.got(), (codes, scales, xo)))
+        want = run_gate(cuda, x, r, "silu")
+        rows = lora.Q8Rows(out.codes, out.codes.stride(0), out.scales, r, d)
+        lora.q8_gate(lora.Q8Gate(x, d, r, d, lora.LORA_ACT_SILU, d, rows), T, stream(cuda))
+        assert cuda.equal(out.codes[:T], want[0]) and cuda.equal(out.scales[:T], want[1]) and cuda.equal(r, want[2])
