@@ -26,14 +26,12 @@ constexpr int kW8WideRows = 256;               // rows of W of a tile: 128 a CTA
 constexpr int kW8WideK = 128;                  // K of a step
 constexpr int kW8WideThreads = 640;
 constexpr int kW8MaxPairs = 96;
-constexpr int kW8Bufs = 4;                     // A buffers in tensor memory and stages of x
 constexpr int kW8WBytes = 128 * kW8WideK;
 
-// By the most columns (rows of x) of a tile: stages of W, as many as fit beside x, an even number.
-__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 6 : n > 64 ? 8 : 12; }
-// Steps of W that are fetched together.  A step is 128 bytes of each row, and memory answers better to
-// four in a row: 5.8 TB/s, one by one 5.3 (478 MB, in a kernel that does nothing else).
-__host__ __device__ constexpr int w8_w_group(int n) { return n > 128 ? 2 : 4; }
+constexpr int kW8Bufs = 4;                     // A buffers in tensor memory and stages of x
+// By the most columns (rows of x) of a tile: stages of W, an even number.  64 rows of two 14336 x 4096
+// take 28 us with 6, 8 or 12 of them and 31 with 4.
+__host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 6 : 8; }
 __host__ __device__ constexpr size_t w8_wide_smem(int n) {
     return 1024 + (size_t)w8_w_stages(n) * kW8WBytes + (size_t)kW8Bufs * n * 128;
 }
@@ -209,15 +207,17 @@ __device__ __forceinline__ void w8_store(const uint32_t* from, __nv_bfloat16*& t
     }
 }
 
-// Adds parts 0 .. n - 1 of sixteen columns of a row, `stride` apart, in their order, SOME at a time:
-// what is in flight counts, an answer takes 800 clocks, or 1,500 from the other die.
+// Adds parts q .. n - 1 of sixteen columns of a row in their order, SOME at a time: what is in flight
+// counts, an answer takes 800 clocks, or 1,500 from the other die.  The first pair's part is in the
+// second of its two slots, the others' in their first.
 template <int SOME>
-__device__ __forceinline__ void w8_add_parts(float (&sum)[16], const float4* from, int64_t stride, int n) {
-    for (int q = 0; q < n; q += SOME) {
+__device__ __forceinline__ void w8_add_parts(float (&sum)[16], const float4* first, int64_t slot, int q, int n) {
+    for (; q < n; q += SOME) {
         float4 x[SOME][4];
 #pragma unroll
         for (int k = 0; k < SOME; ++k) {
-            const float4* at = from + min(q + k, n - 1) * stride;      // past the last: the last again
+            const int j = min(q + k, n - 1);                   // past the last: the last again
+            const float4* at = first + (j ? 4 * j : 1) * slot;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[k][i] = __ldcg(at + i * 128);
         }
@@ -239,7 +239,7 @@ __device__ __forceinline__ void w8_add_parts(float (&sum)[16], const float4* fro
 // (the code for that takes registers from the path of whole tiles).
 template <int NMAX, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w8_wide_kernel(const __grid_constant__ W8WideParams p) {
-    constexpr int kWStages = w8_w_stages(NMAX), kWGroup = w8_w_group(NMAX), kXStage = NMAX * 128;
+    constexpr int kWStages = w8_w_stages(NMAX), kXStage = NMAX * 128;
     // Registers move from the warps that issue and widen to those that hold a row's sums: the shares of
     // the five groups of four warps add up to the 480 of the launch.  (A few spilled registers in the
     // path of whole tiles cost as much as the path itself.)
@@ -248,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     // A wait for a barrier's phase must not fall two phases behind.  The two groups of widening warps take
     // the steps in turn, so each stage and buffer has to belong to one of them: with an odd number, a
     // group may come to a stage whose last step the other one has not even seen arrive.
-    static_assert(kWStages % 2 == 0 && kW8Bufs % 2 == 0 && kWStages % kWGroup == 0, "stages of one group each");
+    static_assert(kWStages % 2 == 0 && kW8Bufs % 2 == 0, "stages of one group each");
     constexpr uint32_t kACol = 256;            // D in columns 0 .. 255, four A buffers of 64 columns after it
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full, d_empty, final_bar;
@@ -262,15 +262,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     const int first = min(pair * p.per, p.total), end = min(first + p.per, p.total);
     const int half_cols = p.cols / 2;
     auto bar = [](uint64_t& b) { return smem_addr(&b); };
-    if (tid == 0) {
-        for (int i = 0; i < kWStages; ++i) {
-            mbar_init(bar(w_full[i]), 1);
-            mbar_init(bar(w_empty[i]), 4);
-        }
-        for (int i = 0; i < kW8Bufs; ++i) {
-            mbar_init(bar(ready[i]), 1 + 8);           // of the even CTA: x's bytes in both, and both CTAs' four widening warps
-            mbar_init(bar(freed[i]), 1);
-        }
+    if (tid < kWStages) {
+        mbar_init(bar(w_full[tid]), 1);
+        mbar_init(bar(w_empty[tid]), 4);
+        fence_mbar_init();
+    } else if (tid >= 32 && tid < 32 + kW8Bufs) {
+        mbar_init(bar(ready[tid - 32]), 1 + 8);        // of the even CTA: x's bytes in both, and both CTAs' four widening warps
+        mbar_init(bar(freed[tid - 32]), 1);
+        fence_mbar_init();
+    } else if (tid == 64) {
         mbar_init(bar(d_full), 1);
         mbar_init(bar(d_empty), 16);
         mbar_init(bar(final_bar), 1);
@@ -296,17 +296,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         if (lane == 0) {
             W8At a = w8_at(p, first);
             uint32_t i = 0;
-            const uint32_t steps = end - first;
-            while (i < steps) {
-                const uint32_t n = min(steps, i + kWGroup);
-                for (uint32_t k = i; k < n && ok; ++k)
-                    ok = mbar_wait_quiet(bar(w_empty[k % kWStages]), ((k / kWStages) & 1) ^ 1, p.limit_ns);
-                if (!ok) break;
-                for (; i < n; ++i, w8_next(p, a)) {
-                    const uint32_t s = i % kWStages;
-                    mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);
-                    tma_load_2d(w0 + s * kW8WBytes, &p.w[a.prob], a.kb * kW8WideK, a.rt * kW8WideRows + (int)rank * 128, bar(w_full[s]));
-                }
+            for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
+                const uint32_t s = i % kWStages;
+                if (!mbar_wait_quiet(bar(w_empty[s]), ((i / kWStages) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
+                mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);
+                tma_load_2d(w0 + s * kW8WBytes, &p.w[a.prob], a.kb * kW8WideK, a.rt * kW8WideRows + (int)rank * 128, bar(w_full[s]));
             }
             if (!ok) set_error(p.err, LORA_DERR_TIMEOUT);
             // every copy has landed before the CTA can end
@@ -474,8 +468,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
                 // the sum over all parts, in the order of K; `mine`: the first one is in tensor memory
                 auto join = [&](bool mine) {
-                    constexpr int64_t kSlot = w8_part_floats(NMAX) / 4;    // the first pair's part is in the second of
-                    const float4* from = part_of((int64_t)p0 * 2 + rank, 0);   // its two slots, the others' in their first
+                    constexpr int64_t kSlot = w8_part_floats(NMAX) / 4;
+                    constexpr int kSome = NMAX > 128 ? 3 : NMAX > 64 ? 4 : 6;
+                    const float4* from = part_of((int64_t)p0 * 2 + rank, 0);
                     int left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
                     const int64_t two = 2 * pr.ldy;
                     __nv_bfloat16* to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
@@ -487,9 +482,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                         } else {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) sum[i] = 0.f;
-                            w8_add_parts<1>(sum, from + kSlot, 0, 1);
                         }
-                        w8_add_parts<(NMAX > 128 ? 2 : 4)>(sum, from + 4 * kSlot, 4 * kSlot, p1 - p0);
+                        w8_add_parts<kSome>(sum, from, kSlot, mine, p1 - p0 + 1);
                         uint32_t out[8];
                         w8_scale(sum, &sx[half][c * 16], sw, out);
                         w8_store(out, to, two, left);
