@@ -82,8 +82,19 @@ lora_status check_sizes(const lora_w8_problem* probs, int32_t nprob, int32_t T) 
     return LORA_OK;
 }
 
-// Rows up to which w8_narrow.cuh serves.
-constexpr int kW8NarrowRows = 32;
+// Rows and bytes of W up to which w8_narrow.cuh serves: it begins 5 us earlier than w8_wide.cuh, but
+// widens x once per 16 rows of W.  16 rows, narrow and wide: q, k, v of 25 MB 9.3 and 14.8 us, 59 MB 21.6
+// and 22.9, 79 MB 21.5 and 20.7, 117 MB 29 and 27.4; 32 rows: 17 MB 9.1 and 12.9, 25 MB 15.5 and 15.2,
+// 79 MB 36 and 21; 8 rows of 117 MB 23 and 28.
+constexpr int64_t kW8Narrow16 = 64 << 20, kW8Narrow32 = 24 << 20;
+bool narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
+    if (T <= 8) return true;
+    if (T > 32) return false;
+    int64_t bytes = 0;
+    for (int32_t i = 0; i < nprob; ++i) bytes += (int64_t)probs[i].N * probs[i].K;
+    return bytes <= (T <= 16 ? kW8Narrow16 : kW8Narrow32);
+}
+
 // Steps that joining a tile from several pairs costs.
 constexpr int kW8JoinCost = 8;
 
@@ -110,7 +121,7 @@ int32_t x_of(const lora_w8_problem* probs, int32_t i) {
 size_t x_bytes(const lora_w8_problem& p, int32_t T) { return align256((size_t)T * p.K * 2); }
 
 size_t workspace_bytes(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
-    if (T <= kW8NarrowRows) return align256(kStepPartAt);
+    if (narrow(probs, nprob, T)) return align256(kStepPartAt);
     size_t n = align256(kStepPartAt) + w8_part_bytes(wide_shape(T).nmax);
     for (int32_t i = 0; i < nprob; ++i)
         if (x_of(probs, i) == i) n += x_bytes(probs[i], T);
@@ -334,7 +345,7 @@ lora_status lora_w8_matmul(const lora_w8_problem* probs, int32_t nprob, int32_t 
     if (nprob == 0 || T == 0) return LORA_OK;
     if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes(probs, nprob, T)) return LORA_EWORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
-    return T <= kW8NarrowRows ? run_narrow(probs, nprob, T, s) : run_wide(probs, nprob, T, ws, s);
+    return narrow(probs, nprob, T) ? run_narrow(probs, nprob, T, s) : run_wide(probs, nprob, T, ws, s);
 }
 
 }  // extern "C"

@@ -43,9 +43,10 @@ __device__ __forceinline__ void codes8_f16(uint32_t w, uint32_t& lo, uint32_t& h
 }
 
 // By the column tiles: steps of a group, whose loads are on their way while the group before is
-// multiplied, and CTAs that an SM should hold.
-__host__ __device__ constexpr int w8_group(int nt) { return nt == 1 ? 4 : 2; }
-__host__ __device__ constexpr int w8_ctas(int nt) { return nt == 2 ? 3 : nt == 1 ? 2 : 1; }
+// multiplied, and CTAs that an SM should hold (8 rows of two 14336 x 4096: groups of two and three
+// CTAs 23 us, four and two 27; 13 rows of q, k, v: one and four 9.2, two and two 9.8, four and one 10.9).
+__host__ __device__ constexpr int w8_group(int nt) { return nt == 1 ? 2 : 1; }
+__host__ __device__ constexpr int w8_ctas(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 2; }
 
 // Lane (g, t) = (lane / 4, lane % 4) takes the 16 bytes from k = 16 t of its row's 64: word j of
 // them are the two pairs that an MMA of 16 of K wants of the lane, for W and for x alike, so
