@@ -95,8 +95,10 @@ bool narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
     return bytes <= (T <= 16 ? kW8Narrow16 : kW8Narrow32);
 }
 
-// Steps that joining a tile from several pairs costs.
-constexpr int kW8JoinCost = 8;
+// Steps that joining a tile from several pairs costs: 200 rows of three 5120 x 5120 take 28 us in whole
+// tiles (40 steps a pair) and 35 in shares (32); 300 rows of 4096 x 4096 18 (32 steps) and 24 (14); 700
+// rows of 4096 x 14336 66 in shares of 71 steps, where a whole tile has 112.
+constexpr int kW8JoinCost = 24;
 
 // Tiles of a wide call along x.
 struct WideShape {

@@ -29,6 +29,8 @@ constexpr int kW8MaxPairs = 96;
 constexpr int kW8WBytes = 128 * kW8WideK;
 
 constexpr int kW8Bufs = 4;                     // A buffers in tensor memory and stages of x
+constexpr int kW8JoinBufs = 5;                 // pieces of parts under way in a join, 32 columns of 128 rows each
+constexpr int kW8PieceBytes = 32 * 128 * 4;
 // By the most columns (rows of x) of a tile: stages of W, an even number.  64 rows of two 14336 x 4096
 // take 28 us with 6, 8 or 12 of them and 31 with 4.
 __host__ __device__ constexpr int w8_w_stages(int n) { return n > 128 ? 6 : 8; }
@@ -207,32 +209,14 @@ __device__ __forceinline__ void w8_store(const uint32_t* from, __nv_bfloat16*& t
     }
 }
 
-// Adds parts q .. n - 1 of sixteen columns of a row in their order, SOME at a time: what is in flight
-// counts, an answer takes 800 clocks, or 1,500 from the other die.  The first pair's part is in the
-// second of its two slots, the others' in their first.
-template <int SOME>
-__device__ __forceinline__ void w8_add_parts(float (&sum)[16], const float4* first, int64_t slot, int q, int n) {
-    for (; q < n; q += SOME) {
-        float4 x[SOME][4];
-#pragma unroll
-        for (int k = 0; k < SOME; ++k) {
-            const int j = min(q + k, n - 1);                   // past the last: the last again
-            const float4* at = first + (j ? 4 * j : 1) * slot;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[k][i] = __ldcg(at + i * 128);
-        }
-#pragma unroll
-        for (int k = 0; k < SOME; ++k) {
-            const bool in = q + k < n;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum[4 * i] += in ? x[k][i].x : 0.f;
-                sum[4 * i + 1] += in ? x[k][i].y : 0.f;
-                sum[4 * i + 2] += in ? x[k][i].z : 0.f;
-                sum[4 * i + 3] += in ? x[k][i].w : 0.f;
-            }
-        }
-    }
+// Where part q of a tile's n lies, from the place of the pair that begins it: its own in the second of
+// that pair's two slots, the next pairs' in their first.
+__device__ __forceinline__ const float* w8_part(const float* first, int q, int64_t slot) { return first + (q ? 4 * q : 1) * slot; }
+__device__ __forceinline__ void w8_add(float (&sum)[16], int i, const float4& x) {
+    sum[4 * i] += x.x;
+    sum[4 * i + 1] += x.y;
+    sum[4 * i + 2] += x.z;
+    sum[4 * i + 3] += x.w;
 }
 
 // NMAX: the most columns of a tile.  SPLIT: whether a pair's range may begin or end inside a tile
@@ -243,6 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     // Registers move from the warps that issue and widen to those that hold a row's sums: the shares of
     // the five groups of four warps add up to the 480 of the launch.  (A few spilled registers in the
     // path of whole tiles cost as much as the path itself.)
+    constexpr int kDs = NMAX > 128 ? 1 : 2;    // D buffers, 128 columns apart
     constexpr int kRegsOut = NMAX > 128 ? 160 : 136, kRegsWiden = NMAX > 128 ? 56 : 80, kRegsMisc = 48;
     static_assert(kRegsMisc + 2 * kRegsWiden + 2 * kRegsOut <= 480, "registers of the launch");
     // A wait for a barrier's phase must not fall two phases behind.  The two groups of widening warps take
@@ -251,7 +236,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     static_assert(kWStages % 2 == 0 && kW8Bufs % 2 == 0, "stages of one group each");
     constexpr uint32_t kACol = 256;            // D in columns 0 .. 255, four A buffers of 64 columns after it
     extern __shared__ unsigned char raw[];
-    __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full, d_empty, final_bar;
+    __shared__ __align__(8) uint64_t w_full[kWStages], w_empty[kWStages], ready[kW8Bufs], freed[kW8Bufs], d_full[kDs], d_empty[kDs], final_bar;
+    __shared__ __align__(8) uint64_t piece[2][kW8JoinBufs];
     __shared__ __align__(16) float sx[2][128];
     __shared__ uint32_t tmem_slot, last_in[2], lost[2];
     unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -271,10 +257,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         mbar_init(bar(freed[tid - 32]), 1);
         fence_mbar_init();
     } else if (tid == 64) {
-        mbar_init(bar(d_full), 1);
-        mbar_init(bar(d_empty), 16);
+        for (int i = 0; i < kDs; ++i) {
+            mbar_init(bar(d_full[i]), 1);
+            mbar_init(bar(d_empty[i]), 16);
+        }
         mbar_init(bar(final_bar), 1);
         lost[0] = lost[1] = 0;
+        fence_mbar_init();
+    } else if (SPLIT && tid >= 128 && tid < 128 + 2 * kW8JoinBufs) {
+        mbar_init(bar(piece[0][tid - 128]), 1);
         fence_mbar_init();
     }
     if (warp == 3) {
@@ -347,17 +338,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 const uint32_t b = i % kW8Bufs;
                 const bool last = a.kb + 1 == p.prob[a.prob].kblocks || u + 1 == end;
                 w8_next(p, a);
-                if (fresh && !wait(d_empty, (tiles & 1) ^ 1)) { ok = false; break; }
+                const uint32_t d = tiles % kDs;
+                if (fresh && !wait(d_empty[d], ((tiles / kDs) & 1) ^ 1)) { ok = false; break; }
                 if (!wait(ready[b], (i / kW8Bufs) & 1)) { ok = false; break; }
                 tc_fence_after();
                 const uint64_t db = desc_at(x_desc, b * kXStage);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kW8WideK / 16; ++k)
-                        tc_mma_pair(tmem, tmem + kACol + b * 64 + k * 8, desc_at(db, (k / 4) * box + (k % 4) * 32), idesc,
+                        tc_mma_pair(tmem + d * 128, tmem + kACol + b * 64 + k * 8, desc_at(db, (k / 4) * box + (k % 4) * 32), idesc,
                                     !(fresh && k == 0));
                     tc_commit_pair(bar(freed[b]));
-                    if (last) tc_commit_pair(bar(d_full));
+                    if (last) tc_commit_pair(bar(d_full[d]));
                 }
                 __syncwarp();
                 fresh = last;
@@ -410,13 +402,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         regs_inc<kRegsOut>();
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
         constexpr int kChunks = NMAX / 32;
-        const uint32_t dcol = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
+        const uint32_t dcol0 = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
         const int chunks = half_cols / 16;
         auto meet = [&]() { named_bar_sync(1 + half, 128); };
         W8At a = w8_at(p, first);
         uint32_t tiles = 0;
         for (int at = first; at < end; ++tiles) {
             const W8WideProb& pr = p.prob[a.prob];
+            const uint32_t d = tiles % kDs, dcol = dcol0 + d * 128;
             const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = min(tile_end, end);
             const int row0 = a.rt * kW8WideRows + (int)rank * 128, col0 = a.tt * p.cols + half * half_cols;
             const bool whole = !SPLIT || (at == tile_first && stop == tile_end);
@@ -425,15 +418,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             sx[half][g] = col0 + g < p.T && g < half_cols ? pr.x_scales[col0 + g] : 0.f;
             // after a wait that ran out the four warps take no more sums, as one, but still count
             // their parts of the range's tiles (with the error set), so that the tickets end as they began
-            if (ok && !wait(d_full, tiles & 1)) lost[half] = 1;
+            if (ok && !wait(d_full[d], (tiles / kDs) & 1)) lost[half] = 1;
             meet();
             ok = *reinterpret_cast<volatile uint32_t*>(&lost[half]) == 0;
-            // a part lies [column / 4][row][4]
-            auto part_of = [&](int64_t cta, int slot) {
-                return reinterpret_cast<float4*>(p.part + (cta * 2 + slot) * (int64_t)w8_part_floats(NMAX) + (int64_t)half * half_cols * 128) + r;
-            };
-            float4* part = part_of(blockIdx.x, tile_first < first ? 0 : 1);
             tc_fence_after();
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(mapa(bar(d_empty[d]), 0));
+            };
             // a whole tile's sums become y in registers, a part goes out as it is: either way the
             // MMAs of the next tile wait for no store
             auto drain = [&](auto&& take) {
@@ -447,9 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                         take(c, v[c & 1]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
+                release();
             };
             if (whole) {
                 uint32_t out[8 * kChunks];
@@ -464,29 +455,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                         if (c < chunks) w8_store(out + c * 8, to, two, left);
                 }
             } else {
-                const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per;
-                uint32_t* ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
-                // the sum over all parts, in the order of K; `mine`: the first one is in tensor memory
-                auto join = [&](bool mine) {
-                    constexpr int64_t kSlot = w8_part_floats(NMAX) / 4;
-                    constexpr int kSome = NMAX > 128 ? 3 : NMAX > 64 ? 4 : 6;
-                    const float4* from = part_of((int64_t)p0 * 2 + rank, 0);
+                // A part lies [column / 4][row][4].  This pair's, and the place of those of the pair that begins the tile:
+                constexpr int64_t kSlot = w8_part_floats(NMAX);
+                const int p0 = tile_first / p.per, p1 = (tile_end - 1) / p.per, n = p1 - p0 + 1;
+                uint32_t* const ticket = p.tickets + (p0 * 2 + rank) * 2 + half;
+                const float* const parts = p.part + (4 * (int64_t)p0 + 2 * rank) * kSlot + half * half_cols * 128;
+                float4* const part = reinterpret_cast<float4*>(const_cast<float*>(w8_part(parts, pair - p0, kSlot))) + r;
+                // The sum over all parts in the order of K; `mine`: the first one is in tensor memory.  At the end
+                // of the pair's range its rings are free (the MMAs are done): the parts come through them
+                // by bulk copies, since an answer takes 800 clocks, or 1,500 from the other die, and more
+                // cannot be under way in registers.
+                auto join = [&](int mine) {
+                    const bool rings = stop == end && ok;
+                    const uint32_t ring = w0 + half * kW8JoinBufs * kW8PieceBytes;
+                    const int m = n - mine, all = (chunks + 1) / 2 * m;
+                    int put = 0, got = 0;
+                    auto fetch = [&]() {                       // pieces: 32 columns after 32, of one part after the other
+                        for (; put < all && put < got + kW8JoinBufs; ++put) {
+                            const int c = put / m, q = mine + put - c * m, b = put % kW8JoinBufs;
+                            const uint32_t bytes = 2 * c + 1 < chunks ? kW8PieceBytes : kW8PieceBytes / 2;
+                            mbar_arrive_expect_tx(bar(piece[half][b]), bytes);
+                            bulk_g2s(ring + b * kW8PieceBytes, w8_part(parts, q, kSlot) + c * 4096, bytes, bar(piece[half][b]));
+                        }
+                    };
+                    if (rings && g == 0) {
+                        // parts were written by plain stores: they are seen by now, the copies have to see them too
+                        asm volatile("fence.proxy.async;" ::: "memory");
+                        fetch();
+                    }
+                    put = min(all, kW8JoinBufs);
                     int left = row0 + r < pr.N ? p.T - col0 - (lane & 1) : 0;
                     const int64_t two = 2 * pr.ldy;
                     __nv_bfloat16* to = pr.y + (int64_t)(col0 + (lane & 1)) * pr.ldy + row0 + (r & ~1);
-                    for (int c = 0; c < chunks; ++c, from += 512) {
-                        float sum[16];
+                    for (int c = 0; c < chunks; c += 2) {      // past the last sixteen columns nothing is stored
+                        float sum[2][16];
                         if (mine) {
-                            tmem_ld16(dcol + c * 16, sum);
-                            tmem_ld_wait16(sum);
+                            tmem_ld16(dcol + c * 16, sum[0]);
+                            tmem_ld16(dcol + (c + 1) * 16, sum[1]);
+                            tmem_ld_wait16(sum[0]);
+                            tmem_ld_wait16(sum[1]);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) sum[i] = 0.f;
+                            for (int i = 0; i < 32; ++i) sum[i / 16][i % 16] = 0.f;
                         }
-                        w8_add_parts<kSome>(sum, from, kSlot, mine, p1 - p0 + 1);
-                        uint32_t out[8];
-                        w8_scale(sum, &sx[half][c * 16], sw, out);
-                        w8_store(out, to, two, left);
+                        for (int q = mine; q < n; ++q, ++got) {
+                            if (rings && put < all && put - got <= kW8JoinBufs / 2) {
+                                meet();                        // all have read the pieces before this one
+                                if (g == 0) fetch();
+                                put = min(all, got + kW8JoinBufs);
+                            }
+                            if (rings) {
+                                const int b = got % kW8JoinBufs;
+                                if (ok && !wait(piece[half][b], (got / kW8JoinBufs) & 1)) ok = false;
+                                const uint32_t from = ring + b * kW8PieceBytes + r * 16;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const uint4 x = lds128(from + i * 2048);
+                                    w8_add(sum[i / 4], i % 4, make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)));
+                                }
+                            } else {
+                                const float4* from = reinterpret_cast<const float4*>(w8_part(parts, q, kSlot)) + c * 512 + r;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) w8_add(sum[i / 4], i % 4, __ldcg(from + (c + 1 < chunks ? i : i % 4) * 128));
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (c + i == chunks) break;
+                            uint32_t out[8];
+                            w8_scale(sum[i], &sx[half][(c + i) * 16], sw, out);
+                            w8_store(out, to, two, left);
+                        }
                     }
                 };
                 // Where all other parts are there already (a pair comes to the tile that it begins last, when
@@ -494,16 +533,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 if (g == 0) {
                     uint32_t there = 0;
                     if (pair == p0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(ticket) : "memory");
-                    last_in[half] = there == (uint32_t)(p1 - p0);
+                    last_in[half] = there == (uint32_t)(n - 1);
                 }
                 meet();
                 const bool early = *reinterpret_cast<volatile uint32_t*>(&last_in[half]) && ok;
                 if (early) {
                     __threadfence();
-                    join(true);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(mapa(bar(d_empty), 0));
+                    join(1);
+                    release();
                     if (g == 0) *ticket = 0;
                 } else {
                     drain([&](int c, const float (&v)[16]) {
@@ -513,12 +550,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                     });
                     __threadfence();
                     meet();
-                    if (g == 0) last_in[half] = atomicAdd(ticket, 1u) == (uint32_t)(p1 - p0);
+                    if (g == 0) last_in[half] = atomicAdd(ticket, 1u) == (uint32_t)(n - 1);
                     meet();
                     if (*reinterpret_cast<volatile uint32_t*>(&last_in[half])) {
                         __threadfence();
                         if (g == 0) *ticket = 0;
-                        join(false);
+                        join(0);
                     }
                 }
                 meet();
