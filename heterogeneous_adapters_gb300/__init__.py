@@ -22,7 +22,7 @@ from ._binding import (LORA_KV_MAX_HEADS, LORA_KV_MAX_SEQS, LORA_ROPE_HALVES, LO
                        w4_workspace_size)
 from ._binding import (LORA_ACT_GELU, LORA_ACT_GELU_TANH, LORA_ACT_NONE, LORA_ACT_SILU, LORA_Q8_MAX_ROWS, LORA_Q8_MAX_WIDTH,
                        LORA_Q8_X_FULL, LORA_Q8_X_HELD, LORA_W8_MAX_K, LORA_W8_MAX_PROBLEMS, LORA_W8_MAX_ROWS, Q8Gate, Q8Norm,
-                       Q8Rows, q8_gate, q8_norm, w8_matmul, w8_problems, w8_workspace_size)
+                       Q8Rows, debug_w8_lost_step, q8_gate, q8_norm, w8_matmul, w8_problems, w8_workspace_size)
 
 __all__ = ["costmodel", "DERR", "LORA_ENOSPACE", "LORA_MAX_PROBLEMS_PER_LAUNCH", "LORA_MAX_RANK",
            "LORA_MAX_SEGMENTS", "LORA_NOALLOC_MAX_TOKENS", "LORA_STAGE_MAX_RUNS", "LORA_UNIT_ABSENT",
@@ -38,4 +38,4 @@ __all__ = ["costmodel", "DERR", "LORA_ENOSPACE", "LORA_MAX_PROBLEMS_PER_LAUNCH",
            "w4_workspace_size",
            "LORA_ACT_GELU", "LORA_ACT_GELU_TANH", "LORA_ACT_NONE", "LORA_ACT_SILU", "LORA_Q8_MAX_ROWS", "LORA_Q8_MAX_WIDTH",
            "LORA_Q8_X_FULL", "LORA_Q8_X_HELD", "LORA_W8_MAX_K", "LORA_W8_MAX_PROBLEMS", "LORA_W8_MAX_ROWS", "Q8Gate", "Q8Norm",
-           "Q8Rows", "q8_gate", "q8_norm", "w8_matmul", "w8_problems", "w8_workspace_size"]
+           "Q8Rows", "debug_w8_lost_step", "q8_gate", "q8_norm", "w8_matmul", "w8_problems", "w8_workspace_size"]

@@ -48,7 +48,7 @@ EXPORTED = ["lora_pool_create", "lora_pool_destroy", "lora_pool_set_tuning", "lo
             "lora_kv_block_bytes", "lora_kv_workspace_size", "lora_kv_workspace_init", "lora_kv_append",
             "lora_kv_read", "lora_kv_attend", "lora_w4_workspace_size", "lora_w4_matvec", "lora_debug_w4_lost_block",
             # an 8-bit base model (include/lora_w8.h)
-            "lora_q8_norm", "lora_q8_gate", "lora_w8_workspace_size", "lora_w8_matmul"]
+            "lora_q8_norm", "lora_q8_gate", "lora_w8_workspace_size", "lora_w8_matmul", "lora_debug_w8_lost_step"]
 
 
 class lora_pool_desc(ctypes.Structure):
@@ -200,6 +200,7 @@ def lib():
             "lora_q8_gate": [p, i32, p],
             "lora_w8_workspace_size": [p, i32, i32, ctypes.POINTER(sz)],
             "lora_w8_matmul": [p, i32, i32, p, sz, p],
+            "lora_debug_w8_lost_step": [p, i32, i32, i32, ctypes.c_uint64, p, sz, p],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -565,6 +566,12 @@ def w8_workspace_size(problems, T: int) -> int:
 def w8_matmul(problems, T, ws, ws_bytes, stream):
     """y = x W^T of 8-bit integers for every projection of w8_problems(...)."""
     _check(lib().lora_w8_matmul(problems.ref, problems.n, T, _ptr(ws), ws_bytes, stream), "lora_w8_matmul")
+
+
+def debug_w8_lost_step(problems, T, step, limit_ns, ws, ws_bytes, stream):
+    """w8_matmul with one step's W missing: its waits run out after limit_ns."""
+    _check(lib().lora_debug_w8_lost_step(problems.ref, problems.n, T, step, limit_ns, _ptr(ws), ws_bytes, stream),
+           "lora_debug_w8_lost_step")
 
 
 # ----------------------------------------------------------------------------- host runtime

@@ -82,35 +82,66 @@ lora_status check_sizes(const lora_w8_problem* probs, int32_t nprob, int32_t T) 
     return LORA_OK;
 }
 
-// Rows and bytes of W up to which w8_narrow.cuh serves: it begins 5 us earlier than w8_wide.cuh, but
-// widens x once per 16 rows of W.  16 rows, narrow and wide: q, k, v of 25 MB 9.3 and 14.8 us, 59 MB 21.6
-// and 22.9, 79 MB 21.5 and 20.7, 117 MB 29 and 27.4; 32 rows: 17 MB 9.1 and 12.9, 25 MB 15.5 and 15.2,
-// 79 MB 36 and 21; 8 rows of 117 MB 23 and 28.
-constexpr int64_t kW8Narrow16 = 64 << 20, kW8Narrow32 = 24 << 20;
+// Which kernel serves.  w8_narrow.cuh begins 5 us earlier than w8_wide.cuh, but takes W through the SMs once
+// per 32 rows of x and widens x once per 16 rows of W.  Narrow and wide, us: 8 rows of 117 MB 23 and 28;
+// 16 rows of 25 MB 9.3 and 14.8, 59 MB 21.6 and 22.9, 79 MB 21.5 and 20.7, 117 MB 29 and 27; 32 rows of 17 MB
+// 8.5 and 12.8, 25 MB 15.5 and 15.2, 79 MB 36 and 21; 128 rows of 4 MB 9.5 and 10.7; 400 rows of 1 MB 9.3
+// and 10.6, 800 rows 16 and 11.
+constexpr int64_t kW8Narrow16 = 64 << 20, kW8Narrow = 24 << 20;
 bool narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
     if (T <= 8) return true;
-    if (T > 32) return false;
     int64_t bytes = 0;
     for (int32_t i = 0; i < nprob; ++i) bytes += (int64_t)probs[i].N * probs[i].K;
-    return bytes <= (T <= 16 ? kW8Narrow16 : kW8Narrow32);
+    return T <= 16 ? bytes <= kW8Narrow16 : bytes * ((T + 31) / 32) <= kW8Narrow;
 }
 
-// Steps that joining a tile from several pairs costs: 200 rows of three 5120 x 5120 take 28 us in whole
-// tiles (40 steps a pair) and 35 in shares (32); 300 rows of 4096 x 4096 18 (32 steps) and 24 (14); 700
-// rows of 4096 x 14336 66 in shares of 71 steps, where a whole tile has 112.
-constexpr int kW8JoinCost = 24;
-
-// Tiles of a wide call along x.
+// How a wide call is shared out.
 struct WideShape {
-    int nmax, cols, ttiles;
+    int cols, ttiles;              // columns of a tile (rows of x), tiles along x
+    int32_t per;                   // steps of a pair
+    bool split;                    // whether a pair's range begins or ends inside a tile
 };
-WideShape wide_shape(int32_t T) {
-    if (T <= 256) {
-        const int cols = (T + 31) / 32 * 32;
-        return {cols <= 64 ? 64 : cols <= 128 ? 128 : 256, cols, 1};
+constexpr int wide_max(int cols) { return cols <= 64 ? 64 : cols <= 128 ? 128 : 256; }
+
+// The tiles of up to 64, 128 or 256 columns, whole or in equal shares of all steps, that should take the
+// fewest clocks: a step of c columns takes 4 c for its MMAs, 640 for its widening, and 870 for its W from
+// memory where all pairs stream and no other tile has fetched it; joining a tile from several pairs
+// some 8,000 + 60 c (200 rows of three 5120 x 5120: 28 us in whole tiles of 224 columns, 40 steps a
+// pair, 35 in shares of 32).  A share is not so small that a tile has many parts (35 rows of 184 x
+// 6400: 28 us in 50 parts, 13 in 9; 100 rows of 4096 x 4096 19 in 6, 15 in 4).
+WideShape wide_shape(const lora_w8_problem* probs, int32_t nprob, int32_t T, int pairs) {
+    WideShape best = {0, 0, 0, false};
+    int64_t least = INT64_MAX;
+    for (const int most : {64, 128, 256}) {
+        const int ttiles = (T + most - 1) / most, cols = ((T + ttiles - 1) / ttiles + 31) / 32 * 32;
+        int64_t tiles = 0, steps = 0;
+        int32_t kb = 0;
+        bool one_k = true;
+        for (int32_t i = 0; i < nprob; ++i) {
+            const int32_t k = (probs[i].K + kW8WideK - 1) / kW8WideK;
+            const int64_t n = (int64_t)((probs[i].N + kW8WideRows - 1) / kW8WideRows) * ttiles;
+            one_k = one_k && (i == 0 || k == kb);
+            kb = std::max(kb, k);
+            tiles += n;
+            steps += n * k;
+        }
+        auto clocks = [&](int64_t per) {
+            const int64_t busy = std::min<int64_t>(pairs, (steps + per - 1) / per);
+            return per * std::max<int64_t>({640, 4 * cols, 870 * busy / pairs / ttiles});
+        };
+        const int64_t share = std::max<int64_t>((steps + pairs - 1) / pairs, cols <= 64 ? 6 : 10);
+        const int64_t in_shares = clocks(share) + 8000 + 60 * cols;
+        if (in_shares < least) {
+            least = in_shares;
+            best = {cols, ttiles, (int32_t)std::min<int64_t>(share, INT32_MAX), true};
+        }
+        const int64_t whole = (tiles + pairs - 1) / pairs * kb;
+        if (one_k && clocks(whole) < least) {
+            least = clocks(whole);
+            best = {cols, ttiles, (int32_t)std::min<int64_t>(whole, INT32_MAX), false};
+        }
     }
-    const int tiles = (T + 255) / 256;
-    return {256, ((T + tiles - 1) / tiles + 31) / 32 * 32, tiles};
+    return best;
 }
 
 // The first problem with i's x.
@@ -124,7 +155,7 @@ size_t x_bytes(const lora_w8_problem& p, int32_t T) { return align256((size_t)T 
 
 size_t workspace_bytes(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
     if (narrow(probs, nprob, T)) return align256(kStepPartAt);
-    size_t n = align256(kStepPartAt) + w8_part_bytes(wide_shape(T).nmax);
+    size_t n = align256(kStepPartAt) + w8_part_bytes(wide_max(std::min(T, 256)));   // of the widest tiles
     for (int32_t i = 0; i < nprob; ++i)
         if (x_of(probs, i) == i) n += x_bytes(probs[i], T);
     return n;
@@ -146,7 +177,7 @@ lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, c
     const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
     if (nt == 1) w8_narrow_kernel<1><<<(unsigned)total, kW8Threads, 0, s>>>(p);
     else if (nt == 2) w8_narrow_kernel<2><<<(unsigned)total, kW8Threads, 0, s>>>(p);
-    else w8_narrow_kernel<4><<<(unsigned)total, kW8Threads, 0, s>>>(p);
+    else w8_narrow_kernel<4><<<dim3((unsigned)total, (unsigned)((T + 31) / 32)), kW8Threads, 0, s>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -210,23 +241,30 @@ lora_status launch_wide(const W8WideParams& w, int pairs, cudaStream_t s) {
 }
 
 template <int NMAX>
-lora_status share_wide(W8WideParams& w, cudaStream_t s) {
-    int pairs = 0, same = 0;
-    lora_status st = ready_wide<NMAX, false>(&pairs);
-    if (st == LORA_OK) st = ready_wide<NMAX, true>(&same);
-    if (st != LORA_OK) return st;
-    // equal shares of all steps, or whole tiles where the largest share of them is not much more
-    // (which needs one K for all projections)
-    w.per = (w.total + pairs - 1) / pairs;
-    const int32_t kb = w.prob[0].kblocks;
-    bool one_k = true;
-    for (int32_t i = 1; i < w.nprob; ++i) one_k = one_k && w.prob[i].kblocks == kb;
-    const int32_t whole = (w.total / kb + pairs - 1) / pairs * kb;
-    if (one_k && whole <= w.per + kW8JoinCost) w.per = whole;
-    return one_k && w.per % kb == 0 ? launch_wide<NMAX, false>(w, pairs, s) : launch_wide<NMAX, true>(w, pairs, s);
+lora_status launch_wide(const W8WideParams& w, bool split, int pairs, cudaStream_t s) {
+    return split ? launch_wide<NMAX, true>(w, pairs, s) : launch_wide<NMAX, false>(w, pairs, s);
 }
 
-lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, cudaStream_t s) {
+// Pairs of CTAs that the device holds, all kernels ready.
+lora_status ready_wide(int* pairs) {
+    lora_status st = LORA_OK;
+    *pairs = kW8MaxPairs;
+    int n = 0;
+    auto take = [&](lora_status r) {
+        if (st == LORA_OK) st = r;
+        *pairs = std::min(*pairs, n);
+    };
+    take(ready_wide<64, false>(&n));
+    take(ready_wide<64, true>(&n));
+    take(ready_wide<128, false>(&n));
+    take(ready_wide<128, true>(&n));
+    take(ready_wide<256, false>(&n));
+    take(ready_wide<256, true>(&n));
+    return st;
+}
+
+lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, cudaStream_t s, int32_t lost,
+                     uint64_t limit_ns) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     lora_status st = encode_fn(&enc);
     if (st != LORA_OK) return st;
@@ -234,7 +272,10 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
     static thread_local W8Widen v;
     memset(&w, 0, sizeof w);
     memset(&v, 0, sizeof v);
-    const WideShape sh = wide_shape(T);
+    int pairs = 0;
+    if ((st = ready_wide(&pairs)) != LORA_OK) return st;
+    const WideShape sh = wide_shape(probs, nprob, T, pairs);
+    const int nmax = wide_max(sh.cols);
     char* base = reinterpret_cast<char*>(ws);
     w.nprob = nprob;
     w.T = v.T = T;
@@ -243,8 +284,10 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
     w.tickets = reinterpret_cast<uint32_t*>(base + sizeof(WsHeader));
     w.part = reinterpret_cast<float*>(base + align256(kStepPartAt));
     w.err = &reinterpret_cast<WsHeader*>(ws)->err;
-    w.limit_ns = kWaitLimitNs;
-    char* at = base + align256(kStepPartAt) + w8_part_bytes(sh.nmax);
+    w.limit_ns = limit_ns;
+    w.lost = lost;
+    w.per = sh.per;
+    char* at = base + align256(kStepPartAt) + w8_part_bytes(nmax);
     int32_t copies = 0, slot[LORA_W8_MAX_PROBLEMS];
     int64_t total = 0, most = 0;
     for (int32_t i = 0; i < nprob; ++i) {
@@ -268,7 +311,7 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
         if (st != LORA_OK) return st;
         w.prob[i] = {pr.x_scales, pr.w_scales, reinterpret_cast<__nv_bfloat16*>(pr.y), pr.ldy, pr.N, (pr.K + kW8WideK - 1) / kW8WideK, (int32_t)total, slot[i]};
         total += (int64_t)((pr.N + kW8WideRows - 1) / kW8WideRows) * sh.ttiles * w.prob[i].kblocks;
-        if (total > INT32_MAX) return LORA_ETOOBIG;
+        if (total > (1 << 30)) return LORA_ETOOBIG;
     }
     w.total = (int32_t)total;
     DeviceInfo* di = nullptr;
@@ -277,8 +320,26 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
     w8_widen_kernel<<<dim3((unsigned)blocks, (unsigned)copies), kWidenThreads, 0, s>>>(v);
     st = cuda_status(cudaGetLastError());
     if (st != LORA_OK) return st;
-    if (sh.nmax == 64) return share_wide<64>(w, s);
-    return sh.nmax == 128 ? share_wide<128>(w, s) : share_wide<256>(w, s);
+    if (nmax == 64) return launch_wide<64>(w, sh.split, pairs, s);
+    return nmax == 128 ? launch_wide<128>(w, sh.split, pairs, s) : launch_wide<256>(w, sh.split, pairs, s);
+}
+
+lora_status run(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes, void* stream, int32_t lost,
+                uint64_t limit_ns) {
+    lora_status st = check_sizes(probs, nprob, T);
+    if (st != LORA_OK) return st;
+    for (int32_t i = 0; i < nprob; ++i) {
+        const lora_w8_problem& pr = probs[i];
+        if (pr.x == nullptr || pr.x_scales == nullptr || pr.y == nullptr || pr.w == nullptr || pr.w_scales == nullptr) return LORA_EINVAL;
+        if (!aligned16(pr.x) || !aligned16(pr.y) || !aligned16(pr.w) || ((uintptr_t)pr.x_scales & 3u) != 0 ||
+            ((uintptr_t)pr.w_scales & 3u) != 0 || pr.ldx % 16 != 0 || pr.ldy % 8 != 0)
+            return LORA_EALIGN;
+        if (pr.ldx < pr.K || pr.ldy < pr.N) return LORA_EINVAL;
+    }
+    if (nprob == 0 || T == 0) return LORA_OK;
+    if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes(probs, nprob, T)) return LORA_EWORKSPACE;
+    cudaStream_t s = (cudaStream_t)stream;
+    return narrow(probs, nprob, T) ? run_narrow(probs, nprob, T, s) : run_wide(probs, nprob, T, ws, s, lost, limit_ns);
 }
 
 }  // namespace
@@ -334,20 +395,16 @@ lora_status lora_w8_workspace_size(const lora_w8_problem* probs, int32_t nprob, 
 }
 
 lora_status lora_w8_matmul(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes, void* stream) {
+    return run(probs, nprob, T, ws, ws_bytes, stream, -1, kWaitLimitNs);
+}
+
+lora_status lora_debug_w8_lost_step(const lora_w8_problem* probs, int32_t nprob, int32_t T, int32_t step, uint64_t limit_ns,
+                                    void* ws, size_t ws_bytes, void* stream) {
     lora_status st = check_sizes(probs, nprob, T);
     if (st != LORA_OK) return st;
-    for (int32_t i = 0; i < nprob; ++i) {
-        const lora_w8_problem& pr = probs[i];
-        if (pr.x == nullptr || pr.x_scales == nullptr || pr.y == nullptr || pr.w == nullptr || pr.w_scales == nullptr) return LORA_EINVAL;
-        if (!aligned16(pr.x) || !aligned16(pr.y) || !aligned16(pr.w) || ((uintptr_t)pr.x_scales & 3u) != 0 ||
-            ((uintptr_t)pr.w_scales & 3u) != 0 || pr.ldx % 16 != 0 || pr.ldy % 8 != 0)
-            return LORA_EALIGN;
-        if (pr.ldx < pr.K || pr.ldy < pr.N) return LORA_EINVAL;
-    }
-    if (nprob == 0 || T == 0) return LORA_OK;
-    if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes(probs, nprob, T)) return LORA_EWORKSPACE;
-    cudaStream_t s = (cudaStream_t)stream;
-    return narrow(probs, nprob, T) ? run_narrow(probs, nprob, T, s) : run_wide(probs, nprob, T, ws, s);
+    if (narrow(probs, nprob, T) || step < 0 || limit_ns < 1000000ull) return LORA_EINVAL;
+    if (limit_ns > kWaitLimitNs) return LORA_ETOOBIG;
+    return run(probs, nprob, T, ws, ws_bytes, stream, step, limit_ns);
 }
 
 }  // extern "C"

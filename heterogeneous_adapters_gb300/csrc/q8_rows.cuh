@@ -262,18 +262,22 @@ __device__ __forceinline__ uint64_t q8_act(uint64_t v) {
     unpack2f(v, a[0], a[1]);
     if (ACT == LORA_ACT_NONE) {
         return v;
-    } else if (ACT == LORA_ACT_SILU) {
-        // e^-a to 2^-24 (4 + |a|) of itself; where it passes fp32's range, a e^a is nothing
+    } else if (ACT == LORA_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) a[i] = 0.5f * a[i] * (1.f + erff(a[i] * 0.70710678f));
+        return pack2f(a[0], a[1]);
+    } else {
+        // a / (1 + e^-z): z = a, or (1 + tanh(z / 2)) / 2 with the z of the other form.  e^-z is right to 2^-24
+        // (4 + |z|) of itself; where it passes fp32's range, a e^z is nothing
+        uint64_t z = mul2(v, pack2f(-1.44269504f, -1.44269504f));
+        if (ACT == LORA_ACT_GELU_TANH) {
+            constexpr float k = 2.f * 0.79788456f;
+            z = mul2(z, fma2(mul2(v, v), pack2f(k * 0.044715f, k * 0.044715f), pack2f(k, k)));
+        }
         float e[2];
-        unpack2f(mul2(v, pack2f(-1.44269504f, -1.44269504f)), e[0], e[1]);
+        unpack2f(z, e[0], e[1]);
         unpack2f(add2(pack2f(exp2_approx(e[0]), exp2_approx(e[1])), pack2f(1.f, 1.f)), e[0], e[1]);
         return mul2(v, pack2f(rcp_approx(e[0]), rcp_approx(e[1])));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            a[i] = 0.5f * a[i] * (1.f + (ACT == LORA_ACT_GELU ? erff(a[i] * 0.70710678f)
-                                                              : tanhf(0.79788456f * (a[i] + 0.044715f * a[i] * a[i] * a[i]))));
-        return pack2f(a[0], a[1]);
     }
 }
 

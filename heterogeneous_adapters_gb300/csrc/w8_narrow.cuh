@@ -59,13 +59,13 @@ __global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(cons
     int i = 0;
     while (i + 1 < p.nprob && (int)blockIdx.x >= p.prob[i + 1].first) ++i;
     const W8Prob& pr = p.prob[i];
-    const int row0 = ((int)blockIdx.x - pr.first) * kW8Rows, K = pr.K;
+    const int row0 = ((int)blockIdx.x - pr.first) * kW8Rows, K = pr.K, t0 = blockIdx.y * 8 * NT;
     const bool in1 = row0 + 8 + g < pr.N;                      // N is a multiple of 8
     const unsigned char* w0 = pr.w + (int64_t)(row0 + g) * K;
     const unsigned char* w1 = w0 + (in1 ? 8 * (int64_t)K : 0);
     const unsigned char* xr[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xr[n] = pr.x + min(n * 8 + g, p.T - 1) * pr.ldx;   // rows past the last: the last again
+    for (int n = 0; n < NT; ++n) xr[n] = pr.x + min(t0 + n * 8 + g, p.T - 1) * pr.ldx;   // rows past the last: the last again
     int32_t sum[NT][4];
     float acc[NT][4];
 #pragma unroll
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(cons
         int32_t s = 0;
 #pragma unroll
         for (int w = 0; w < kW8Warps; ++w) s += red[w][col][r];
-        if (col < p.T && row0 + r < pr.N)
-            pr.y[col * pr.ldy + row0 + r] = __float2bfloat16_rn((float)s * pr.x_scales[col] * pr.w_scales[row0 + r]);
+        if (t0 + col < p.T && row0 + r < pr.N)
+            pr.y[(t0 + col) * pr.ldy + row0 + r] = __float2bfloat16_rn((float)s * pr.x_scales[t0 + col] * pr.w_scales[row0 + r]);
     }
 }
 

@@ -65,7 +65,8 @@ struct W8WideParams {
     uint32_t* tickets;                         // [kStepTickets], zero between calls
     float* part;
     uint32_t* err;
-    uint64_t limit_ns;
+    uint64_t limit_ns;                         // of every wait
+    int32_t lost;                              // a step whose W never comes (a test of the waits), or -1
 };
 
 // ---------------------------------------------------------------------------- x in f16
@@ -287,7 +288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         if (lane == 0) {
             W8At a = w8_at(p, first);
             uint32_t i = 0;
-            for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
+            for (int u = first; u < end && u != p.lost; ++u, w8_next(p, a), ++i) {
                 const uint32_t s = i % kWStages;
                 if (!mbar_wait_quiet(bar(w_empty[s]), ((i / kWStages) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
                 mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);

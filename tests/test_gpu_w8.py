@@ -68,12 +68,27 @@ def test_one_projection(cuda, T, N, K):
     check(cuda, p)
 
 
+@pytest.mark.parametrize("T", [33, 40, 64, 65, 100, 128, 129, 200, 256, 257, 300, 520])
+@pytest.mark.parametrize("N,K", [(8200, 4112), (6152, 4880), (16392, 2064), (65544, 400), (392, 65536)])
+def test_one_large_projection(cuda, T, N, K):
+    """W of 25 MB and more, its last tiles and its last block of K not full."""
+    g = cuda.Generator(device="cuda").manual_seed(T + N)
+    p = problem(cuda, g, T, N, K, pad=8 * (T % 3))
+    call(cuda, [p], T)
+    check(cuda, p)
+
+
 @pytest.mark.parametrize("T", [1, 5, 24, 40, 64, 130, 257, 700])
 def test_projections_of_different_shapes_in_one_call(cuda, T):
     g = cuda.Generator(device="cuda").manual_seed(T)
     a = problem(cuda, g, T, 512, 1024)
     ps = [a, problem(cuda, g, T, 128, 1024, x=a), problem(cuda, g, T, 264, 2048, pad=16), problem(cuda, g, T, 40, 96),
           problem(cuda, g, T, 2048, 256), problem(cuda, g, T, 8, 16)]
+    call(cuda, ps, T)
+    for p in ps:
+        check(cuda, p)
+    # the same behind one that takes the call to the other kernel
+    ps.insert(1, problem(cuda, g, T, 6152, 4880))
     call(cuda, ps, T)
     for p in ps:
         check(cuda, p)
