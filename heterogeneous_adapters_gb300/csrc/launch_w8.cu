@@ -161,9 +161,9 @@ size_t workspace_bytes(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
     return n;
 }
 
+template <int MAX>
 lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, cudaStream_t s) {
-    static thread_local W8Params p;
-    memset(&p, 0, sizeof p);
+    W8Params<MAX> p;
     p.T = T;
     p.nprob = nprob;
     int64_t total = 0;
@@ -175,9 +175,10 @@ lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, c
     }
     p.total = (int32_t)total;
     const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
-    if (nt == 1) w8_narrow_kernel<1><<<(unsigned)total, kW8Threads, 0, s>>>(p);
-    else if (nt == 2) w8_narrow_kernel<2><<<(unsigned)total, kW8Threads, 0, s>>>(p);
-    else w8_narrow_kernel<4><<<dim3((unsigned)total, (unsigned)((T + 31) / 32)), kW8Threads, 0, s>>>(p);
+    const dim3 grid((unsigned)total, (unsigned)((T + 31) / 32));
+    if (nt == 1) w8_narrow_kernel<1, MAX><<<grid, kW8Threads, 0, s>>>(p);
+    else if (nt == 2) w8_narrow_kernel<2, MAX><<<grid, kW8Threads, 0, s>>>(p);
+    else w8_narrow_kernel<4, MAX><<<grid, kW8Threads, 0, s>>>(p);
     return cuda_status(cudaGetLastError());
 }
 
@@ -339,7 +340,8 @@ lora_status run(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws
     if (nprob == 0 || T == 0) return LORA_OK;
     if (ws == nullptr || ((uintptr_t)ws & 255u) != 0 || ws_bytes < workspace_bytes(probs, nprob, T)) return LORA_EWORKSPACE;
     cudaStream_t s = (cudaStream_t)stream;
-    return narrow(probs, nprob, T) ? run_narrow(probs, nprob, T, s) : run_wide(probs, nprob, T, ws, s, lost, limit_ns);
+    if (!narrow(probs, nprob, T)) return run_wide(probs, nprob, T, ws, s, lost, limit_ns);
+    return nprob <= 3 ? run_narrow<3>(probs, nprob, T, s) : run_narrow<LORA_W8_MAX_PROBLEMS>(probs, nprob, T, s);
 }
 
 }  // namespace

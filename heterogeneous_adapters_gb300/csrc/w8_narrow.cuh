@@ -28,8 +28,10 @@ struct W8Prob {
     int32_t first;                 // tiles before the projection
 };
 
+// MAX: the most projections of a launch (a launch's parameters take the host time by their size).
+template <int MAX>
 struct W8Params {
-    W8Prob prob[LORA_W8_MAX_PROBLEMS];
+    W8Prob prob[MAX];
     int32_t nprob;
     int32_t T;
     int32_t total;                 // tiles
@@ -51,8 +53,8 @@ __host__ __device__ constexpr int w8_ctas(int nt) { return nt == 1 ? 3 : nt == 2
 // Lane (g, t) = (lane / 4, lane % 4) takes the 16 bytes from k = 16 t of its row's 64: word j of
 // them are the two pairs that an MMA of 16 of K wants of the lane, for W and for x alike, so
 // that the order of K within the 64 is the same for both.
-template <int NT>
-__global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(const __grid_constant__ W8Params p) {
+template <int NT, int MAX>
+__global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(const __grid_constant__ W8Params<MAX> p) {
     constexpr int G = w8_group(NT), kStride = kW8Warps * kW8Chunk;
     __shared__ int32_t red[kW8Warps][8 * NT][kW8Rows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
