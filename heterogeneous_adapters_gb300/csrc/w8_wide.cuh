@@ -58,7 +58,7 @@ struct W8WideParams {
     W8WideProb prob[LORA_W8_MAX_PROBLEMS];
     int32_t nprob;
     int32_t T;
-    int32_t cols;                              // rows of x of a tile, a multiple of 32
+    int32_t cols;                              // rows of x of a tile, a multiple of 32 as an MMA over two CTAs takes them
     int32_t ttiles;                            // tiles along x
     int32_t total;                             // steps
     int32_t per;                               // steps of a pair
