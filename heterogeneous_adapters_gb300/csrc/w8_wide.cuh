@@ -77,9 +77,9 @@ struct W8Widen {
     int32_t K[LORA_W8_MAX_PROBLEMS];
     int32_t T;
 };
-constexpr int kWidenThreads = 256, kWidenAhead = 4;
+constexpr int kWidenThreads = 256, kWidenAhead = 2;
 
-// Sixteen codes a thread and time, four times in flight; blockIdx.y: the matrix.  At most one CTA of
+// Sixteen codes a thread and time, two times in flight; blockIdx.y: the matrix.  At most one CTA of
 // these for each that an SM holds: the next kernel begins when all have begun.
 __global__ void __launch_bounds__(kWidenThreads, 8) w8_widen_kernel(const __grid_constant__ W8Widen p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -100,9 +100,10 @@ __global__ void __launch_bounds__(kWidenThreads, 8) w8_widen_kernel(const __grid
             codes8_f16(v[k].y, a.z, a.w);
             codes8_f16(v[k].z, b.x, b.y);
             codes8_f16(v[k].w, b.z, b.w);
-            uint32_t* to = p.out[i] + (int64_t)(e + k * step) * 8;       // rows lie end to end
-            st16(to, a);
-            st16(to + 4, b);
+            // rows lie end to end, 32-byte aligned
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p.out[i] + (int64_t)(e + k * step) * 8), "r"(a.x),
+                         "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                         : "memory");
         }
     }
 }
