@@ -83,16 +83,27 @@ lora_status check_sizes(const lora_w8_problem* probs, int32_t nprob, int32_t T) 
 }
 
 // Which kernel serves.  w8_narrow.cuh begins 5 us earlier than w8_wide.cuh, but takes W through the SMs once
-// per 32 rows of x and widens x once per 16 rows of W.  Narrow and wide, us: 8 rows of 117 MB 23 and 28;
-// 16 rows of 25 MB 9.3 and 14.8, 59 MB 21.6 and 22.9, 79 MB 21.5 and 20.7, 117 MB 29 and 27; 32 rows of 17 MB
-// 8.5 and 12.8, 25 MB 15.5 and 15.2, 79 MB 36 and 21; 128 rows of 4 MB 9.5 and 10.7; 400 rows of 1 MB 9.3
-// and 10.6, 800 rows 16 and 11.
-constexpr int64_t kW8Narrow16 = 64 << 20, kW8Narrow = 24 << 20;
+// per 32 rows of x and widens x once per 16 rows of W.  Narrow and wide, us: 8 rows of 117 MB 24 and 27;
+// 16 rows of 25 MB 7.9 and 14.1, 59 MB 16.8 and 21.7, 63 MB 19.3 and 17.6, 117 MB 31 and 27.  From 17 rows on
+// an SM holds one narrow CTA, whose time goes by K; the wide kernel joins its sums where K is long: 32 rows
+// of 17 MB 8.4 and 12.7, 25 MB 12.1 and 14.3, 29 MB in rows of 14336 13.2 and 17.6, 17 MB in rows of 1024 14.4
+// and 7.7; 128 rows of 1024 x 4096 8.3 and 12.2, of 2048 x 4096 15.8 and 13.4; 400 rows of 1 MB 8.4 and 12.3.
+// A call that is narrow is so for fewer rows too: a workspace serves those.
+constexpr int64_t kW8Narrow16 = 58 << 20;
 bool narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
     if (T <= 8) return true;
-    int64_t bytes = 0;
-    for (int32_t i = 0; i < nprob; ++i) bytes += (int64_t)probs[i].N * probs[i].K;
-    return T <= 16 ? bytes <= kW8Narrow16 : bytes * ((T + 31) / 32) <= kW8Narrow;
+    int64_t bytes = 0, tiles = 0, k = 0;
+    for (int32_t i = 0; i < nprob; ++i) {
+        bytes += (int64_t)probs[i].N * probs[i].K;
+        tiles += (probs[i].N + kW8Rows - 1) / kW8Rows;
+        k = std::max<int64_t>(k, probs[i].K);
+    }
+    if (bytes > kW8Narrow16) return false;
+    if (T <= 16) return true;
+    const int64_t turns = (tiles * ((T + 31) / 32) + 151) / 152;                      // CTAs of an SM, one by one
+    const int64_t narrow_ns = 2000 + turns * (1100 + k * 58 / 100);
+    const int64_t wide_ns = 4300 + std::min<int64_t>(7600, k * 34 / 10) + bytes / 10000;
+    return narrow_ns <= wide_ns;
 }
 
 // How a wide call is shared out.
@@ -167,8 +178,10 @@ lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, c
     p.T = T;
     p.nprob = nprob;
     int64_t total = 0;
+    uint64_t at = 0;
     for (int32_t i = 0; i < nprob; ++i) {
         const lora_w8_problem& pr = probs[i];
+        at |= (uintptr_t)pr.x | (uintptr_t)pr.w | (uint64_t)pr.ldx | (uint64_t)pr.K;
         p.prob[i] = {reinterpret_cast<const unsigned char*>(pr.x), pr.x_scales, reinterpret_cast<__nv_bfloat16*>(pr.y),
                      reinterpret_cast<const unsigned char*>(pr.w), pr.w_scales, pr.ldx, pr.ldy, pr.N, pr.K, (int32_t)total};
         total += (pr.N + kW8Rows - 1) / kW8Rows;
@@ -176,9 +189,17 @@ lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, c
     p.total = (int32_t)total;
     const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
     const dim3 grid((unsigned)total, (unsigned)((T + 31) / 32));
-    if (nt == 1) w8_narrow_kernel<1, MAX><<<grid, kW8Threads, 0, s>>>(p);
-    else if (nt == 2) w8_narrow_kernel<2, MAX><<<grid, kW8Threads, 0, s>>>(p);
-    else w8_narrow_kernel<4, MAX><<<grid, kW8Threads, 0, s>>>(p);
+    const bool by32 = at % 32 == 0;
+    if (nt == 1) {
+        if (by32) w8_narrow_kernel<1, MAX, true><<<grid, kW8Threads, 0, s>>>(p);
+        else w8_narrow_kernel<1, MAX, false><<<grid, kW8Threads, 0, s>>>(p);
+    } else if (nt == 2) {
+        if (by32) w8_narrow_kernel<2, MAX, true><<<grid, kW8Threads, 0, s>>>(p);
+        else w8_narrow_kernel<2, MAX, false><<<grid, kW8Threads, 0, s>>>(p);
+    } else {
+        if (by32) w8_narrow_kernel<4, MAX, true><<<grid, kW8Threads, 0, s>>>(p);
+        else w8_narrow_kernel<4, MAX, false><<<grid, kW8Threads, 0, s>>>(p);
+    }
     return cuda_status(cudaGetLastError());
 }
 

@@ -5,6 +5,13 @@
 // pipe, where they are exact: 1024 + 128 + c is the f16 with c + 128 in its last bits, and
 // 1152 comes off exactly.  Products of two codes have 15 bits; 1,024 of them sum exactly in
 // fp32 (2^24), after which the sums go on as integers: y is rounded from the exact sum.
+//
+// A CTA takes 16 rows of W over all of K, its eight warps 128 of K each in turn; their sums meet in
+// shared memory, and nothing waits for another CTA.  W and x come in pieces of 32 bytes a lane, a
+// request a sector: by 16 bytes 1 row of 4096 x 4096 takes 4.9 us and 13 rows of q, k, v (25 MB)
+// 10.2, by 32 bytes 4.1 (4.1 TB/s) and 7.5 (3.4 TB/s).  8 rows of 117 MB take 24.1 (4.9 TB/s): up to 8 rows
+// memory bounds it, and for the smallest the launch and the first data; beyond, the widening of x
+// for each 16 rows of W counts (16 rows of 117 MB 31).
 #pragma once
 #include "lora_w8.h"
 #include "mma_legacy.cuh"
@@ -15,7 +22,7 @@ namespace lora {
 constexpr int kW8Warps = 8;
 constexpr int kW8Threads = kW8Warps * 32;
 constexpr int kW8Rows = 16;        // rows of W of a tile
-constexpr int kW8Chunk = 64;       // K of a warp's step: 16 bytes a lane and row
+constexpr int kW8Chunk = 128;      // K of a warp's step: 32 bytes a lane and row
 
 struct W8Prob {
     const unsigned char* x;
@@ -44,18 +51,45 @@ __device__ __forceinline__ void codes8_f16(uint32_t w, uint32_t& lo, uint32_t& h
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(0x64806480u));
 }
 
-// By the column tiles: steps of a group, whose loads are on their way while the group before is
-// multiplied, and CTAs that an SM should hold (8 rows of two 14336 x 4096: groups of two and three
-// CTAs 23 us, four and two 27; 13 rows of q, k, v: one and four 9.2, two and two 9.8, four and one 10.9).
-__host__ __device__ constexpr int w8_group(int nt) { return nt == 1 ? 2 : 1; }
-__host__ __device__ constexpr int w8_ctas(int nt) { return nt == 1 ? 3 : nt == 2 ? 4 : 2; }
+// CTAs that an SM should hold, by the column tiles.
+__host__ __device__ constexpr int w8_ctas(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
 
-// Lane (g, t) = (lane / 4, lane % 4) takes the 16 bytes from k = 16 t of its row's 64: word j of
+// 32 bytes of a lane's row from k on, zeros past K (a multiple of 16); of STREAM the first-level cache keeps nothing.
+template <bool BY32, bool STREAM>
+__device__ __forceinline__ void w8_load(uint32_t (&v)[8], const unsigned char* row, int k, int K) {
+    if constexpr (BY32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0;
+        if (k >= K) return;
+        if constexpr (STREAM)
+            asm("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                : "l"(row + k));
+        else
+            asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                         : "l"(row + k));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const unsigned char* p = row + k + 4 * i;
+            const uint4 x = k + 4 * i >= K ? make_uint4(0, 0, 0, 0) : STREAM ? ld_stream16(p) : ld16(p);
+            v[i] = x.x;
+            v[i + 1] = x.y;
+            v[i + 2] = x.z;
+            v[i + 3] = x.w;
+        }
+    }
+}
+
+// Lane (g, t) = (lane / 4, lane % 4) takes the 32 bytes from k = 32 t of its row's 128: word j of
 // them are the two pairs that an MMA of 16 of K wants of the lane, for W and for x alike, so
-// that the order of K within the 64 is the same for both.
-template <int NT, int MAX>
+// that the order of K within the 128 is the same for both.  The next step's loads are on their
+// way while one is multiplied.  BY32: every row of x and W begins at a multiple of 32 bytes and is
+// loaded by 32 at a time; else by 16.
+template <int NT, int MAX, bool BY32>
 __global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(const __grid_constant__ W8Params<MAX> p) {
-    constexpr int G = w8_group(NT), kStride = kW8Warps * kW8Chunk;
+    constexpr int kStride = kW8Warps * kW8Chunk;
     __shared__ int32_t red[kW8Warps][8 * NT][kW8Rows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     int i = 0;
@@ -86,53 +120,42 @@ __global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(cons
                 acc[n][j] = 0.f;
             }
     };
-    struct Group {
-        uint4 a[G][2], b[G][NT];
+    struct Step {
+        uint32_t a[2][8], b[NT][8];
     };
-    // a group's words; what lies past K is zeros in W
-    auto load = [&](Group& q, int k0) {
+    // a step's words; what lies past K is zeros
+    auto load = [&](Step& q, int k) {
+        w8_load<BY32, true>(q.a[0], w0, k, K);
+        w8_load<BY32, true>(q.a[1], w1, k, K);
 #pragma unroll
-        for (int s = 0; s < G; ++s) {
-            const int k = k0 + s * kStride;
-            const bool in = k < K;
-            q.a[s][0] = in ? ld_stream16(w0 + k) : make_uint4(0, 0, 0, 0);
-            q.a[s][1] = in ? ld_stream16(w1 + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) q.b[s][n] = ld16(xr[n] + (in ? k : 0));
-        }
+        for (int n = 0; n < NT; ++n) w8_load<BY32, false>(q.b[n], xr[n], k, K);
     };
-    auto multiply = [&](const Group& q) {
+    auto multiply = [&](const Step& q) {
 #pragma unroll
-        for (int s = 0; s < G; ++s) {
-            const uint32_t aw0[4] = {q.a[s][0].x, q.a[s][0].y, q.a[s][0].z, q.a[s][0].w};
-            const uint32_t aw1[4] = {q.a[s][1].x, q.a[s][1].y, q.a[s][1].z, q.a[s][1].w};
+        for (int j = 0; j < 8; ++j) {
+            uint32_t a[4];
+            codes8_f16(q.a[0][j], a[0], a[2]);
+            codes8_f16(q.a[1][j], a[1], a[3]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t a[4];
-                codes8_f16(aw0[j], a[0], a[2]);
-                codes8_f16(aw1[j], a[1], a[3]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint32_t bw[4] = {q.b[s][n].x, q.b[s][n].y, q.b[s][n].z, q.b[s][n].w};
-                    uint32_t b0, b1;
-                    codes8_f16(bw[j], b0, b1);
-                    mma16816_f16(acc[n], a[0], a[1], a[2], a[3], b0, b1);
-                }
+            for (int n = 0; n < NT; ++n) {
+                uint32_t b0, b1;
+                codes8_f16(q.b[n][j], b0, b1);
+                mma16816_f16(acc[n], a[0], a[1], a[2], a[3], b0, b1);
             }
         }
     };
-    Group q[2];
-    const int k0 = warp * kW8Chunk + 16 * t, end = K + 16 * t;  // a warp's lanes end together
+    Step q[2];
+    const int k0 = warp * kW8Chunk + 32 * t, end = K + 32 * t;      // a warp's lanes end together
     load(q[0], k0);
     int steps = 0;
     for (int k = k0; k < end;) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             if (h == 1 && k >= end) break;
-            if (k + G * kStride < end) load(q[1 - h], k + G * kStride);
+            if (k + kStride < end) load(q[1 - h], k + kStride);
             multiply(q[h]);
-            k += G * kStride;
-            if ((steps += G) == 1024 / kW8Chunk) {
+            k += kStride;
+            if (++steps == 1024 / kW8Chunk) {
                 flush();
                 steps = 0;
             }

@@ -103,6 +103,26 @@ def test_model_widths(cuda, T):
         check(cuda, p)
 
 
+@pytest.mark.parametrize("T", [1, 8, 13, 16, 20, 32, 33, 70])
+@pytest.mark.parametrize("N,K", [(264, 1040), (4096, 1024), (40, 96), (512, 4096)])
+def test_rows_at_any_multiple_of_16_bytes(cuda, T, N, K):
+    """Rows that begin 16 bytes past a multiple of 32, of x, of W or of both, give the bits of rows that do not."""
+    g = cuda.Generator(device="cuda").manual_seed(T + K)
+    a = problem(cuda, g, T, N, K)
+    call(cuda, [a], T)
+    check(cuda, a)
+    for move_x, move_w, pad in ((True, False, 0), (False, True, 0), (False, False, 16), (True, True, 32)):
+        b = dict(a, y=cuda.full_like(a["y"], 7.0))
+        store = cuda.full((T * (K + pad) + 32,), 99, dtype=cuda.int8, device="cuda")
+        b["x"] = store[16 * move_x:][:T * (K + pad)].view(T, K + pad)
+        b["x"][:, :K] = a["x"][:, :K]
+        store = cuda.full((N * K + 32,), 99, dtype=cuda.int8, device="cuda")
+        b["w"] = store[16 * move_w:][:N * K].view(N, K)
+        b["w"].copy_(a["w"])
+        call(cuda, [b], T)
+        assert cuda.equal(a["y"].view(cuda.int16), b["y"].view(cuda.int16))
+
+
 @pytest.mark.parametrize("T", [1, 12, 40, 64, 200, 300])
 @pytest.mark.parametrize("a,b", [(-128, -128), (-128, 127), (127, 127)])
 def test_largest_codes(cuda, T, a, b):
