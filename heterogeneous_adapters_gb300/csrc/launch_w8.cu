@@ -114,41 +114,49 @@ struct WideShape {
 };
 constexpr int wide_max(int cols) { return cols <= 64 ? 64 : cols <= 128 ? 128 : 256; }
 
-// The tiles of up to 64, 128 or 256 columns, whole or in equal shares of all steps, that should take the
-// fewest clocks: a step of c columns takes 4 c for its MMAs, 640 for its widening, and 870 for its W from
-// memory where all pairs stream and no other tile has fetched it; joining a tile from several pairs
-// some 8,000 + 60 c (200 rows of three 5120 x 5120: 28 us in whole tiles of 224 columns, 40 steps a
-// pair, 35 in shares of 32).  A share is not so small that a tile has many parts (35 rows of 184 x
-// 6400: 28 us in 50 parts, 13 in 9; 100 rows of 4096 x 4096 19 in 6, 15 in 4).
+// The number of tiles along x, whole or in equal shares of all steps, that should take the fewest clocks: a
+// step of c columns takes 4 c for its MMAs, 620 for its widening, and 870 for its W from memory where
+// all pairs stream and no other tile has fetched it; a tile of more than 128 columns, whose sums leave before
+// the next one's begin, 5,000 at its end; joining a tile from several pairs 6,000 + 100 c, and
+// 18 c for each part past the second.  us: 700 rows of 4096 x 14336 63 in shares of tiles of 256, 56 in whole ones of 192, 58 in shares
+// of 160; 300 rows 36 in shares of 160, 46 whole, 41 in whole ones of 128; 500 rows of it 50 in
+// shares of 256, 43 in whole ones of 128; 200 rows of three 5120 x 5120 29 in whole tiles of 224, 35 in
+// shares of them, 34 in whole ones of 128; 600 rows of two 14336 x 4096 90 in shares of 224, 86 in whole ones
+// of 160.  A share is not so small that a tile has many parts (35 rows of 184 x 6400: 28 us in 50 parts,
+// 13 in 9; 100 rows of 4096 x 4096 19 in 6, 15 in 4).
 WideShape wide_shape(const lora_w8_problem* probs, int32_t nprob, int32_t T, int pairs) {
     WideShape best = {0, 0, 0, false};
-    int64_t least = INT64_MAX;
-    for (const int most : {64, 128, 256}) {
-        const int ttiles = (T + most - 1) / most, cols = ((T + ttiles - 1) / ttiles + 31) / 32 * 32;
-        int64_t tiles = 0, steps = 0;
-        int32_t kb = 0;
-        bool one_k = true;
-        for (int32_t i = 0; i < nprob; ++i) {
-            const int32_t k = (probs[i].K + kW8WideK - 1) / kW8WideK;
-            const int64_t n = (int64_t)((probs[i].N + kW8WideRows - 1) / kW8WideRows) * ttiles;
-            one_k = one_k && (i == 0 || k == kb);
-            kb = std::max(kb, k);
-            tiles += n;
-            steps += n * k;
-        }
+    int64_t least = INT64_MAX, rows = 0, blocks = 0;               // tiles along W, and their steps
+    int32_t kb = 0;
+    bool one_k = true;
+    for (int32_t i = 0; i < nprob; ++i) {
+        const int32_t k = (probs[i].K + kW8WideK - 1) / kW8WideK;
+        const int64_t n = (probs[i].N + kW8WideRows - 1) / kW8WideRows;
+        one_k = one_k && (i == 0 || k == kb);
+        kb = std::max(kb, k);
+        rows += n;
+        blocks += n * k;
+    }
+    const int fewest = (T + 255) / 256, most = (T + 63) / 64;
+    for (const int ttiles : {fewest, fewest + 1, fewest + 2, fewest + 3, (T + 127) / 128, most}) {
+        if (ttiles > most) continue;
+        const int cols = ((T + ttiles - 1) / ttiles + 31) / 32 * 32;
+        const int64_t tiles = rows * ttiles, steps = blocks * ttiles, drain = cols > 128 ? 5000 : 0;
         auto clocks = [&](int64_t per) {
             const int64_t busy = std::min<int64_t>(pairs, (steps + per - 1) / per);
-            return per * std::max<int64_t>({640, 4 * cols, 870 * busy / pairs / ttiles});
+            return per * std::max<int64_t>({620, 4 * cols, 870 * busy / pairs / ttiles});
         };
         const int64_t share = std::max<int64_t>((steps + pairs - 1) / pairs, cols <= 64 ? 6 : 10);
-        const int64_t in_shares = clocks(share) + 8000 + 60 * cols;
+        const int64_t in_shares = clocks(share) + 6000 + 100 * cols + std::max<int64_t>(share / kb - 1, 0) * drain +
+                                  std::max<int64_t>(kb - 2 * share, 0) * 18 * cols / share;
         if (in_shares < least) {
             least = in_shares;
             best = {cols, ttiles, (int32_t)std::min<int64_t>(share, INT32_MAX), true};
         }
         const int64_t whole = (tiles + pairs - 1) / pairs * kb;
-        if (one_k && clocks(whole) < least) {
-            least = clocks(whole);
+        const int64_t as_whole = clocks(whole) + std::max<int64_t>(whole / kb * drain, 2000);
+        if (one_k && as_whole < least) {
+            least = as_whole;
             best = {cols, ttiles, (int32_t)std::min<int64_t>(whole, INT32_MAX), false};
         }
     }
@@ -253,7 +261,7 @@ lora_status launch_wide(const W8WideParams& w, int pairs, cudaStream_t s) {
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * std::min(pairs, (w.total + w.per - 1) / w.per));
+    cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(kW8WideThreads);
     cfg.dynamicSmemBytes = w8_wide_smem(NMAX);
     cfg.attrs = &early;
@@ -308,7 +316,6 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
     w.err = &reinterpret_cast<WsHeader*>(ws)->err;
     w.limit_ns = limit_ns;
     w.lost = lost;
-    w.per = sh.per;
     char* at = base + align256(kStepPartAt) + w8_part_bytes(nmax);
     int32_t copies = 0, slot[LORA_W8_MAX_PROBLEMS];
     int64_t total = 0, most = 0;
@@ -336,6 +343,19 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
         if (total > (1 << 30)) return LORA_ETOOBIG;
     }
     w.total = (int32_t)total;
+    pairs = std::min(pairs, (w.total + sh.per - 1) / sh.per);
+    w.per = sh.per;
+    if (!sh.split) {
+        const int32_t kb = w.prob[0].kblocks, tiles = w.total / kb;
+        w.per = tiles / pairs;
+        w.more = tiles % pairs;
+        w.over_rt = pairs / sh.ttiles;
+        w.over_tt = pairs % sh.ttiles;
+        if (lost >= 0) {
+            w.lost_pair = lost / kb % pairs;
+            w.lost = lost / kb / pairs * kb + lost % kb;
+        }
+    }
     DeviceInfo* di = nullptr;
     if ((st = device_info(&di)) != LORA_OK) return st;
     const int64_t blocks = std::min<int64_t>((most + kWidenThreads - 1) / kWidenThreads, std::max(di->sm_count * 8 / copies, 1));

@@ -12,14 +12,15 @@
 //
 // Warp 0 streams W (128 rows x 128 of K a CTA and step) and warp 2 x by TMA, warps 4 to 11
 // widen W into tensor memory, warp 1 of the even CTA issues the MMAs of both, warps 12 to 19
-// take the sums out.  The pairs take equal contiguous ranges of the steps of all tiles, or
-// whole tiles; a tile shared by several pairs is joined over partial sums in the workspace by
-// the one that arrives last, in the order of K.
+// take the sums out.  The pairs take equal contiguous ranges of the steps of all tiles, or whole
+// tiles in turn, so that neighbours work on the same W at a time (300 rows of two 14336 x 4096:
+// 49 us with a pair's tiles in a row, 46 in turn); a tile shared by several pairs is joined over
+// partial sums in the workspace by the one that arrives last, in the order of K.
 //
-// 64 rows of 117 MB take 27 us (4.4 TB/s): TMA boxes of 128 bytes of 128 rows stream at 5.3 TB/s alone, and
-// the start takes 4.9 us to the first W.  2,011 rows of two 14336 x 4096 take 240 us (1.97 PFLOP/s, the
-// tensor pipe busy 92% of the time), 700 rows of 4096 x 14336 63, of which x's widening 5 and the
-// joining of shared tiles some 10.
+// 64 rows of 117 MB take 27 us (4.4 TB/s): TMA boxes of 128 bytes of 128 rows stream at 5.3 TB/s alone,
+// and the start takes 4.9 us to the first W.  2,011 rows of two 14336 x 4096 take 236 us (2.0 PFLOP/s,
+// the tensor pipe busy 92% of the time), 700 rows of 4096 x 14336 55.7 (1.48 PFLOP/s: 64 tiles for 76
+// pairs, and 5 us of x's widening before them).
 #pragma once
 #include <cuda.h>
 
@@ -66,12 +67,14 @@ struct W8WideParams {
     int32_t cols;                              // rows of x of a tile, a multiple of 32 as an MMA over two CTAs takes them
     int32_t ttiles;                            // tiles along x
     int32_t total;                             // steps
-    int32_t per;                               // steps of a pair
+    int32_t per;                               // shares: steps of a pair; whole tiles: its tiles, of the first `more` pairs one more
+    int32_t more;
+    int32_t over_rt, over_tt;                  // whole tiles: from a pair's tile to its next, along W and along x
     uint32_t* tickets;                         // [kStepTickets], zero between calls
     float* part;
     uint32_t* err;
     uint64_t limit_ns;                         // of every wait
-    int32_t lost;                              // a step whose W never comes (a test of the waits), or -1
+    int32_t lost, lost_pair;                   // a step whose W never comes (a test of the waits), or -1; whole tiles: of that pair's
 };
 
 // ---------------------------------------------------------------------------- x in f16
@@ -184,14 +187,24 @@ __device__ __forceinline__ W8At w8_at(const W8WideParams& p, int u) {
     a.tt = tile - a.rt * p.ttiles;
     return a;
 }
-__device__ __forceinline__ void w8_next(const W8WideParams& p, W8At& a) {
-    if (++a.kb < p.prob[a.prob].kblocks) return;
+// A pair's next tile: the next one of all, or of whole tiles, which go to the pairs in turn, the one past the others'.
+template <bool SPLIT>
+__device__ __forceinline__ void w8_next_tile(const W8WideParams& p, W8At& a) {
     a.kb = 0;
-    if (++a.tt < p.ttiles) return;
-    a.tt = 0;
-    if (++a.rt * kW8WideRows < p.prob[a.prob].N) return;
-    a.rt = 0;
-    ++a.prob;
+    a.tt += SPLIT ? 1 : p.over_tt;
+    if (!SPLIT) a.rt += p.over_rt;
+    if (a.tt >= p.ttiles) {
+        a.tt -= p.ttiles;
+        ++a.rt;
+    }
+    while (a.prob < p.nprob && a.rt * kW8WideRows >= p.prob[a.prob].N) {
+        a.rt -= (p.prob[a.prob].N + kW8WideRows - 1) / kW8WideRows;
+        ++a.prob;
+    }
+}
+template <bool SPLIT>
+__device__ __forceinline__ void w8_next(const W8WideParams& p, W8At& a) {
+    if (++a.kb == p.prob[a.prob].kblocks) w8_next_tile<SPLIT>(p, a);
 }
 
 // Sixteen columns' sums as bf16 pairs of y.
@@ -252,7 +265,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cta_rank();
     const int pair = blockIdx.x >> 1;
-    const int first = min(pair * p.per, p.total), end = min(first + p.per, p.total);
+    // The steps of this pair: of all tiles' steps, or counted within its own whole tiles
+    const int blocks = p.prob[0].kblocks;
+    const int first = SPLIT ? min(pair * p.per, p.total) : 0;
+    const int end = SPLIT ? min(first + p.per, p.total) : (p.per + (pair < p.more)) * blocks;
+    const int start = SPLIT ? first : pair * blocks;
     const int half_cols = p.cols / 2;
     auto bar = [](uint64_t& b) { return smem_addr(&b); };
     if (tid < kWStages) {
@@ -292,9 +309,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         // ------------------------------------------------------------------ W, one thread
         regs_dec<kRegsMisc>();
         if (lane == 0) {
-            W8At a = w8_at(p, first);
+            W8At a = w8_at(p, start);
+            const int lost = SPLIT || pair == p.lost_pair ? p.lost : -1;
             uint32_t i = 0;
-            for (int u = first; u < end && u != p.lost; ++u, w8_next(p, a), ++i) {
+            for (int u = first; u < end && u != lost; ++u, w8_next<SPLIT>(p, a), ++i) {
                 const uint32_t s = i % kWStages;
                 if (!mbar_wait_quiet(bar(w_empty[s]), ((i / kWStages) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
                 mbar_arrive_expect_tx(bar(w_full[s]), kW8WBytes);
@@ -311,10 +329,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         regs_dec<kRegsMisc>();
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            W8At a = w8_at(p, first);
+            W8At a = w8_at(p, start);
             uint32_t i = 0;
             const uint32_t box = half_cols * 128;
-            for (int u = first; u < end; ++u, w8_next(p, a), ++i) {
+            for (int u = first; u < end; ++u, w8_next<SPLIT>(p, a), ++i) {
                 const uint32_t b = i % kW8Bufs;
                 if (!mbar_wait_quiet(bar(freed[b]), ((i / kW8Bufs) & 1) ^ 1, p.limit_ns)) { ok = false; break; }
                 const uint32_t at = mapa(bar(ready[b]), 0);
@@ -338,13 +356,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
             const uint32_t idesc = (1u << 4) | ((uint32_t)(p.cols >> 3) << 17) | ((256u >> 4) << 24);   // f16, fp32 sums
             const uint64_t x_desc = smem_desc(x0, 16, 1024, 2);
             const uint32_t box = half_cols * 128;
-            W8At a = w8_at(p, first);
+            W8At a = w8_at(p, start);
             uint32_t i = 0, tiles = 0;
             bool fresh = true;
             for (int u = first; u < end && ok; ++u, ++i) {
                 const uint32_t b = i % kW8Bufs;
                 const bool last = a.kb + 1 == p.prob[a.prob].kblocks || u + 1 == end;
-                w8_next(p, a);
+                w8_next<SPLIT>(p, a);
                 const uint32_t d = tiles % kDs;
                 if (fresh && !wait(d_empty[d], ((tiles / kDs) & 1) ^ 1)) { ok = false; break; }
                 if (!wait(ready[b], (i / kW8Bufs) & 1)) { ok = false; break; }
@@ -412,12 +430,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         const uint32_t dcol0 = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
         const int chunks = half_cols / 16;
         auto meet = [&]() { named_bar_sync(1 + half, 128); };
-        W8At a = w8_at(p, first);
+        W8At a = w8_at(p, start);
         uint32_t tiles = 0;
         for (int at = first; at < end; ++tiles) {
             const W8WideProb& pr = p.prob[a.prob];
             const uint32_t d = tiles % kDs, dcol = dcol0 + d * 128;
-            const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = min(tile_end, end);
+            const int tile_first = at - a.kb, tile_end = tile_first + pr.kblocks, stop = SPLIT ? min(tile_end, end) : tile_end;
             const int row0 = a.rt * kW8WideRows + (int)rank * 128, col0 = a.tt * p.cols + half * half_cols;
             const bool whole = !SPLIT || (at == tile_first && stop == tile_end);
             const float sw = row0 + r < pr.N ? pr.w_scales[row0 + r] : 0.f;
@@ -568,7 +586,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
                 meet();
             }
             at = stop;
-            if (at < end) a = w8_at(p, at);
+            if (SPLIT && at < end) a = w8_at(p, at);
+            if (!SPLIT) w8_next_tile<false>(p, a);
         }
         if (!ok && lane == 0) set_error(p.err, LORA_DERR_TIMEOUT);
     } else {

@@ -180,6 +180,38 @@ def test_the_workspace_serves_on_after_a_wait_that_ran_out(cuda, T, N, K, step):
         check(cuda, p)
 
 
+
+@pytest.mark.parametrize("step", [0, 200, 1000])
+def test_the_workspace_serves_on_after_a_wait_in_one_of_many_tiles(cuda, step):
+    """Several whole tiles a pair, the step that never comes in its first, a later or its last one."""
+    g = cuda.Generator(device="cuda").manual_seed(step)
+    T, ps = 300, []
+    for N in (32776, 264, 8):
+        ps.append(problem(cuda, g, T, N, 400, x=ps[0] if ps else None))
+    pr = problems(ps)
+    ws, size = workspace(cuda, pr, T)
+    stream = cuda.cuda.current_stream().cuda_stream
+    lora.debug_w8_lost_step(pr, T, step, 5_000_000, ws, size, stream)
+    assert lora.get_device_error(ws, stream) == 0x20
+    for _ in range(2):
+        lora.w8_matmul(pr, T, ws, size, stream)
+        assert lora.get_device_error(ws, stream) == 0
+        for p in ps:
+            check(cuda, p)
+
+
+@pytest.mark.parametrize("T", [33, 64, 100, 130, 257, 300, 520, 700, 1030])
+@pytest.mark.parametrize("K", [16, 400, 1040])
+def test_many_tiles_of_projections_of_one_length(cuda, T, K):
+    """Projections of one tile and of many, all with as many blocks of K: whole tiles, one pair's in several projections."""
+    g = cuda.Generator(device="cuda").manual_seed(T + K)
+    a = problem(cuda, g, T, 264, K)
+    ps = [a, problem(cuda, g, T, 20488, K, x=a), problem(cuda, g, T, 8, K), problem(cuda, g, T, 16, K, x=a), problem(cuda, g, T, 5128, K, pad=8)]
+    call(cuda, ps, T)
+    for p in ps:
+        check(cuda, p)
+
+
 def test_lost_step_refusals(cuda):
     from heterogeneous_adapters_gb300 import _binding as B
     g = cuda.Generator(device="cuda").manual_seed(1)
