@@ -138,9 +138,9 @@ WideShape wide_shape(const lora_w8_problem* probs, int32_t nprob, int32_t T, int
         blocks += n * k;
     }
     const int fewest = (T + 255) / 256, most = (T + 63) / 64;
-    for (const int ttiles : {fewest, fewest + 1, fewest + 2, fewest + 3, (T + 127) / 128, most}) {
-        if (ttiles > most) continue;
-        const int cols = ((T + ttiles - 1) / ttiles + 31) / 32 * 32;
+    for (const int about : {fewest, fewest + 1, fewest + 2, fewest + 3, (T + 127) / 128, most}) {
+        if (about > most) continue;
+        const int cols = ((T + about - 1) / about + 31) / 32 * 32, ttiles = (T + cols - 1) / cols;
         const int64_t tiles = rows * ttiles, steps = blocks * ttiles, drain = cols > 128 ? 5000 : 0;
         auto clocks = [&](int64_t per) {
             const int64_t busy = std::min<int64_t>(pairs, (steps + per - 1) / per);

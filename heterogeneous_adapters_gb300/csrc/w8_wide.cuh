@@ -296,6 +296,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    if (tid == 352 || tid == 384) {                            // the first tile's maps, on their way meanwhile
+        const W8At a = w8_at(p, start);
+        prefetch_tmap(tid == 352 ? &p.w[a.prob] : &p.x[p.prob[a.prob].xi]);
+    }
     tc_fence_before();
     cluster_sync();                                            // nothing is fetched before: W's loads delay all others
     tc_fence_after();
