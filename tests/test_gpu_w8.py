@@ -78,6 +78,16 @@ def test_one_large_projection(cuda, T, N, K):
     check(cuda, p)
 
 
+
+@pytest.mark.parametrize("T", [5000, 40001, lora.LORA_W8_MAX_ROWS])
+@pytest.mark.parametrize("N,K", [(8, 16), (264, 80), (520, 1040)])
+def test_the_most_rows(cuda, T, N, K):
+    g = cuda.Generator(device="cuda").manual_seed(T + N)
+    p = problem(cuda, g, T, N, K, pad=8)
+    call(cuda, [p], T)
+    check(cuda, p)
+
+
 @pytest.mark.parametrize("T", [1, 5, 24, 40, 64, 130, 257, 700])
 def test_projections_of_different_shapes_in_one_call(cuda, T):
     g = cuda.Generator(device="cuda").manual_seed(T)
