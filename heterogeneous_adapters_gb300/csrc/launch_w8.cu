@@ -42,6 +42,25 @@ Q8Out out_of(const lora_q8_rows& o) {
             o.x_kind == LORA_Q8_X_FULL};
 }
 
+// A launch that is made ready while the kernel before it in the stream still runs; the kernel waits for that one's end by
+// grid_wait().  In a graph, us: one row of 4096 x 4096 4.2 -> 3.9, 8,191 rows of the norm 49.5 -> 49.0; called one behind
+// the other 13 rows of q, k, v 10.4 -> 7.4, 2,339 gated rows 41.4 -> 38.9, 64 rows of 117 MB 29.5 -> 27.5.  Where the few-row
+// kernel lets the next one begin while it runs, that one's CTAs take uneven places: 3.9 -> 5.0, 7.1 -> 7.9.
+template <typename P>
+lora_status launch_early(void (*kern)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    cfg.stream = s;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, p));
+}
+
 // Threads of a row, and CTAs: every row its own while the SMs hold them all, else as many as the
 // SMs hold (1,024 threads, at the kernels' 64 registers), each with rows in turn.
 template <typename K, typename P>
@@ -50,8 +69,7 @@ lora_status launch_rows(K kern, const P& q, int v, cudaStream_t s) {
     lora_status st = device_info(&di);
     if (st != LORA_OK) return st;
     const int threads = ((q.d / 8 + v - 1) / v + 31) / 32 * 32;
-    kern<<<std::min(q.T, di->sm_count * std::max(1024 / threads, 1)), threads, 0, s>>>(q);
-    return cuda_status(cudaGetLastError());
+    return launch_early(kern, dim3(std::min(q.T, di->sm_count * std::max(1024 / threads, 1))), threads, 0, s, q);
 }
 
 // Eights of a row that a thread holds, by measured times: a norm's weights fit beside one of them and
@@ -198,17 +216,10 @@ lora_status run_narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T, c
     const int nt = T <= 8 ? 1 : T <= 16 ? 2 : 4;
     const dim3 grid((unsigned)total, (unsigned)((T + 31) / 32));
     const bool by32 = at % 32 == 0;
-    if (nt == 1) {
-        if (by32) w8_narrow_kernel<1, MAX, true><<<grid, kW8Threads, 0, s>>>(p);
-        else w8_narrow_kernel<1, MAX, false><<<grid, kW8Threads, 0, s>>>(p);
-    } else if (nt == 2) {
-        if (by32) w8_narrow_kernel<2, MAX, true><<<grid, kW8Threads, 0, s>>>(p);
-        else w8_narrow_kernel<2, MAX, false><<<grid, kW8Threads, 0, s>>>(p);
-    } else {
-        if (by32) w8_narrow_kernel<4, MAX, true><<<grid, kW8Threads, 0, s>>>(p);
-        else w8_narrow_kernel<4, MAX, false><<<grid, kW8Threads, 0, s>>>(p);
-    }
-    return cuda_status(cudaGetLastError());
+    void (*kern)(W8Params<MAX>) = nt == 1 ? (by32 ? w8_narrow_kernel<1, MAX, true> : w8_narrow_kernel<1, MAX, false>)
+                                : nt == 2 ? (by32 ? w8_narrow_kernel<2, MAX, true> : w8_narrow_kernel<2, MAX, false>)
+                                          : (by32 ? w8_narrow_kernel<4, MAX, true> : w8_narrow_kernel<4, MAX, false>);
+    return launch_early(kern, grid, kW8Threads, 0, s, p);
 }
 
 // 2-D map of `rows` rows of `inner` elements, box {box0, box1}, zeros outside.
@@ -257,17 +268,7 @@ lora_status ready_wide(int* out) {
 
 template <int NMAX, bool SPLIT>
 lora_status launch_wide(const W8WideParams& w, int pairs, cudaStream_t s) {
-    cudaLaunchAttribute early;                         // it waits for w8_widen_kernel itself
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kW8WideThreads);
-    cfg.dynamicSmemBytes = w8_wide_smem(NMAX);
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    cfg.stream = s;
-    return cuda_status(cudaLaunchKernelEx(&cfg, w8_wide_kernel<NMAX, SPLIT>, w));
+    return launch_early(w8_wide_kernel<NMAX, SPLIT>, dim3(2 * pairs), kW8WideThreads, w8_wide_smem(NMAX), s, w);
 }
 
 template <int NMAX>
@@ -359,8 +360,7 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
     DeviceInfo* di = nullptr;
     if ((st = device_info(&di)) != LORA_OK) return st;
     const int64_t blocks = std::min<int64_t>((most + kWidenThreads - 1) / kWidenThreads, std::max(di->sm_count * 8 / copies, 1));
-    w8_widen_kernel<<<dim3((unsigned)blocks, (unsigned)copies), kWidenThreads, 0, s>>>(v);
-    st = cuda_status(cudaGetLastError());
+    st = launch_early(w8_widen_kernel, dim3((unsigned)blocks, (unsigned)copies), kWidenThreads, 0, s, v);
     if (st != LORA_OK) return st;
     if (nmax == 64) return launch_wide<64>(w, sh.split, pairs, s);
     return nmax == 128 ? launch_wide<128>(w, sh.split, pairs, s) : launch_wide<256>(w, sh.split, pairs, s);

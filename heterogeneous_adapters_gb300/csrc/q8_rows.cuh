@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(1024) q8_norm_kernel(const __grid_constant__ Q
 #pragma unroll
         for (int j = 0; j < V; ++j) fetch(row, j);
     };
+    grid_wait();
     if (PRE) fetch_row(blockIdx.x);
     float bad = 0.f;                                        // NaN where a weight is not finite
     // eight weights: kept where there are no more, else from the first-level cache
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(1024) q8_gate_kernel(const __grid_constant__ Q
 #pragma unroll
         for (int j = 0; j < V; ++j) fetch(row, j);
     };
+    grid_wait();
     if (PRE) fetch_row(blockIdx.x);
     int turn = 0;
     for (int64_t row = blockIdx.x; row < q.T; row += gridDim.x, turn ^= 1) {

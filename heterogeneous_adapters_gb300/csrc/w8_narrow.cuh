@@ -62,7 +62,7 @@ __device__ __forceinline__ void w8_load(uint32_t (&v)[8], const unsigned char* r
         for (int i = 0; i < 8; ++i) v[i] = 0;
         if (k >= K) return;
         if constexpr (STREAM)
-            asm("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                 : "l"(row + k));
         else
@@ -73,7 +73,7 @@ __device__ __forceinline__ void w8_load(uint32_t (&v)[8], const unsigned char* r
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
             const unsigned char* p = row + k + 4 * i;
-            const uint4 x = k + 4 * i >= K ? make_uint4(0, 0, 0, 0) : STREAM ? ld_stream16(p) : ld16(p);
+            const uint4 x = k + 4 * i >= K ? make_uint4(0, 0, 0, 0) : ld16(p);
             v[i] = x.x;
             v[i + 1] = x.y;
             v[i + 2] = x.z;
@@ -92,6 +92,7 @@ __global__ void __launch_bounds__(kW8Threads, w8_ctas(NT)) w8_narrow_kernel(cons
     constexpr int kStride = kW8Warps * kW8Chunk;
     __shared__ int32_t red[kW8Warps][8 * NT][kW8Rows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    grid_wait();
     int i = 0;
     while (i + 1 < p.nprob && (int)blockIdx.x >= p.prob[i + 1].first) ++i;
     const W8Prob& pr = p.prob[i];

@@ -90,7 +90,8 @@ constexpr int kWidenThreads = 256, kWidenAhead = 2;
 // Sixteen codes a thread and time, two times in flight; blockIdx.y: the matrix.  At most one CTA of
 // these for each that an SM holds: the next kernel begins when all have begun.
 __global__ void __launch_bounds__(kWidenThreads, 8) w8_widen_kernel(const __grid_constant__ W8Widen p) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();                               // W may be of the kernel before, and the next one does not wait to read it
+    grid_let_next();
     const int i = blockIdx.y;
     const uint32_t per_row = p.K[i] / 16, n = p.T * per_row, step = gridDim.x * kWidenThreads;   // n < 2^28
     for (uint32_t e = blockIdx.x * kWidenThreads + threadIdx.x; e < n; e += kWidenAhead * step) {
@@ -332,7 +333,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
         // ------------------------------------------------------------------ x, one thread
         regs_dec<kRegsMisc>();
         if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
+            grid_wait();
             W8At a = w8_at(p, start);
             uint32_t i = 0;
             const uint32_t box = half_cols * 128;

@@ -7,7 +7,7 @@ import pytest
 
 import heterogeneous_adapters_gb300 as lora
 
-from .test_gpu_w8 import call, check, problem, problems, workspace
+from .test_gpu_w8 import call, check, codes, problem, problems, workspace
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 sys.path.insert(0, os.path.join(ROOT, "examples"))
@@ -224,3 +224,66 @@ def test_lost_step_refusals(cuda):
             lora.debug_w8_lost_step(pr, T, step, limit, ws, size, 0)
         assert e.value.status == want
     assert bool((p["y"] == 7).all())
+
+
+@pytest.mark.parametrize("T", [1, 13, 40, 300])
+def test_calls_that_feed_each_other_wait_for_each_other(cuda, T):
+    """A chain of calls, each of which reads what the one before wrote and writes what the one before read, with
+    and without a wait of the host between them, in a graph, and with W written by the kernel before."""
+    g = cuda.Generator(device="cuda").manual_seed(T)
+    d, f = 1024, 2064
+    h0 = cuda.randn(T, d, generator=g, device="cuda").bfloat16()
+    weight = cuda.ones(d, dtype=cuda.bfloat16, device="cuda")
+    up_w, down_w = codes(cuda, g, f, d), codes(cuda, g, d, f)
+    up_s, down_s = (cuda.full((n,), 2.0 ** -12, device="cuda") for n in (f, d))
+    h, y = cuda.empty_like(h0), cuda.zeros(T, d, dtype=cuda.bfloat16, device="cuda")
+    xc, xs = cuda.empty(T, d, dtype=cuda.int8, device="cuda"), cuda.empty(T, device="cuda")
+    a, ac, as_ = cuda.empty(T, f, dtype=cuda.bfloat16, device="cuda"), cuda.empty(T, f, dtype=cuda.int8, device="cuda"), cuda.empty(T, device="cuda")
+    up_now = cuda.empty_like(up_w)
+    norm = lora.Q8Norm(h, d, y, d, h, d, weight, 1e-5, d, lora.Q8Rows(xc, d, xs, None, 0, lora.LORA_Q8_X_HELD))
+    gate = lora.Q8Gate(a, f, None, 0, lora.LORA_ACT_GELU, f, lora.Q8Rows(ac, f, as_, None, 0, lora.LORA_Q8_X_HELD))
+    up = lora.w8_problems([(xc, xs, a, d, f, up_now, up_s, f, d)])
+    down = lora.w8_problems([(ac, as_, y, f, d, down_w, down_s, d, f)])
+    size = max(lora.w8_workspace_size(up, T), lora.w8_workspace_size(down, T))
+    ws = cuda.empty(size, dtype=cuda.uint8, device="cuda")
+
+    def steps(stream, between=lambda: None, n=20):
+        h.copy_(h0)
+        y.zero_()
+        for i in range(n):
+            up_now.copy_(up_w if i % 2 else up_w.flip(0))
+            between()
+            lora.q8_norm(norm, T, stream)
+            between()
+            lora.w8_matmul(up, T, ws, size, stream)
+            between()
+            lora.q8_gate(gate, T, stream)
+            between()
+            lora.w8_matmul(down, T, ws, size, stream)
+            between()
+            up_now.zero_()
+            # W by the kernel right before
+            up_now.copy_(up_w)
+            lora.w8_matmul(up, T, ws, size, stream)
+            between()
+
+    side = cuda.cuda.Stream()
+    with cuda.cuda.stream(side):
+        s = side.cuda_stream
+        lora.kv_workspace_init(ws, size, s)
+        steps(s, side.synchronize)
+        want = [t.clone() for t in (h, y, a, ac)]
+        assert all(bool(cuda.isfinite(t.float()).all()) for t in want)
+        for _ in range(5):
+            steps(s)
+            for t, w in zip((h, y, a, ac), want):
+                assert cuda.equal(t, w)
+        graph = cuda.cuda.CUDAGraph()
+        side.synchronize()
+        with cuda.cuda.graph(graph, stream=side):
+            steps(side.cuda_stream)
+        for _ in range(5):
+            graph.replay()
+            for t, w in zip((h, y, a, ac), want):
+                assert cuda.equal(t, w)
+        assert lora.get_device_error(ws, s) == 0
