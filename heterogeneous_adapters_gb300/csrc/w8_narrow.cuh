@@ -8,8 +8,8 @@
 //
 // A CTA takes 16 rows of W over all of K, its eight warps 128 of K each in turn; their sums meet in
 // shared memory, and nothing waits for another CTA.  W and x come in pieces of 32 bytes a lane, a
-// request a sector: by 16 bytes 1 row of 4096 x 4096 takes 4.9 us and 13 rows of q, k, v (25 MB)
-// 10.2, by 32 bytes 4.1 (4.1 TB/s) and 7.5 (3.4 TB/s).  8 rows of 117 MB take 24.1 (4.9 TB/s): up to 8 rows
+// request a sector: by 16 bytes 1 row of 4096 x 4096 takes 4.0 us and 13 rows of q, k, v (25 MB)
+// 8.0, by 32 bytes 3.9 (4.3 TB/s) and 7.1 to 7.5 (3.4 TB/s).  8 rows of 117 MB take 23.7 (5.0 TB/s): up to 8 rows
 // memory bounds it, and for the smallest the launch and the first data; beyond, the widening of x
 // for each 16 rows of W counts (16 rows of 117 MB 31).
 #pragma once
@@ -54,7 +54,7 @@ __device__ __forceinline__ void codes8_f16(uint32_t w, uint32_t& lo, uint32_t& h
 // CTAs that an SM should hold, by the column tiles.
 __host__ __device__ constexpr int w8_ctas(int nt) { return nt == 1 ? 3 : nt == 2 ? 2 : 1; }
 
-// 32 bytes of a lane's row from k on, zeros past K (a multiple of 16); of STREAM the first-level cache keeps nothing.
+// 32 bytes of a lane's row from k on, zeros past K (a multiple of 16); STREAM: 32 at a time past the first-level cache.
 template <bool BY32, bool STREAM>
 __device__ __forceinline__ void w8_load(uint32_t (&v)[8], const unsigned char* row, int k, int K) {
     if constexpr (BY32) {

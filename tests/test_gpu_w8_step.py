@@ -287,3 +287,63 @@ def test_calls_that_feed_each_other_wait_for_each_other(cuda, T):
             for t, w in zip((h, y, a, ac), want):
                 assert cuda.equal(t, w)
         assert lora.get_device_error(ws, s) == 0
+
+
+@pytest.mark.parametrize("T", [1, 13, 40, 300])
+@pytest.mark.parametrize("first", ["call", "copy", "nothing"])
+def test_branches_of_streams_that_join(cuda, T, first):
+    """Calls behind two streams' work, eager and in one graph: each waits for both."""
+    g = cuda.Generator(device="cuda").manual_seed(T)
+    d, f = 1024, 2064
+    x, gin = (cuda.randn(T, n, generator=g, device="cuda").bfloat16() for n in (d, f))
+    weight = cuda.ones(d, dtype=cuda.bfloat16, device="cuda")
+    up_w, down_w = codes(cuda, g, f, d), codes(cuda, g, d, f)
+    up_s, down_s = (cuda.full((n,), 2.0 ** -12, device="cuda") for n in (f, d))
+    xc, xs = cuda.empty(T, d, dtype=cuda.int8, device="cuda"), cuda.empty(T, device="cuda")
+    ac, as_ = cuda.empty(T, f, dtype=cuda.int8, device="cuda"), cuda.empty(T, device="cuda")
+    y1, y2 = cuda.empty(T, f, dtype=cuda.bfloat16, device="cuda"), cuda.empty(T, d, dtype=cuda.bfloat16, device="cuda")
+    source = x.clone()
+    norm = lora.Q8Norm(x, d, None, 0, None, 0, weight, 1e-5, d, lora.Q8Rows(xc, d, xs, None, 0, lora.LORA_Q8_X_HELD))
+    gate = lora.Q8Gate(gin, f, None, 0, lora.LORA_ACT_SILU, f, lora.Q8Rows(ac, f, as_, None, 0, lora.LORA_Q8_X_HELD))
+    both = lora.w8_problems([(xc, xs, y1, d, f, up_w, up_s, f, d), (ac, as_, y2, f, d, down_w, down_s, d, f)])
+    size = lora.w8_workspace_size(both, T)
+    ws = cuda.empty(size, dtype=cuda.uint8, device="cuda")
+    main, side = cuda.cuda.Stream(), cuda.cuda.Stream()
+    outs = (xc, xs, ac, as_, y1, y2)
+
+    def run(wait=False):
+        if first == "copy":
+            x.copy_(source)
+        elif first == "call":
+            lora.q8_norm(norm, T, main.cuda_stream)
+        side.wait_stream(main)
+        lora.q8_gate(gate, T, side.cuda_stream)
+        lora.q8_norm(norm, T, main.cuda_stream)
+        main.wait_stream(side)
+        if wait:
+            main.synchronize()
+        lora.w8_matmul(both, T, ws, size, main.cuda_stream)
+        side.wait_stream(main)
+        lora.q8_gate(gate, T, side.cuda_stream)
+        main.wait_stream(side)
+        lora.w8_matmul(both, T, ws, size, main.cuda_stream)
+
+    with cuda.cuda.stream(main):
+        lora.kv_workspace_init(ws, size, main.cuda_stream)
+        run(True)
+        main.synchronize()
+        want = [t.clone() for t in outs]
+        for t in outs:
+            t.zero_()
+        run()
+        assert all(cuda.equal(t, w) for t, w in zip(outs, want))
+        graph = cuda.cuda.CUDAGraph()
+        main.synchronize()
+        with cuda.cuda.graph(graph, stream=main):
+            run()
+        for _ in range(3):
+            for t in outs:
+                t.zero_()
+            graph.replay()
+            assert all(cuda.equal(t, w) for t, w in zip(outs, want))
+        assert lora.get_device_error(ws, main.cuda_stream) == 0
