@@ -260,9 +260,18 @@ __global__ void __launch_bounds__(1024) q8_norm_kernel(const __grid_constant__ Q
     }
 }
 
-// act of a pair.  Every value that is not finite gives one that is not.
+// Of the forms with a quotient, a / (1 + e^-z): -z log2(e), z = a or that of (1 + tanh(z / 2)) / 2.
 template <int ACT>
-__device__ __forceinline__ uint64_t q8_act(uint64_t v) {
+__device__ __forceinline__ uint64_t q8_exponent(uint64_t v) {
+    const uint64_t z = mul2(v, pack2f(-1.44269504f, -1.44269504f));
+    if (ACT != LORA_ACT_GELU_TANH) return z;
+    constexpr float k = 2.f * 0.79788456f;
+    return mul2(z, fma2(mul2(v, v), pack2f(k * 0.044715f, k * 0.044715f), pack2f(k, k)));
+}
+
+// act of a pair; `most`: the largest e^-z so far.  Every value that is not finite gives one that is not.
+template <int ACT>
+__device__ __forceinline__ uint64_t q8_act(uint64_t v, float& most) {
     float a[2];
     unpack2f(v, a[0], a[1]);
     if (ACT == LORA_ACT_NONE) {
@@ -285,24 +294,39 @@ __device__ __forceinline__ uint64_t q8_act(uint64_t v) {
         const uint64_t below = mul2(mul2(mul2(f, s), t), pack2f(exp2_approx(e[0]), exp2_approx(e[1])));
         return fma2(below, pack2f(-1.f, -1.f), pack2f(fmaxf(a[0], 0.f), fmaxf(a[1], 0.f)));
     } else {
-        // a / (1 + e^-z): z = a, or (1 + tanh(z / 2)) / 2 with the z of the other form.  e^-z is right to 2^-24
-        // (4 + |z|) of itself; where it passes fp32's range, a e^z is nothing
-        uint64_t z = mul2(v, pack2f(-1.44269504f, -1.44269504f));
-        if (ACT == LORA_ACT_GELU_TANH) {
-            constexpr float k = 2.f * 0.79788456f;
-            z = mul2(z, fma2(mul2(v, v), pack2f(k * 0.044715f, k * 0.044715f), pack2f(k, k)));
-        }
+        // e^-z is right to 2^-24 (4 + 1.5 |z|) of itself
         float e[2];
-        unpack2f(z, e[0], e[1]);
-        unpack2f(add2(pack2f(exp2_approx(e[0]), exp2_approx(e[1])), pack2f(1.f, 1.f)), e[0], e[1]);
+        unpack2f(q8_exponent<ACT>(v), e[0], e[1]);
+        e[0] = exp2_approx(e[0]);
+        e[1] = exp2_approx(e[1]);
+        most = fmaxf(most, fmaxf(e[0], e[1]));
+        unpack2f(add2(pack2f(e[0], e[1]), pack2f(1.f, 1.f)), e[0], e[1]);
         return mul2(v, pack2f(rcp_approx(e[0]), rcp_approx(e[1])));
     }
+}
+// Above this e^-z the quotient leaves fp32's normal values before a e^z does (a of -87 and less: up to 2^-119.5): there
+// a e^z goes by two halves of the exponent.  Nothing is left below a of -103.
+constexpr float kQ8Tail = 0x1p125f;
+template <int ACT>
+__device__ __forceinline__ uint64_t q8_act_tail(uint64_t v) {
+    float most = 0.f, z[2], a[2], y[2];
+    unpack2f(q8_exponent<ACT>(v), z[0], z[1]);
+    unpack2f(v, a[0], a[1]);
+    unpack2f(q8_act<ACT>(v, most), y[0], y[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (z[i] > 125.f) {
+            const float h = exp2_approx(-0.5f * z[i]);
+            y[i] = a[i] * h * h;
+        }
+    return pack2f(y[0], y[1]);
 }
 
 template <int V, int ACT, bool PRE>
 __global__ void __launch_bounds__(1024) q8_gate_kernel(const __grid_constant__ Q8GateParams q) {
     __shared__ uint32_t red_top[2][32];
     __shared__ float red_ss[2][32];
+    constexpr bool kQuotient = ACT == LORA_ACT_SILU || ACT == LORA_ACT_GELU_TANH;
     const int tid = threadIdx.x;
     const bool gated = q.up != nullptr;
     uint4 an[V], un[V];
@@ -323,17 +347,31 @@ __global__ void __launch_bounds__(1024) q8_gate_kernel(const __grid_constant__ Q
     int turn = 0;
     for (int64_t row = blockIdx.x; row < q.T; row += gridDim.x, turn ^= 1) {
         uint64_t p[V][4], zeros = 0;                        // zeros: 0 y summed, NaN where a y is not finite
-        float top = 0.f;
+        float top = 0.f, most = 0.f;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if (!PRE) fetch(row, j);
             const uint32_t a[4] = {an[j].x, an[j].y, an[j].z, an[j].w}, u[4] = {un[j].x, un[j].y, un[j].z, un[j].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[j][i] = q8_act<ACT>(pair_of(a[i]));
+                p[j][i] = q8_act<ACT>(pair_of(a[i]), most);
                 if (gated) p[j][i] = mul2(p[j][i], pair_of(u[i]));
                 zeros = fma2(p[j][i], 0, zeros);
                 top = max_pair(p[j][i], top);
+            }
+        }
+        if (kQuotient && most > kQ8Tail) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (!PRE) fetch(row, j);                    // nothing of the row is written yet
+                const uint32_t a[4] = {an[j].x, an[j].y, an[j].z, an[j].w}, u[4] = {un[j].x, un[j].y, un[j].z, un[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    p[j][i] = q8_act_tail<ACT>(pair_of(a[i]));
+                    if (gated) p[j][i] = mul2(p[j][i], pair_of(u[i]));
+                    zeros = fma2(p[j][i], 0, zeros);
+                    top = max_pair(p[j][i], top);
+                }
             }
         }
         if (PRE) fetch_row(row + gridDim.x);

@@ -63,7 +63,8 @@ typedef struct {
     lora_q8_rows out;
 } lora_q8_norm_desc;
 
-/* The gated activation: y = act(gate) up (act(gate) without up), in fp32, left in 8 bits. */
+/* The gated activation: y = act(gate) up (act(gate) without up), in fp32, left in 8 bits.  act(gate) is right to a
+ * share of its own size (up to 4e-5 where it is smallest); one below 2^-126 may be 0. */
 enum { LORA_ACT_NONE = 0, LORA_ACT_SILU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3 };
 typedef struct {
     const void* gate;            /* bf16 [T][ldg]                                           */

@@ -34,9 +34,11 @@ def check_close(torch, gate, up, act, kind=lora.LORA_Q8_X_HELD):
     codes, scales, xo = run_gate(torch, gate, up, act, kind)
     y = value(torch, act, gate.double())
     tol = (roundings(torch, act, gate.double()) + 1) * U      # and the product with up
+    # below the smallest normal value, 2^-126, an activation may be nothing, and so may y's digits (bf16's steps are 2^-133 there)
+    least = torch.full_like(y, 2.0 ** -126)
     if up is not None:
-        y = y * up.double()
-    tol = tol * y.abs() + 2.0 ** -126                         # below fp32's smallest normal value it is nothing
+        y, least = y * up.double(), least * up.double().abs().clamp(min=1)
+    tol = tol * y.abs() + least
     top, at = y.abs().max(1)
     slack = tol.gather(1, at[:, None])[:, 0]
     assert bool(((scales.double() * 127 - top).abs() <= 3 * U * top + torch.maximum(slack, tol.amax(1))).all())
@@ -49,7 +51,9 @@ def check_close(torch, gate, up, act, kind=lora.LORA_Q8_X_HELD):
         assert bool(((xo.double() - y).abs() <= 2.0 ** -8 * (y.abs() + tol) + tol).all())
 
 
-@pytest.mark.parametrize("act,low,high", [("gelu", -13, -9), ("gelu", -9, -4), ("gelu", -5.5, 0), ("gelu", -4, 4), ("gelu", 0, 14)])
+@pytest.mark.parametrize("act,low,high", [("gelu", -13, -9), ("gelu", -9, -4), ("gelu", -5.5, 0), ("gelu", -4, 4), ("gelu", 0, 14),
+                                          ("silu", -100, -70), ("silu", -86.75, -86.25), ("silu", -20, 10), ("silu", 80, 100),
+                                          ("gelu-tanh", -10.5, -9), ("gelu-tanh", -9, -4), ("gelu-tanh", -4, 4), ("gelu-tanh", 4, 14)])
 @pytest.mark.parametrize("large", [False, True])
 def test_activations_keep_their_digits(cuda, act, low, high, large):
     """Rows of gates in a range, without up, with one of ordinary values and with large ones beside the lowest gates."""
@@ -64,13 +68,17 @@ def test_activations_keep_their_digits(cuda, act, low, high, large):
             check_close(cuda, gate, up, act, kind)
 
 
-def test_every_gate(cuda):
-    """Rows of one gate, and of one gate beside zeros: all bf16 values of a size from 2^-30 to 2^7 whose activation fp32 holds."""
+@pytest.mark.parametrize("act,gates", [("gelu", 20), ("silu", 128), ("gelu-tanh", 20)])
+def test_every_gate(cuda, act, gates):
+    """Rows of one gate, and of one gate beside zeros: all bf16 values of a size from 2^-30 to `gates` whose activation is
+    a normal fp32 value, alone and with a factor that takes the smallest ones where 8 bits and bf16 hold them."""
     bits = cuda.arange((127 - 30) << 7, (127 + 7) << 7, device="cuda", dtype=cuda.int32)
     a = cuda.cat([bits, bits + 0x8000]).to(cuda.int16).view(cuda.bfloat16)
-    for act in ("gelu",):
-        kept = a[value(cuda, act, a.double()).abs() > 2.0 ** -100]
-        rows = kept[:, None].repeat(1, 32).contiguous()
+    a = a[a.abs() <= gates]
+    size = value(cuda, act, a.double()).abs()
+    for least, factor in ((2.0 ** -100, None), (2.0 ** -100, 2.0 ** -20), (2.0 ** -125, 2.0 ** 40), (2.0 ** -125, 2.0 ** 100)):
+        rows = a[size > least][:, None].repeat(1, 32).contiguous()
         rows[1::2, 1:] = 0
-        check_close(cuda, rows, None, act)
-        check_close(cuda, rows, cuda.full_like(rows, 2.0 ** -20), act, lora.LORA_Q8_X_FULL)
+        up = None if factor is None else cuda.full_like(rows, factor)
+        check_close(cuda, rows, up, act)
+        check_close(cuda, rows, up, act, lora.LORA_Q8_X_FULL)
