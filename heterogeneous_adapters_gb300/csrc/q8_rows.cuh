@@ -44,7 +44,7 @@ struct Q8GateParams {
 
 // Between these magnitudes of a row's largest value the quotients below are right; a row outside
 // is multiplied by a power of two first.
-constexpr float kQ8Small = 0x1p-64f, kQ8Large = 0x1p100f, kQ8Up = 0x1p64f, kQ8Down = 0x1p-80f;
+constexpr float kQ8Small = 0x1p-96f, kQ8Large = 0x1p100f, kQ8Up = 0x1p64f, kQ8Down = 0x1p-80f;
 
 // A word of two bf16 as a pair of fp32.
 __device__ __forceinline__ uint64_t pair_of(uint32_t w) { return pack2f(bf16lo(w), bf16hi(w)); }
@@ -132,10 +132,10 @@ template <int V>
 __device__ __forceinline__ Q8Row q8_row(uint64_t (&p)[V][4], float top, float over, float back, bool finite) {
     Q8Row r;
     r.top = top;
-    r.inv = top != 0.f ? 127.f * rcp_approx(top) : 0.f;
     r.scale = top * over * (1.f / 127.f) * back;
+    r.inv = r.scale != 0.f ? 127.f * rcp_approx(top) : 0.f;
     r.over = over * back;
-    if (!finite) {
+    if (!finite || !(r.scale < __uint_as_float(0x7F800000u))) {
         r.top = 1.f;
         r.inv = 0.f;
         r.scale = r.over = __uint_as_float(0x7FC00000u);
@@ -214,12 +214,15 @@ __global__ void __launch_bounds__(1024) q8_norm_kernel(const __grid_constant__ Q
         ss += odd;
         q8_reduce(top, ss, red_top[turn], red_ss[turn]);
         float over = rsqrtf(fmaf(ss, q.by_d, q.eps)), back = 1.f;
-        const bool large = !(ss < 0x1p125f);
-        if (large || top > kQ8Large || (top != 0.f && top < kQ8Small)) {
-            // squares or products near an end of fp32's range: once more by powers of two
-            const float by_h = large ? kQ8Down : top < 1.f ? 0x1p32f : 1.f;
-            const float by_w = large ? 1.f : top < 1.f ? 0x1p32f : kQ8Down;
-            back = large ? 1.f : top < 1.f ? 1.f / kQ8Up : 1.f / kQ8Down;
+        bool large = !(ss < 0x1p125f);
+        const bool huge = top > kQ8Large, tiny = top != 0.f && top < kQ8Small && !large;
+        if (large || huge || tiny) {
+            // squares or products near an end of fp32's range: once more by powers of two, the products' by one for the
+            // larger factor and one for the smaller.  Squares that are not large say that h is below 2^63; large ones, that
+            // eps is nothing and tiny products are too
+            const float by_s = large ? kQ8Down : 1.f, larger = !huge ? 1.f : large ? kQ8Down : 0x1p-96f,
+                        smaller = tiny ? kQ8Up : large && huge ? kQ8Down : 1.f;
+            back = tiny ? 1.f / kQ8Up : !large ? 0x1p96f : huge ? 1.f / kQ8Down : kQ8Down;
             ss = bad;
             top = 0.f;
             // from h where that is held: x or the residual may have given it their place
@@ -239,18 +242,27 @@ __global__ void __launch_bounds__(1024) q8_norm_kernel(const __grid_constant__ Q
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint64_t h = mul2(pair_of(w[i]), pack2f(by_h, by_h));
-                    p[j][i] = mul2(h, mul2(pair_of(g[i]), pack2f(by_w, by_w)));
-                    float lo, hi;
-                    unpack2f(h, lo, hi);
-                    ss = fmaf(hi, hi, fmaf(lo, lo, ss));
+                    float h[2], m[2];
+                    unpack2f(pair_of(w[i]), h[0], h[1]);
+                    unpack2f(pair_of(g[i]), m[0], m[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        ss = fmaf(h[k] * by_s, h[k] * by_s, ss);
+                        const bool low = fabsf(h[k]) <= fabsf(m[k]);
+                        h[k] *= low ? smaller : larger;
+                        m[k] *= low ? larger : smaller;
+                    }
+                    p[j][i] = pack2f(h[0] * m[0], h[1] * m[1]);
                     top = max_pair(p[j][i], top);
                 }
             }
             q8_reduce(top, ss, red_top[2], red_ss[2]);
-            if (large) over = rsqrtf(ss * q.by_d);          // of values so large that eps is nothing
+            if (large) {
+                over = rsqrtf(ss * q.by_d);
+                large = !(ss < 0x1p125f);
+            }
         }
-        const Q8Row r = q8_row(p, top, over, back, ss < 0x1p125f && top <= kQ8Large);
+        const Q8Row r = q8_row(p, top, over, back, !large && top <= kQ8Large);
         if (tid == 0) q.out.scales[row] = r.scale;
 #pragma unroll
         for (int j = 0; j < V; ++j) {

@@ -48,7 +48,8 @@ typedef struct {
 /* The norm: with h = bf16(x + residual) (x itself without a residual),
  *     y = h weight / sqrt(mean h^2 + eps),
  * left in 8 bits.  The sum of squares is fp32.  The codes are those of the exact quotients
- * (they depend on h weight alone); scales are within a few 2^-24 of theirs. */
+ * (they depend on h weight alone, which is fp32: 0 below 2^-150); scales are within a few 2^-24 of theirs.
+ * In the full x a value below 2^-64 of its row's largest may be 0. */
 typedef struct {
     const void* x;               /* bf16 [T][ldx]                                           */
     const void* residual;        /* bf16 [T][ldr], or NULL                                  */
