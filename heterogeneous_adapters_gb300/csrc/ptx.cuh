@@ -108,7 +108,8 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int3
 }
 
 // For launches with programmatic serialisation.  grid_wait: until the kernel before in the stream is complete
-// and its writes are seen; nothing reads or writes global memory earlier.  grid_let_next: the next kernel may begin
+// and its writes are seen; nothing reads or writes global memory earlier (w8_wide.cuh has one exception, and
+// says why it holds).  grid_let_next: the next kernel may begin
 // when all CTAs have come here, else when this kernel ends.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

@@ -90,10 +90,12 @@ constexpr int kWidenThreads = 256, kWidenAhead = 2;
 // Sixteen codes a thread and time, two times in flight; blockIdx.y: the matrix.  At most one CTA of
 // these for each that an SM holds: the next kernel begins when all have begun.
 __global__ void __launch_bounds__(kWidenThreads, 8) w8_widen_kernel(const __grid_constant__ W8Widen p) {
-    grid_wait();                               // W may be of the kernel before, and the next one does not wait to read it
+    // The order matters: the next kernel fetches W without a wait of its own, and W may be what the kernel before this
+    // one wrote.  It begins when all CTAs of this one have seen that kernel's end.
+    grid_wait();
     grid_let_next();
     const int i = blockIdx.y;
-    const uint32_t per_row = p.K[i] / 16, n = p.T * per_row, step = gridDim.x * kWidenThreads;   // n < 2^28
+    const uint32_t per_row = p.K[i] / 16, n = p.T * per_row, step = gridDim.x * kWidenThreads;   // n <= 2^28
     for (uint32_t e = blockIdx.x * kWidenThreads + threadIdx.x; e < n; e += kWidenAhead * step) {
         uint4 v[kWidenAhead];
 #pragma unroll
@@ -312,6 +314,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
 
     if (warp == 0) {
         // ------------------------------------------------------------------ W, one thread
+        // No grid_wait: the widening, which this kernel's start overlaps, reads x and writes its copy, and let this kernel
+        // begin only after the end of the kernel before it.  Everything else in global memory is touched after a grid_wait.
         regs_dec<kRegsMisc>();
         if (lane == 0) {
             W8At a = w8_at(p, start);
@@ -430,6 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     } else if (warp >= 12) {
         // ------------------------------------------------------------------ sums out: a row of W, half of the columns
         regs_inc<kRegsOut>();
+        grid_wait();                                           // the scales may be of the kernel before the widening
         const int quad = warp & 3, half = (warp - 12) >> 2, r = quad * 32 + lane, g = tid - (12 + 4 * half) * 32;
         constexpr int kChunks = NMAX / 32;
         const uint32_t dcol0 = tmem + ((uint32_t)(quad * 32) << 16) + half * half_cols;
