@@ -343,6 +343,7 @@ lora_status run_wide(const lora_w8_problem* probs, int32_t nprob, int32_t T, voi
         total += (int64_t)((pr.N + kW8WideRows - 1) / kW8WideRows) * sh.ttiles * w.prob[i].kblocks;
         if (total > (1 << 30)) return LORA_ETOOBIG;
     }
+    if (lost >= total) return LORA_EINVAL;
     w.total = (int32_t)total;
     pairs = std::min(pairs, (w.total + sh.per - 1) / sh.per);
     w.per = sh.per;

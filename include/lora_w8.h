@@ -112,7 +112,7 @@ lora_status lora_w8_matmul(const lora_w8_problem* probs, int32_t nprob, int32_t 
 /* Self-test of the bounded waits: lora_w8_matmul in which W of `step` (256 rows of a W by 128 of K,
  * counted K fastest, then the tiles along x, then those along W) never comes and every wait gives up
  * after limit_ns nanoseconds (1 ms .. 2 s, else LORA_EINVAL / LORA_ETOOBIG).  LORA_EINVAL for calls
- * whose kernel does not wait (up to 8 rows, and more where rows times W are few).
+ * whose kernel does not wait (up to 8 rows, and more where rows times W are few) and for a step past the call's last.
  * LORA_DERR_TIMEOUT is set, y is incomplete, and the workspace serves later calls as before. */
 lora_status lora_debug_w8_lost_step(const lora_w8_problem* probs, int32_t nprob, int32_t T, int32_t step, uint64_t limit_ns,
                                     void* ws, size_t ws_bytes, void* stream);
