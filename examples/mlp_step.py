@@ -45,6 +45,7 @@ class Mlp:
                               self.scales, adapters, 1, 3, rank, proj_dims=self.dims)
         # buffers and descriptions a server keeps
         bf = lambda d: torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+        self.adapter = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
         self.x, self.residual, self.xn, self.xa, self.out = bf(h), bf(h), bf(h), bf(f), bf(h)
         self.both = bf(2 * f)                                       # gate and up, side by side
         self.q, self.qs = torch.empty(rows, h, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
@@ -90,21 +91,23 @@ class Mlp:
         T = x.shape[0]
         self.x[:T].copy_(x)
         self.residual[:T].copy_(residual)
-        if self.graph is not None and T == self.graph[1]:
+        if self.graph is not None and T == self.graph[1] and len(adapters) == 1:
+            self.adapter[:T].copy_(adapters[0])
             self.graph[0].replay()
         else:
             self.calls(T, *adapters)
         return self.out[:T]
 
-    def capture(self, T, *adapters):
-        """Later steps of T rows replay one CUDA graph of the calls; the adapters' tensors stay where they are."""
+    def capture(self, T, adapter):
+        """Later steps of T requests replay one CUDA graph of the calls, each with the adapters it is given."""
+        self.adapter[:T].copy_(adapter)
         side, held = torch.cuda.Stream(), self.residual.clone()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            self.calls(T, *adapters)                                # loads the kernels
+            self.calls(T, self.adapter[:T])                         # loads the kernels
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph, stream=side):
-                self.calls(T, *adapters)
+                self.calls(T, self.adapter[:T])
             self.residual.copy_(held)
         torch.cuda.current_stream().wait_stream(side)
         self.graph = graph, T
