@@ -43,8 +43,8 @@ Q8Out out_of(const lora_q8_rows& o) {
 }
 
 // A launch that is made ready while the kernel before it in the stream still runs; the kernel waits for that one's end by
-// grid_wait().  In a graph, us: one row of 4096 x 4096 4.2 -> 3.9, 8,191 rows of the norm 49.5 -> 49.0; called one behind
-// the other 13 rows of q, k, v 10.4 -> 7.4, 2,339 gated rows 41.4 -> 38.9, 64 rows of 117 MB 29.5 -> 27.5.  Where the few-row
+// grid_wait().  In a graph, us: one row of 4096 x 4096 (in L2) 4.2 -> 3.9, 8,191 rows of the norm 49.5 -> 49.0; called one behind
+// the other 13 rows of q, k, v (in L2) 10.4 -> 7.4, 2,339 gated rows 41.4 -> 38.9, 64 rows of 117 MB 29.5 -> 27.5.  Where the few-row
 // kernel lets the next one begin while it runs, that one's CTAs take uneven places: 3.9 -> 5.0, 7.1 -> 7.9.
 template <typename P>
 lora_status launch_early(void (*kern)(P), dim3 grid, int threads, size_t smem, cudaStream_t s, const P& p) {
@@ -74,8 +74,8 @@ lora_status launch_rows(K kern, const P& q, int v, cudaStream_t s) {
 
 // Eights of a row that a thread holds, by measured times: a norm's weights fit beside one of them and
 // the next row (8,191 rows of 4096: 49 us, 59 with two), above that several CTAs an SM with four each
-// and nothing ahead are better (8,000 of 5120: 70 with one, 76 with two, 65; 2,000 of 14336: 67 with
-// two, 50).  An activation has no weights: two and the next row (2,339 gated of 14336 39, 50 with
+// and nothing ahead are better (8,000 of 5120: 70 with one, 76 with two, 64, 86% of a copy's rate; 2,000 of 14336:
+// 67 with two, 50 to 54, 72 to 78%).  An activation has no weights: two and the next row (2,339 gated of 14336 39, 50 with
 // four; 8,000 of 4096 without a gate 29, 36 with one), for narrow rows one.
 template <int ACT>
 lora_status launch_gate(const Q8GateParams& q, cudaStream_t s) {
@@ -101,12 +101,14 @@ lora_status check_sizes(const lora_w8_problem* probs, int32_t nprob, int32_t T) 
 }
 
 // Which kernel serves.  w8_narrow.cuh begins 5 us earlier than w8_wide.cuh, but takes W through the SMs once
-// per 32 rows of x and widens x once per 16 rows of W.  Narrow and wide, us: 8 rows of 117 MB 24 and 27;
-// 16 rows of 25 MB 7.9 and 14.1, 59 MB 16.8 and 21.7, 63 MB 19.3 and 17.6, 117 MB 31 and 27.  From 17 rows on
-// an SM holds one narrow CTA, whose time goes by K; the wide kernel joins its sums where K is long: 32 rows
-// of 17 MB 8.4 and 12.7, 25 MB 12.1 and 14.3, 29 MB in rows of 14336 13.2 and 17.6, 17 MB in rows of 1024 14.4
-// and 7.7; 128 rows of 1024 x 4096 8.3 and 12.2, of 2048 x 4096 15.8 and 13.4; 400 rows of 1 MB 8.4 and 12.3.
-// A call that is narrow is so for fewer rows too: a workspace serves those.
+// per 32 rows of x and widens x once per 16 rows of W.  Narrow and wide, us, W from memory: 16 rows of 17 MB
+// 6.8 and 14.4, 25 MB 10.5 and 16.1, 50 MB 16.1 and 16.5, 59 MB in rows of 14336 16.7 and 21.5, 79 MB 22.8 and 19.9,
+// 117 MB 31 and 27.  From 17 rows on an SM holds one narrow CTA, whose time goes by K; the wide kernel joins its
+// sums where K is long: 32 rows of 4 MB 5.9 and 13.0, 17 MB 10.9 and 14.2, 25 MB 15.6 and 16.2, 50 MB 28.7 and
+// 16.6, 59 MB in rows of 14336 26.4 and 21.7, 17 MB in rows of 1024 19.2 and 9.7; 64 rows of 8 MB 9.9 and 14.4,
+// 17 MB 18.2 and 16.0; 128 rows of 4 MB 10.0 and 14.4, 8 MB 17.2 and 15.5; 300 rows of 4 MB 21.0 and 15.7.  The
+// estimate, fitted with W in L2, takes the faster one at each of these.  152 SMs: a workspace's size is asked for
+// without a device.  A call that is narrow is so for fewer rows too: a workspace serves those.
 constexpr int64_t kW8Narrow16 = 58 << 20;
 bool narrow(const lora_w8_problem* probs, int32_t nprob, int32_t T) {
     if (T <= 8) return true;

@@ -5,8 +5,9 @@
 // only read and its only write, with one exchange between the warps.  A CTA takes row after row,
 // with the next row's loads on their way while it works on one.
 //
-// Memory bounds it: 8,191 rows of 4096 with the addition take 49.0 us (6.2 TB/s, 92% of a copy), 2,339
-// gated rows of 14336 38.5 (6.1 TB/s), at 72 and 63% of the issue slots.  One row takes 2.2: the launch
+// Memory bounds it: 8,191 rows of 4096 with the addition take 49.2 us (6.1 TB/s, 92% of a copy), 2,339
+// gated rows of 14336 38.9 (6.0 TB/s), at 72 and 63% of the issue slots; wider norms, which have no registers for
+// the next row, 72 to 86% of a copy.  One row takes 2.3: the launch
 // and a chain of a load, two exchanges between warps and a store.
 #pragma once
 #include "lora_w8.h"

@@ -8,10 +8,13 @@
 //
 // A CTA takes 16 rows of W over all of K, its eight warps 128 of K each in turn; their sums meet in
 // shared memory, and nothing waits for another CTA.  W and x come in pieces of 32 bytes a lane, a
-// request a sector: by 16 bytes 1 row of 4096 x 4096 takes 4.0 us and 13 rows of q, k, v (25 MB)
-// 8.0, by 32 bytes 3.9 (4.3 TB/s) and 7.1 to 7.5 (3.4 TB/s).  8 rows of 117 MB take 23.7 (5.0 TB/s): up to 8 rows
-// memory bounds it, and for the smallest the launch and the first data; beyond, the widening of x
-// for each 16 rows of W counts (16 rows of 117 MB 31).
+// request a sector (W in L2: by 16 bytes 1 row of 4096 x 4096 takes 4.0 us and 13 rows of q, k, v 8.0, by 32
+// bytes 3.9 and 7.1 to 7.5).  W from memory, as a layer finds it: 1 row of 4096 x 4096 6.1 to 6.3 us (2.7 TB/s), of
+// q, k, v (25 MB) 7.5 (3.3), of 117 MB 23.5 (5.0); the launch and the first data bound the small ones, memory
+// the large.  Up to 8 rows take as long as 1; beyond, the widening of x for each 16 rows of W counts (13 rows of
+// q, k, v 10.5, 16 rows of 117 MB 31).
+//
+// The one-row kernel with loads of 32 bytes spills one register (4 bytes); none of the others does.
 #pragma once
 #include "lora_w8.h"
 #include "mma_legacy.cuh"

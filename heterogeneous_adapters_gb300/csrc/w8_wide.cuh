@@ -18,9 +18,10 @@
 // partial sums in the workspace by the one that arrives last, in the order of K.
 //
 // 64 rows of 117 MB take 27 us (4.4 TB/s): TMA boxes of 128 bytes of 128 rows stream at 5.3 TB/s alone,
-// and the start takes 4.9 us to the first W.  2,011 rows of two 14336 x 4096 take 236 us (2.0 PFLOP/s,
-// the tensor pipe busy 92% of the time), 700 rows of 4096 x 14336 55.7 (1.48 PFLOP/s: 64 tiles for 76
-// pairs, and 5 us of x's widening before them).
+// and the start takes 4.9 us to the first W.  2,011 rows of two 14336 x 4096 take 232 us, 253 where the power
+// limit holds the clock down (2.0 and 1.9 PFLOP/s, the tensor pipe busy 92% of the time), 700 rows of 4096 x 14336
+// 55.8 (1.47 PFLOP/s: 64 tiles for 76 pairs, and 5 us of x's widening before them).  Small W is far from memory's
+// rate: 64 rows of 17 MB take 15 to 16 us, of 25 MB 16 to 18, of 59 MB 22.5, the start and the join of few tiles.
 #pragma once
 #include <cuda.h>
 
@@ -249,7 +250,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kW8WideThreads, 1) w
     constexpr int kWStages = w8_w_stages(NMAX), kXStage = NMAX * 128;
     // Registers move from the warps that issue and widen to those that hold a row's sums: the shares of
     // the five groups of four warps add up to the 480 of the launch.  (A few spilled registers in the
-    // path of whole tiles cost as much as the path itself.)
+    // path of whole tiles cost as much as the path itself: those kernels spill none.  Of those for shares the one of
+    // up to 128 columns spills seven, 28 bytes.)
     constexpr int kDs = NMAX > 128 ? 1 : 2;    // D buffers, 128 columns apart
     constexpr int kRegsOut = NMAX > 128 ? 160 : 136, kRegsWiden = NMAX > 128 ? 56 : 80, kRegsMisc = 48;
     static_assert(kRegsMisc + 2 * kRegsWiden + 2 * kRegsOut <= 480, "registers of the launch");

@@ -92,7 +92,7 @@ typedef struct {
     const float* w_scales;       /* [N], 4-byte aligned                                     */
     int64_t ldx;
     int64_t ldy;
-    int32_t N;                   /* a multiple of 8                                         */
+    int32_t N;                   /* a multiple of 8, at most 2^24                           */
     int32_t K;                   /* a multiple of 16, at most LORA_W8_MAX_K                 */
 } lora_w8_problem;
 
@@ -104,8 +104,10 @@ typedef struct {
 lora_status lora_w8_workspace_size(const lora_w8_problem* probs, int32_t nprob, int32_t T, size_t* bytes);
 
 /* All projections of the call, at most LORA_W8_MAX_PROBLEMS, over the same T <=
- * LORA_W8_MAX_ROWS rows (their x may differ).  Sums that stay below 2^24 on the way are whole numbers, and
- * y is theirs times the scales in fp32, rounded once, the same for any T; larger sums are fp32 sums. */
+ * LORA_W8_MAX_ROWS rows (their x may differ); at most 2^30 steps, as counted below (LORA_ETOOBIG).
+ * What is written overlaps nothing else of the call.  Sums that stay below 2^24 on the way are
+ * whole numbers, and y is theirs times the scales in fp32, rounded once, the same for any T;
+ * larger sums are fp32 sums (whole numbers up to 8 rows, rounded to fp32 once). */
 lora_status lora_w8_matmul(const lora_w8_problem* probs, int32_t nprob, int32_t T, void* ws, size_t ws_bytes,
                            void* stream);
 
